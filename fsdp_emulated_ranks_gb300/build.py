@@ -1,5 +1,5 @@
-"""Build ``libcr.so`` (the CUDA kernels and the C ABI of include/cr.h) for
-sm_103a with nvcc, in-tree under ``fsdp_emulated_ranks_gb300/_build``.
+"""Build ``libcr.so`` (the CUDA kernels and the C ABI of include/cr.h and
+include/cr_ffn.h) for sm_103a with nvcc, in-tree under ``fsdp_emulated_ranks_gb300/_build``.
 
 Translation units compile in parallel; the link step produces one shared
 library with the CUDA runtime linked statically, so loading it needs no
@@ -30,7 +30,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]
 SOURCES = ["api.cu", "api_buckets.cu", "api_optim.cu", "api_range.cu", "launch_util.cu", "k_collectives.cu", "k_fsdp.cu",
            "k_bucket.cu", "k_bucket_fused.cu", "k_fsdp2.cu", "k_accum.cu",
-           "k_hsdp.cu", "reducer.cu", "fsdp_noalloc.cu", "check.cu", "plan.cpp",
+           "k_hsdp.cu", "api_ffn.cu", "k_norm.cu", "k_q8.cu", "k_glu.cu", "reducer.cu", "fsdp_noalloc.cu", "check.cu", "plan.cpp",
            "comm.cpp"]
 
 
@@ -43,7 +43,7 @@ def nvcc() -> str:
 
 def _inputs() -> list[str]:
     files = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))]
-    files.append(os.path.join(INCLUDE, "cr.h"))
+    files += [os.path.join(INCLUDE, f) for f in sorted(os.listdir(INCLUDE))]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -1,4 +1,5 @@
-"""ctypes binding of libcr (include/cr.h): argument marshalling only.
+"""ctypes binding of libcr (include/cr.h and include/cr_ffn.h): argument
+marshalling only.
 
 Every function here has the name of the C entry point it calls and does
 nothing but turn Python arguments (torch tensors or integer device
@@ -51,6 +52,16 @@ EXPORTS = ["cr_status_string", "cr_last_error", "cr_version", "cr_chunk_len",
            "cr_comm_all_gather", "cr_comm_broken", "cr_comm_destroy",
            "cr_check_word", "cr_check_selftest"]
 
+# Every symbol include/cr_ffn.h declares.
+FFN_EXPORTS = ["cr_q8_store", "cr_q8_load", "cr_rms_norm",
+               "cr_rms_norm_backward_workspace_bytes", "cr_rms_norm_backward",
+               "cr_glu_workspace_bytes", "cr_glu", "cr_glu_act_backward",
+               "cr_glu_backward_workspace_bytes", "cr_glu_backward"]
+
+ACT_SILU, ACT_GELU = 0, 1
+_ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
+Q8_GROUP = 128  # columns per scale of an 8-bit matrix
+
 _lib = None
 
 
@@ -77,6 +88,19 @@ class BucketPlanT(C.Structure):
                 ("tensor_bucket", C.POINTER(C.c_int)),
                 ("tensor_offset", C.POINTER(C.c_size_t)),
                 ("bucket_numel", C.POINTER(C.c_size_t))]
+
+
+class Q8(C.Structure):
+    """An 8-bit matrix (cr_q8): `codes`, rows x cols bytes, and `scales`, one
+    float per row and 128 columns.  Tensors (uint8 or float8_e4m3fn, and
+    float32) give their own row strides; device pointers need ld and lds.
+    Holds references to both."""
+    _fields_ = [("codes", C.c_void_p), ("ld", C.c_size_t),
+                ("scales", C.c_void_p), ("lds", C.c_size_t)]
+
+    def __init__(self, codes, scales, ld=None, lds=None):
+        super().__init__(_ptr(codes), _ld(codes, ld), _ptr(scales), _ld(scales, lds))
+        self._keep = (codes, scales)
 
 
 _tls = threading.local()  # .recorder: set while prepare() runs a wrapper
@@ -164,7 +188,20 @@ def lib() -> C.CDLL:
     L.cr_adamw_step.argtypes = [sz, vp, vp, vp, vp, C.POINTER(AdamWCfg), vp, vp]
     L.cr_comm_elems.argtypes = [i, i, i, sz, i, C.POINTER(C.c_uint64),
                                 C.POINTER(C.c_uint64), C.POINTER(i)]
-    for name in EXPORTS:
+    q8 = C.POINTER(Q8)
+    L.cr_q8_store.argtypes = [vp, sz, sz, sz, i, q8, vp]
+    L.cr_q8_load.argtypes = [q8, sz, sz, vp, sz, i, vp]
+    L.cr_rms_norm.argtypes = [vp, sz, vp, sz, vp, sz, sz, i, C.c_double, vp, sz, vp, sz, q8, vp, vp]
+    L.cr_rms_norm_backward.argtypes = [vp, sz, vp, sz, q8, vp, vp, vp, sz, sz, sz, i, vp, sz, vp, i,
+                                       vp, sz, vp]
+    L.cr_glu.argtypes = [vp, sz, vp, sz, vp, sz, sz, sz, sz, i, i, vp, sz, q8, q8, vp, sz, vp]
+    L.cr_glu_act_backward.argtypes = [vp, sz, q8, q8, sz, sz, i, i, vp, sz, vp, sz, vp, sz, vp]
+    L.cr_glu_backward.argtypes = [vp, sz, q8, q8, vp, sz, q8, vp, sz, vp, sz, sz, sz, sz, i, i,
+                                  vp, sz, vp, vp, i, vp, sz, vp, sz, vp]
+    for name, n in (("cr_rms_norm_backward", 2), ("cr_glu", 3), ("cr_glu_backward", 3)):
+        fn = getattr(L, name + "_workspace_bytes")
+        fn.restype, fn.argtypes = sz, [sz] * n
+    for name in EXPORTS + FFN_EXPORTS:
         getattr(L, name).restype = getattr(L, name).restype or i
     L.cr_status_string.restype = C.c_char_p
     L.cr_last_error.restype = C.c_char_p
@@ -185,6 +222,19 @@ def _ptr(x) -> int:
     if isinstance(x, int):
         return x
     return x.data_ptr()
+
+
+def _ld(x, ld=None) -> int:
+    """Row stride in elements: the one given, else the 2-D tensor's own (0
+    for an absent matrix, and for a pointer or a vector)."""
+    if ld is not None:
+        return ld
+    if x is None or type(x) is int or x.dim() < 2:
+        return 0
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError("the columns of a matrix must be contiguous")
+    return x.stride(0) if rows > 1 else cols
 
 
 _PACK = {}  # length -> struct packer of that many native 64-bit pointers
@@ -650,6 +700,87 @@ def cr_comm_elems(coll: int, sched: int, nranks: int, count: int,
     return sent.value, recv.value, steps.value
 
 
+# ---- feed-forward operators (include/cr_ffn.h) -----------------------------------------
+#
+# Matrices are 2-D tensors, whose row strides are taken from the tensors, or
+# device pointers, whose row strides are given (ldx, ...); None where optional.
+
+def _act(a) -> int:
+    return a if isinstance(a, int) else _ACTS[a]
+
+
+def _q8(q):
+    return None if q is None else C.byref(q)
+
+
+def cr_q8_store(x, rows, cols, dtype, q: Q8, stream=None, ldx=None) -> None:
+    _check(lib().cr_q8_store(_ptr(x), _ld(x, ldx), rows, cols, _dtype(dtype), _q8(q),
+                             _stream(stream)), "cr_q8_store")
+
+
+def cr_q8_load(q: Q8, rows, cols, x, dtype, stream=None, ldx=None) -> None:
+    _check(lib().cr_q8_load(_q8(q), rows, cols, _ptr(x), _ld(x, ldx), _dtype(dtype),
+                            _stream(stream)), "cr_q8_load")
+
+
+def cr_rms_norm(x, residual, weight, rows, cols, dtype, eps, sum, y, y8: Q8 = None, rstd=None,
+                stream=None, ldx=None, ldr=None, ldsum=None, ldy=None) -> None:
+    _check(lib().cr_rms_norm(_ptr(x), _ld(x, ldx), _ptr(residual), _ld(residual, ldr),
+                             _ptr(weight), rows, cols, _dtype(dtype), eps, _ptr(sum),
+                             _ld(sum, ldsum), _ptr(y), _ld(y, ldy), _q8(y8), _ptr(rstd),
+                             _stream(stream)), "cr_rms_norm")
+
+
+def cr_rms_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return lib().cr_rms_norm_backward_workspace_bytes(rows, cols)
+
+
+def cr_rms_norm_backward(dy, h, h8: Q8, weight, rstd, dres, rows, cols, dtype, dx, dweight,
+                         dw_dtype="bf16", workspace=None, workspace_bytes=0, stream=None,
+                         lddy=None, ldh=None, lddres=None, lddx=None) -> None:
+    _check(lib().cr_rms_norm_backward(_ptr(dy), _ld(dy, lddy), _ptr(h), _ld(h, ldh), _q8(h8),
+                                      _ptr(weight), _ptr(rstd), _ptr(dres), _ld(dres, lddres),
+                                      rows, cols, _dtype(dtype), _ptr(dx), _ld(dx, lddx),
+                                      _ptr(dweight), _dtype(dw_dtype), _ptr(workspace),
+                                      workspace_bytes, _stream(stream)), "cr_rms_norm_backward")
+
+
+def cr_glu_workspace_bytes(tokens: int, dim: int, ffn: int) -> int:
+    return lib().cr_glu_workspace_bytes(tokens, dim, ffn)
+
+
+def cr_glu(x, wg, wu, tokens, dim, ffn, dtype, act, a, g8: Q8 = None, u8: Q8 = None,
+           workspace=None, workspace_bytes=0, stream=None, ldx=None, ldwg=None, ldwu=None,
+           lda=None) -> None:
+    _check(lib().cr_glu(_ptr(x), _ld(x, ldx), _ptr(wg), _ld(wg, ldwg), _ptr(wu), _ld(wu, ldwu),
+                        tokens, dim, ffn, _dtype(dtype), _act(act), _ptr(a), _ld(a, lda),
+                        _q8(g8), _q8(u8), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "cr_glu")
+
+
+def cr_glu_act_backward(da, g8: Q8, u8: Q8, tokens, ffn, dtype, act, dg, du, a=None, stream=None,
+                        ldda=None, lddg=None, lddu=None, lda=None) -> None:
+    _check(lib().cr_glu_act_backward(_ptr(da), _ld(da, ldda), _q8(g8), _q8(u8), tokens, ffn,
+                                     _dtype(dtype), _act(act), _ptr(dg), _ld(dg, lddg), _ptr(du),
+                                     _ld(du, lddu), _ptr(a), _ld(a, lda), _stream(stream)),
+           "cr_glu_act_backward")
+
+
+def cr_glu_backward_workspace_bytes(tokens: int, dim: int, ffn: int) -> int:
+    return lib().cr_glu_backward_workspace_bytes(tokens, dim, ffn)
+
+
+def cr_glu_backward(da, g8: Q8, u8: Q8, x, x8: Q8, wg, wu, tokens, dim, ffn, dtype, act, dx, dwg,
+                    dwu, dw_dtype="bf16", a=None, workspace=None, workspace_bytes=0, stream=None,
+                    ldda=None, ldx=None, ldwg=None, ldwu=None, lddx=None, lda=None) -> None:
+    _check(lib().cr_glu_backward(_ptr(da), _ld(da, ldda), _q8(g8), _q8(u8), _ptr(x), _ld(x, ldx),
+                                 _q8(x8), _ptr(wg), _ld(wg, ldwg), _ptr(wu), _ld(wu, ldwu),
+                                 tokens, dim, ffn, _dtype(dtype), _act(act), _ptr(dx),
+                                 _ld(dx, lddx), _ptr(dwg), _ptr(dwu), _dtype(dw_dtype), _ptr(a),
+                                 _ld(a, lda), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "cr_glu_backward")
+
+
 # ---- prepared calls -----------------------------------------------------------------
 
 # Entry points that launch work on a stream: the ones prepare() can record.
@@ -660,11 +791,15 @@ _PREPARABLE = frozenset([
     "cr_bucket_all_reduce_fused", "cr_fsdp_step", "cr_fsdp_step_clipped",
     "cr_fsdp_step_clipped_noalloc", "cr_fsdp2_step", "cr_fsdp2_plan_upload",
     "cr_fsdp2_step_planned", "cr_all_reduce_range", "cr_reduce_scatter_range",
-    "cr_fsdp_step_range", "cr_accumulate", "cr_all_reduce_accumulate", "cr_adamw_step"])
+    "cr_fsdp_step_range", "cr_accumulate", "cr_all_reduce_accumulate", "cr_adamw_step",
+    "cr_q8_store", "cr_q8_load", "cr_rms_norm", "cr_rms_norm_backward", "cr_glu",
+    "cr_glu_act_backward", "cr_glu_backward"])
 # Functions without side effects that a wrapper may call while it marshals.
 _PURE = frozenset(["cr_last_error", "cr_status_string", "cr_chunk_len", "cr_version",
                    "cr_fsdp_clip_workspace_bytes", "cr_shard_range", "cr_slab_range",
-                   "cr_comm_elems", "cr_fsdp2_plan_table_bytes"])
+                   "cr_comm_elems", "cr_fsdp2_plan_table_bytes",
+                   "cr_rms_norm_backward_workspace_bytes", "cr_glu_workspace_bytes",
+                   "cr_glu_backward_workspace_bytes"])
 
 
 class _Recorder:
