@@ -56,7 +56,7 @@ EXPORTS = ["cr_status_string", "cr_last_error", "cr_version", "cr_chunk_len",
 FFN_EXPORTS = ["cr_q8_store", "cr_q8_load", "cr_rms_norm",
                "cr_rms_norm_backward_workspace_bytes", "cr_rms_norm_backward",
                "cr_glu_workspace_bytes", "cr_glu", "cr_glu_act_backward",
-               "cr_glu_backward_workspace_bytes", "cr_glu_backward"]
+               "cr_glu_backward_workspace_bytes", "cr_glu_backward", "cr_glu_wait_word"]
 
 ACT_SILU, ACT_GELU = 0, 1
 _ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
@@ -198,6 +198,7 @@ def lib() -> C.CDLL:
     L.cr_glu_act_backward.argtypes = [vp, sz, q8, q8, sz, sz, i, i, vp, sz, vp, sz, vp, sz, vp]
     L.cr_glu_backward.argtypes = [vp, sz, q8, q8, vp, sz, q8, vp, sz, vp, sz, sz, sz, sz, i, i,
                                   vp, sz, vp, vp, i, vp, sz, vp, sz, vp]
+    L.cr_glu_wait_word.restype, L.cr_glu_wait_word.argtypes = C.c_longlong, [i]
     for name, n in (("cr_rms_norm_backward", 2), ("cr_glu", 3), ("cr_glu_backward", 3)):
         fn = getattr(L, name + "_workspace_bytes")
         fn.restype, fn.argtypes = sz, [sz] * n
@@ -779,6 +780,12 @@ def cr_glu_backward(da, g8: Q8, u8: Q8, x, x8: Q8, wg, wu, tokens, dim, ffn, dty
                                  _ld(dx, lddx), _ptr(dwg), _ptr(dwu), _dtype(dw_dtype), _ptr(a),
                                  _ld(a, lda), _ptr(workspace), workspace_bytes, _stream(stream)),
            "cr_glu_backward")
+
+
+def cr_glu_wait_word(clear: bool = False) -> int:
+    """Nonzero if a barrier wait of the block's kernels ever ran out (-2:
+    reading the word failed)."""
+    return lib().cr_glu_wait_word(1 if clear else 0)
 
 
 # ---- prepared calls -----------------------------------------------------------------

@@ -157,6 +157,17 @@ uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 // bf16 elements of a workspace matrix whose rows start on 16-byte boundaries.
 uint64_t padded(uint64_t rows, uint64_t cols) { return rows * round_up(cols, 8); }
 
+// TMA reads operands whose rows start on 16-byte boundaries; any other is
+// copied to `ws` first.
+cudaError_t operand(Mat* m, uint64_t rows, uint64_t cols, uint16_t* ws, cudaStream_t s) {
+  if (!m->p || rows == 0 || cols == 0) return cudaSuccess;
+  if (aligned(m->p, 16) && (rows == 1 || m->ld % 8 == 0)) return cudaSuccess;
+  const Mat copy = {ws, round_up(cols, 8)};
+  const cudaError_t e = launch_copy_bf16(*m, copy, rows, (uint32_t)cols, s);
+  *m = copy;
+  return e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -298,8 +309,10 @@ cr_status cr_glu_act_backward(const void* da, size_t ldda, const cr_q8* g8, cons
 }
 
 size_t cr_glu_workspace_bytes(size_t tokens, size_t dim, size_t ffn) {
-  (void)tokens, (void)dim, (void)ffn;
-  return 0;
+  if (tokens >= (1ull << 31) || dim >= (1ull << 31) || ffn >= (1ull << 31)) return 0;
+  if (tokens == 0 || ffn == 0) return 0;
+  // room for copies of operands that are not aligned
+  return 2 * (padded(tokens, dim) + 2 * padded(ffn, dim));
 }
 
 cr_status cr_glu(const void* x, size_t ldx, const void* wg, size_t ldwg, const void* wu,
@@ -322,13 +335,22 @@ cr_status cr_glu(const void* x, size_t ldx, const void* wg, size_t ldwg, const v
   if (tokens == 0 || ffn == 0) return ok();
   GluArgs k = {mat(x, ldx), mat(wg, ldwg), mat(wu, ldwu),   mat(a_out, lda), q8_of(g8),
                q8_of(u8),   (uint32_t)tokens, (uint32_t)dim, (uint32_t)ffn};
-  return launched(launch_glu(act, k, stream_of(stream)), "cr_glu");
+  const cudaStream_t s = stream_of(stream);
+  uint16_t* ws = static_cast<uint16_t*>(workspace);
+  cudaError_t e = operand(&k.x, tokens, dim, ws, s);
+  ws += padded(tokens, dim);
+  if (e == cudaSuccess) e = operand(&k.wg, ffn, dim, ws, s);
+  ws += padded(ffn, dim);
+  if (e == cudaSuccess) e = operand(&k.wu, ffn, dim, ws, s);
+  if (e == cudaSuccess) e = launch_glu(act, k, s);
+  return launched(e, "cr_glu");
 }
 
 size_t cr_glu_backward_workspace_bytes(size_t tokens, size_t dim, size_t ffn) {
   if (tokens >= (1ull << 31) || dim >= (1ull << 31) || ffn >= (1ull << 31)) return 0;
-  // dg and du, and x restored from its checkpoint
-  return 2 * (2 * padded(tokens, ffn) + padded(tokens, dim));
+  // dg and du; x restored from its checkpoint, in two parts; copies of
+  // weights that are not aligned
+  return 2 * (2 * padded(tokens, ffn) + 2 * padded(tokens, dim) + 2 * padded(ffn, dim));
 }
 
 cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr_q8* u8,
@@ -385,17 +407,35 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr
   GluBackArgs k = {};
   k.dg = dg, k.du = du;
   k.x = mat(x, ldx);
-  if (dw && x8 && tokens) {
-    k.x = Mat{ws + 2 * padded(tokens, ffn), round_up(dim, 8)};
-    e = launch_q8_load(CR_BF16, q8_of(x8), k.x, tokens, (uint32_t)dim, xa.vec(), s);
-    if (e != cudaSuccess) return cuda_fail(e, "cr_glu_backward: x8");
-  }
   k.wg = mat(wg, ldwg), k.wu = mat(wu, ldwu);
+  ws += 2 * padded(tokens, ffn);
+  if (dw && x8 && tokens) {
+    k.x = Mat{ws, round_up(dim, 8)};
+    k.x_lo = Mat{ws + padded(tokens, dim), round_up(dim, 8)};
+    e = launch_q8_split(q8_of(x8), k.x, k.x_lo, tokens, (uint32_t)dim, xa.vec(), s);
+  } else if (dw) {
+    e = operand(&k.x, tokens, dim, ws, s);
+  }
+  ws += 2 * padded(tokens, dim);
+  if (dx && e == cudaSuccess) e = operand(&k.wg, ffn, dim, ws, s);
+  ws += padded(ffn, dim);
+  if (dx && e == cudaSuccess) e = operand(&k.wu, ffn, dim, ws, s);
+  if (e != cudaSuccess) return cuda_fail(e, "cr_glu_backward: operands");
   k.dx = mat(tokens ? dx : nullptr, lddx);
   k.dwg = ffn ? dwg : nullptr;
   k.dwu = ffn ? dwu : nullptr;
   k.tokens = (uint32_t)tokens, k.dim = (uint32_t)dim, k.ffn = (uint32_t)ffn;
   return launched(launch_glu_back(dw_dtype, k, s), "cr_glu_backward");
+}
+
+long long cr_glu_wait_word(int clear) {
+  unsigned int word = 0;
+  const cudaError_t e = glu_wait_word(clear != 0, &word);
+  if (e != cudaSuccess) {
+    cuda_fail(e, "cr_glu_wait_word");
+    return -2;
+  }
+  return (long long)word;
 }
 
 }  // extern "C"

@@ -67,6 +67,7 @@ struct ActBackArgs {
   uint32_t cols;
 };
 
+// Operands of the products (x, wg, wu, dg, du): 16-byte aligned rows.
 struct GluArgs {
   Mat x, wg, wu, a;
   Q8 g8, u8;
@@ -74,7 +75,7 @@ struct GluArgs {
 };
 
 struct GluBackArgs {
-  Mat dg, du, x, wg, wu, dx;
+  Mat dg, du, x, x_lo, wg, wu, dx;  // x_lo: what x lacks to a checkpoint's value, or absent
   void *dwg, *dwu;  // [ffn][dim]
   uint32_t tokens, dim, ffn;
 };
@@ -89,9 +90,17 @@ cudaError_t launch_q8_store(cr_dtype d, const Mat& x, const Q8& q, uint64_t rows
                             bool vec, cudaStream_t s);
 cudaError_t launch_q8_load(cr_dtype d, const Q8& q, const Mat& x, uint64_t rows, uint32_t cols,
                            bool vec, cudaStream_t s);
+// The values q stands for as bf16 hi + lo (lo: what the rounding of hi left).
+cudaError_t launch_q8_split(const Q8& q, const Mat& hi, const Mat& lo, uint64_t rows, uint32_t cols,
+                            bool vec, cudaStream_t s);
+// dst = src, rows x cols bf16 at any alignment.
+cudaError_t launch_copy_bf16(const Mat& src, const Mat& dst, uint64_t rows, uint32_t cols,
+                             cudaStream_t s);
 cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, bool vec, cudaStream_t s);
 cudaError_t launch_glu(cr_act act, const GluArgs& a, cudaStream_t s);
 cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& a, cudaStream_t s);
+// Reads (and clears) the word a block sets that gave up a wait.
+cudaError_t glu_wait_word(bool clear, unsigned int* word);
 
 #if defined(__CUDACC__)
 

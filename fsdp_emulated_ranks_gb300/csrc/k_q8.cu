@@ -59,6 +59,45 @@ __global__ void __launch_bounds__(kBlock) k_q8_load(const __grid_constant__ Q8 q
   }
 }
 
+template <bool VEC>
+__global__ void __launch_bounds__(kBlock) k_q8_split(const __grid_constant__ Q8 q,
+                                                     const __grid_constant__ Mat hi,
+                                                     const __grid_constant__ Mat lo, uint32_t cols,
+                                                     const __grid_constant__ ChunkRange r) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const uint64_t stride = (uint64_t)gridDim.x * (kBlock / 32);
+  for (uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); k < r.chunks;
+       k += stride) {
+    const uint64_t row = fastdiv_div(r.per_row, k);
+    const uint32_t base = (uint32_t)(k - row * r.per_row.d) * kChunk;
+    float v[kLaneVals], rest[kLaneVals];
+    ld_chunk_q8<VEC>(q, row, base, cols, lane, v);
+#pragma unroll
+    for (int i = 0; i < kLaneVals; ++i)
+      rest[i] = v[i] - ffn_bf16((uint16_t)ffn_bf16x2(v[i], 0.0f));
+    st_chunk<CR_BF16, VEC>(static_cast<uint16_t*>(hi.p) + row * hi.ld, base, cols, lane, v);
+    st_chunk<CR_BF16, VEC>(static_cast<uint16_t*>(lo.p) + row * lo.ld, base, cols, lane, rest);
+  }
+}
+
+__global__ void __launch_bounds__(kBlock) k_copy_bf16(const __grid_constant__ Mat src,
+                                                      const __grid_constant__ Mat dst,
+                                                      uint32_t cols,
+                                                      const __grid_constant__ ChunkRange r) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const uint64_t stride = (uint64_t)gridDim.x * (kBlock / 32);
+  for (uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); k < r.chunks;
+       k += stride) {
+    const uint64_t row = fastdiv_div(r.per_row, k);
+    const uint32_t base = (uint32_t)(k - row * r.per_row.d) * kChunk;
+    float v[kLaneVals];
+    ld_chunk<CR_BF16, false>(static_cast<const uint16_t*>(src.p) + row * src.ld, base, cols, lane, v);
+    st_chunk<CR_BF16, false>(static_cast<uint16_t*>(dst.p) + row * dst.ld, base, cols, lane, v);
+  }
+}
+
 template <int ACT, bool VEC>
 __global__ void __launch_bounds__(kBlock) k_act_back(const __grid_constant__ ActBackArgs a,
                                                      const __grid_constant__ ChunkRange r) {
@@ -115,6 +154,19 @@ cudaError_t launch_q8_load(cr_dtype d, const Q8& q, const Mat& x, uint64_t rows,
                : launch_pdl(k_q8_load<CR_BF16, false>, grid, kBlock, s, q, x, cols, r);
   return vec ? launch_pdl(k_q8_load<CR_F32, true>, grid, kBlock, s, q, x, cols, r)
              : launch_pdl(k_q8_load<CR_F32, false>, grid, kBlock, s, q, x, cols, r);
+}
+
+cudaError_t launch_q8_split(const Q8& q, const Mat& hi, const Mat& lo, uint64_t rows, uint32_t cols,
+                            bool vec, cudaStream_t s) {
+  const ChunkRange r = chunk_range(rows, cols);
+  return vec ? launch_pdl(k_q8_split<true>, dim3(chunk_grid(r)), kBlock, s, q, hi, lo, cols, r)
+             : launch_pdl(k_q8_split<false>, dim3(chunk_grid(r)), kBlock, s, q, hi, lo, cols, r);
+}
+
+cudaError_t launch_copy_bf16(const Mat& src, const Mat& dst, uint64_t rows, uint32_t cols,
+                             cudaStream_t s) {
+  const ChunkRange r = chunk_range(rows, cols);
+  return launch_pdl(k_copy_bf16, dim3(chunk_grid(r)), kBlock, s, src, dst, cols, r);
 }
 
 cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, bool vec, cudaStream_t s) {

@@ -153,8 +153,8 @@ cr_status cr_glu_act_backward(const void* da, size_t ldda, const cr_q8* g8,
  *     dx = dg wg + du wu,  dwg = dg^T x,  dwu = du^T x,  a = act(g) * u
  * with dg and du as above, rounded to bf16 as operands of the products.
  *   x or x8    the block's input, tokens x dim, as bf16 or as its 8-bit
- *              checkpoint (whose values are rounded to bf16 as operands):
- *              exactly one
+ *              checkpoint (whose values enter the products as a sum of two
+ *              bf16 numbers, exact to 2^-16): exactly one
  *   dx         tokens x dim, bf16 (optional)
  *   dwg, dwu   ffn x dim, row stride dim, of dw_dtype CR_BF16 or CR_F32 (each
  *              optional)
@@ -171,6 +171,13 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8,
                           cr_dtype dw_dtype, void* a, size_t lda,
                           void* workspace, size_t workspace_bytes,
                           cr_stream_t stream);
+
+/* The block's products wait on barriers inside the kernel, each wait for about
+ * two seconds at most.  A wait that runs out (it never should) ends the
+ * kernel, leaves its results undefined and sets this word, which stays set
+ * until it is cleared.  Returns the word (0: no wait ever ran out), or -2 if
+ * reading it failed; waits for the device. */
+long long cr_glu_wait_word(int clear);
 
 #ifdef __cplusplus
 }

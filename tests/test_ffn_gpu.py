@@ -432,8 +432,8 @@ def check_glu_backward(tokens, dim, ffn, held, dw_dt, kind, left, right):
     untouched(wide_a, left, ffn)
     dg, du, av = R.glu_act_backward(da, gv, uv, kind)
     assert torch.all((a.double() - av).abs() <= R.U16 * av.abs() + 2.0 ** -18 * (gv * uv).abs())
-    # exact operands against rounded ones: U16 of every term, 2 U32 an addition
-    xb = R.bf16(xv)
+    # exact operands against rounded ones: U16 of every term (dg and du; x is exact, or
+    # within 2^-16 of its checkpoint's value), 2 U32 an addition
     edg = 2.0 ** -18 * da.double().abs() * uv.abs() * (1 + gv.abs())
     edu = 2.0 ** -18 * da.double().abs() * gv.abs()
 
@@ -450,8 +450,8 @@ def check_glu_backward(tokens, dim, ffn, held, dw_dt, kind, left, right):
             assert R.rel_norm(got, near) <= max(u_out, 2.0 ** -12), what
 
     check(dx, [(dg, wg.double(), edg), (du, wu.double(), edu)], 2 * ffn, R.U16, "dx")
-    check(dwg, [(dg.T, xb, edg.T)], tokens, R.U_OUT[dw_dt], "dwg")
-    check(dwu, [(du.T, xb, edu.T)], tokens, R.U_OUT[dw_dt], "dwu")
+    check(dwg, [(dg.T, xv, edg.T)], tokens, R.U_OUT[dw_dt], "dwg")
+    check(dwu, [(du.T, xv, edu.T)], tokens, R.U_OUT[dw_dt], "dwu")
 
 
 def test_glu_backward_outputs_alone():
