@@ -18,6 +18,11 @@
 // rows and columns outside a matrix with zeros, so ragged sizes need no masks
 // before the epilogue.  Every wait is bounded (tc.cuh); a block that gives up
 // sets g_wait_word and leaves.
+//
+// Where the tiles are too few for the SMs (k_split), the blocks of a cluster
+// share one tile: each takes a range of its K, leaves its partial sums in its
+// own shared memory, and then finishes a range of the tile's rows, reading
+// the partials of all in rank order.
 #include <algorithm>
 
 #include "ffn_internal.cuh"
@@ -51,6 +56,7 @@ struct TileArgs {
   uint32_t blocks;            // K blocks of a tile: one or two products
   uint32_t tiles_m, tiles_n;  // of an output
   uint32_t tiles;             // of all outputs
+  uint32_t splits;            // blocks that share a tile (k_split), a power of two
   int width;                  // bytes of the output stores all rows allow: 32, 16 or 0
   int width8;                 // the same for the codes
 };
@@ -61,7 +67,6 @@ __device__ __forceinline__ void st32(void* p, const uint32_t* w) {
                : "memory");
 }
 
-// n 32-byte words of a row, all inside it.
 template <int WORDS>
 __device__ __forceinline__ void st_words(void* p, const uint32_t* w, int width) {
   if (width == 32) {
@@ -75,42 +80,61 @@ __device__ __forceinline__ void st_words(void* p, const uint32_t* w, int width) 
   }
 }
 
-// 32 values at columns c .. c + 31 of a row.
+constexpr int kSlab = 32 * 33;  // words of a warp's staging slab
+
+// A warp's 32 rows x 32 columns of results, row `row0 + lane` in this
+// thread's w, 4 / sizeof(T) results a word; columns c .. c + 31.  Whole rows
+// go out as vectors, a thread its own row (full 32-byte sectors).  Where the
+// row stride or the pointer does not allow that, or columns are missing, the
+// warp turns the square round in shared memory and stores a row at a time,
+// consecutive lanes to consecutive columns: the scattered element stores this
+// replaces made the epilogue longer than the products.
+template <typename T>
+__device__ __forceinline__ void st_square(T* out, uint64_t ld, uint64_t row0, uint32_t c,
+                                          uint32_t rows, uint32_t cols, int width, int lane,
+                                          const uint32_t* w, uint32_t* slab) {
+  constexpr int per = 4 / sizeof(T), words = 32 / per;
+  if (width && c + 32 <= cols) {
+    if (row0 + lane < rows) st_words<words>(out + (row0 + lane) * ld + c, w, width);
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < words; ++i) slab[lane * 33 + i] = w[i];
+  __syncwarp();
+  const uint32_t height = rows - row0 < 32 ? (uint32_t)(rows - row0) : 32u;
+  if (c + lane < cols)
+    for (uint32_t r = 0; r < height; ++r)
+      out[(row0 + r) * ld + c + lane] =
+          (T)(slab[r * 33 + lane / per] >> (8 * sizeof(T) * (lane % per)));
+}
+
 template <int DT>
-__device__ __forceinline__ void st_values(const Mat& m, uint64_t row, uint32_t c, uint32_t cols,
-                                          int width, const float* v) {
+__device__ __forceinline__ void st_values(const Mat& m, uint64_t row0, uint32_t c, uint32_t rows,
+                                          uint32_t cols, int width, int lane, const float* v,
+                                          uint32_t* slab) {
   if constexpr (DT == CR_BF16) {
-    uint16_t* p = static_cast<uint16_t*>(m.p) + row * m.ld + c;
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = ffn_bf16x2(v[2 * i], v[2 * i + 1]);
-    if (width && c + 32 <= cols) return st_words<16>(p, w, width);
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c + i < cols) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    st_square(static_cast<uint16_t*>(m.p), m.ld, row0, c, rows, cols, width, lane, w, slab);
   } else {
-    float* p = static_cast<float*>(m.p) + row * m.ld + c;
     uint32_t w[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
-    if (width && c + 32 <= cols) return st_words<32>(p, w, width);
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c + i < cols) p[i] = v[i];
+    st_square(static_cast<uint32_t*>(m.p), m.ld, row0, c, rows, cols, width, lane, w, slab);
   }
 }
 
-__device__ __forceinline__ void st_codes(uint8_t* p, uint32_t c, uint32_t cols, int width,
-                                         const float* v, float inv) {
+__device__ __forceinline__ void st_codes(const Q8& q, uint64_t row0, uint32_t c, uint32_t rows,
+                                         uint32_t cols, int width, int lane, const float* v,
+                                         float inv, uint32_t* slab) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     w[i] = e4m3x2(q8_scaled(v[4 * i], inv), q8_scaled(v[4 * i + 1], inv)) |
            e4m3x2(q8_scaled(v[4 * i + 2], inv), q8_scaled(v[4 * i + 3], inv)) << 16;
-  if (width && c + 32 <= cols) return st_words<8>(p + c, w, width);
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (c + i < cols) p[c + i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+  st_square(q.codes, q.ld, row0, c, rows, cols, width, lane, w, slab);
 }
 
 // Tile `t` of an output, tile rows walked kGroupM at a time.
@@ -137,9 +161,11 @@ __device__ __forceinline__ void ld_acc(uint32_t addr, bool any, float* v) {
 // EPI: the activation (kGlu) or the output's dtype.
 template <int MODE, int EPI>
 __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32_t which,
-                                         uint32_t tm, uint32_t tn, int quarter, int lane) {
-  const uint64_t row = (uint64_t)tm * kM + quarter * 32 + lane;
-  const bool live = row < a.rows;
+                                         uint32_t tm, uint32_t tn, int quarter, int lane,
+                                         uint32_t* slab) {
+  const uint64_t row0 = (uint64_t)tm * kM + quarter * 32;
+  if (row0 >= a.rows) return;
+  const bool live = row0 + lane < a.rows;
   const bool any = a.blocks != 0;
   acc += (uint32_t)(quarter * 32) << 16;
   if constexpr (MODE == kGlu) {
@@ -159,31 +185,73 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32
       }
       const float sg = q8_scale(mg), su = q8_scale(mu);
       inv_g = 1.0f / sg, inv_u = 1.0f / su;
-      if (live && a.g8.codes) a.g8.scales[row * a.g8.lds + tn] = sg;
-      if (live && a.u8.codes) a.u8.scales[row * a.u8.lds + tn] = su;
+      if (live && a.g8.codes) a.g8.scales[(row0 + lane) * a.g8.lds + tn] = sg;
+      if (live && a.u8.codes) a.u8.scales[(row0 + lane) * a.u8.lds + tn] = su;
     }
 #pragma unroll 1
-    for (int c = 0; c < kN / 2; c += 32) {
+    for (uint32_t c = 0; c < kN / 2 && c0 + c < a.cols; c += 32) {
       float g[32], u[32];
-      __syncwarp();  // rows past the matrix leave the last turn early
+      __syncwarp();  // the last square's stores leave rows past the matrix out
       ld_acc(acc + c, any, g);
       ld_acc(acc + kN / 2 + c, any, u);
-      if (!live || c0 + c >= a.cols) continue;
-      if (a.g8.codes) st_codes(a.g8.codes + row * a.g8.ld, c0 + c, a.cols, a.width8, g, inv_g);
-      if (a.u8.codes) st_codes(a.u8.codes + row * a.u8.ld, c0 + c, a.cols, a.width8, u, inv_u);
+      if (a.g8.codes)
+        st_codes(a.g8, row0, c0 + c, a.rows, a.cols, a.width8, lane, g, inv_g, slab);
+      if (a.u8.codes)
+        st_codes(a.u8, row0, c0 + c, a.rows, a.cols, a.width8, lane, u, inv_u, slab);
 #pragma unroll
       for (int i = 0; i < 32; ++i) g[i] = act_gate<EPI>(g[i]) * u[i];
-      st_values<CR_BF16>(a.out[0], row, c0 + c, a.cols, a.width, g);
+      st_values<CR_BF16>(a.out[0], row0, c0 + c, a.rows, a.cols, a.width, lane, g, slab);
     }
   } else {
     const uint32_t c0 = tn * kN;
 #pragma unroll 1
-    for (int c = 0; c < kN; c += 32) {
+    for (uint32_t c = 0; c < kN && c0 + c < a.cols; c += 32) {
       float v[32];
       __syncwarp();
       ld_acc(acc + c, any, v);
-      if (live && c0 + c < a.cols) st_values<EPI>(a.out[which], row, c0 + c, a.cols, a.width, v);
+      st_values<EPI>(a.out[which], row0, c0 + c, a.rows, a.cols, a.width, lane, v, slab);
     }
+  }
+  __syncwarp();
+}
+
+// One K block of a tile into buffer `sa`, arriving on `bar`: one thread.
+template <int MODE>
+__device__ __forceinline__ void load_block(const TileArgs& a, uint32_t which, uint32_t tm,
+                                           uint32_t tn, uint32_t k, uint32_t sa, uint32_t bar) {
+  const uint32_t seg = k >= a.seg_blocks, sb = sa + kABytes;
+  const int k0 = (int)((k - seg * a.seg_blocks) * kK);
+  tc::bar_expect(bar, kStageBytes);
+  if constexpr (MODE == kGlu) {
+    tc::tma_load(sa, &a.a[0], k0, (int)(tm * kM), bar);
+    tc::tma_load(sb, &a.b[0], k0, (int)(tn * (kN / 2)), bar);
+    tc::tma_load(sb + kBBytes / 2, &a.b[1], k0, (int)(tn * (kN / 2)), bar);
+  } else {
+    if constexpr (MODE == kDx) {
+      tc::tma_load(sa, &a.a[seg], k0, (int)(tm * kM), bar);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kM / 64; ++j)
+        tc::tma_load(sa + j * 8192, &a.a[which], (int)(tm * kM) + j * 64, k0, bar);
+    }
+#pragma unroll
+    for (int j = 0; j < kN / 64; ++j)
+      tc::tma_load(sb + j * 8192, &a.b[seg], (int)(tn * kN) + j * 64, k0, bar);
+  }
+}
+
+// The products of one K block: one thread.
+template <int MODE>
+__device__ __forceinline__ void multiply_block(uint32_t acc, uint32_t sa, bool first) {
+  constexpr bool a_mn = MODE == kDw, b_mn = MODE != kGlu;
+  constexpr uint32_t desc = tc::product_desc(kM, kN, a_mn, b_mn);
+  const uint32_t sb = sa + kABytes;
+#pragma unroll
+  for (int j = 0; j < kK / 16; ++j) {
+    // 16 K: 32 bytes along a row, or 16 rows
+    const uint64_t da = a_mn ? tc::operand(sa + j * 2048, 8192, 1024) : tc::operand(sa + j * 32, 16, 1024);
+    const uint64_t db = b_mn ? tc::operand(sb + j * 2048, 8192, 1024) : tc::operand(sb + j * 32, 16, 1024);
+    tc::mma(acc, da, db, desc, !first || j);
   }
 }
 
@@ -191,7 +259,7 @@ template <int MODE, int EPI>
 __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant__ TileArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
-  __shared__ uint32_t tmem_base;
+  __shared__ uint32_t tmem_base, slab[4 * kSlab];
   __shared__ uint32_t gave_up_word;
   volatile uint32_t* gave_up = &gave_up_word;
   const uint32_t smem = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
@@ -232,26 +300,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant
           live = false;
           break;
         }
-        const uint32_t seg = k >= a.seg_blocks;
-        const int k0 = (int)((k - seg * a.seg_blocks) * kK);
-        const uint32_t sa = smem + s * kStageBytes, sb = sa + kABytes;
-        tc::bar_expect(bar, kStageBytes);
-        if constexpr (MODE == kGlu) {
-          tc::tma_load(sa, &a.a[0], k0, (int)(tm * kM), bar);
-          tc::tma_load(sb, &a.b[0], k0, (int)(tn * (kN / 2)), bar);
-          tc::tma_load(sb + kBBytes / 2, &a.b[1], k0, (int)(tn * (kN / 2)), bar);
-        } else {
-          if constexpr (MODE == kDx) {
-            tc::tma_load(sa, &a.a[seg], k0, (int)(tm * kM), bar);
-          } else {
-#pragma unroll
-            for (int j = 0; j < kM / 64; ++j)
-              tc::tma_load(sa + j * 8192, &a.a[which], (int)(tm * kM) + j * 64, k0, bar);
-          }
-#pragma unroll
-          for (int j = 0; j < kN / 64; ++j)
-            tc::tma_load(sb + j * 8192, &a.b[seg], (int)(tn * kN) + j * 64, k0, bar);
-        }
+        load_block<MODE>(a, which, tm, tn, k, smem + s * kStageBytes, bar);
       }
     }
     if (!live) {
@@ -260,8 +309,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant
       for (uint32_t i = first; i < it; ++i) tc::bar_poll(full + 8 * (i % kStages), i / kStages & 1);
     }
   } else if (warp == 1 && lane == 0) {
-    constexpr bool a_mn = MODE == kDw, b_mn = MODE != kGlu;
-    constexpr uint32_t desc = tc::product_desc(kM, kN, a_mn, b_mn);
     uint32_t it = 0, n = 0;
     bool live = true;
     for (uint32_t t = blockIdx.x; t < a.tiles && live; t += gridDim.x, ++n) {
@@ -278,14 +325,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant
           break;
         }
         tc::fence_after();
-        const uint32_t sa = smem + s * kStageBytes, sb = sa + kABytes;
-#pragma unroll
-        for (int j = 0; j < kK / 16; ++j) {
-          // 16 K: 32 bytes along a row, or 16 rows
-          const uint64_t da = a_mn ? tc::operand(sa + j * 2048, 8192, 1024) : tc::operand(sa + j * 32, 16, 1024);
-          const uint64_t db = b_mn ? tc::operand(sb + j * 2048, 8192, 1024) : tc::operand(sb + j * 32, 16, 1024);
-          tc::mma(acc, da, db, desc, k || j);
-        }
+        multiply_block<MODE>(acc, smem + s * kStageBytes, k == 0);
         tc::mma_commit(empty + 8 * s);
       }
       if (live) tc::mma_commit(acc_full + 8 * buf);
@@ -305,7 +345,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant
       if (lane == 0) got = tc::bar_wait(acc_full + 8 * buf, n >> 1 & 1, gave_up);
       if (!__shfl_sync(~0u, got, 0)) break;
       tc::fence_after();
-      epilogue<MODE, EPI>(a, tmem + buf * kN, which, tm, tn, warp & 3, lane);
+      epilogue<MODE, EPI>(a, tmem + buf * kN, which, tm, tn, warp & 3, lane, slab + (warp - 2) * kSlab);
       tc::fence_before();
       tc::bar_arrive(acc_empty + 8 * buf);
     }
@@ -316,6 +356,182 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant
   tc::fence_after();
   if (threadIdx.x == 0 && *gave_up) atomicOr(&g_wait_word, 1u);
   if (warp == 1) tc::tmem_free(tmem, 2 * kN);
+}
+
+// ---- few tiles: a cluster for each ------------------------------------------------------
+
+constexpr int kPartStride = kN + 4;  // floats: rows 16 bytes apart in the banks
+static_assert(kM * kPartStride * 4 <= kStages * kStageBytes, "partials reuse the buffers");
+
+// One row of a tile, columns 4 * lane .. + 3 of each half (for kGlu, of g and
+// of u): whole warp.
+template <int MODE, int EPI>
+__device__ __forceinline__ void finish_row(const TileArgs& a, uint32_t which, uint64_t row,
+                                           uint32_t tn, int lane, const float* lo, const float* hi) {
+  if constexpr (MODE == kGlu) {
+    const uint32_t c = tn * (kN / 2) + 4 * lane;
+    float act[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) act[i] = act_gate<EPI>(lo[i]) * hi[i];
+    uint16_t* p = static_cast<uint16_t*>(a.out[0].p) + row * a.out[0].ld + c;
+    if (a.width && c + 4 <= a.cols) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(ffn_bf16x2(act[0], act[1]), ffn_bf16x2(act[2], act[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < a.cols) p[i] = (uint16_t)ffn_bf16x2(act[i], 0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const Q8& q = k ? a.u8 : a.g8;
+      const float* v = k ? hi : lo;
+      if (!q.codes) continue;
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, q8_magnitude(v[i]));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+      const float s = q8_scale(m), inv = 1.0f / s;
+      if (lane == 0) q.scales[row * q.lds + tn] = s;
+      const uint32_t w = e4m3x2(q8_scaled(v[0], inv), q8_scaled(v[1], inv)) |
+                         e4m3x2(q8_scaled(v[2], inv), q8_scaled(v[3], inv)) << 16;
+      uint8_t* codes = q.codes + row * q.ld + c;
+      if (a.width8 && c + 4 <= a.cols) {
+        *reinterpret_cast<uint32_t*>(codes) = w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < a.cols) codes[i] = (uint8_t)(w >> (8 * i));
+      }
+    }
+  } else {
+    const Mat& m = a.out[which];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t c = tn * kN + k * (kN / 2) + 4 * lane;
+      const float* v = k ? hi : lo;
+      if constexpr (EPI == CR_BF16) {
+        uint16_t* p = static_cast<uint16_t*>(m.p) + row * m.ld + c;
+        if (a.width && c + 4 <= a.cols) {
+          *reinterpret_cast<uint2*>(p) = make_uint2(ffn_bf16x2(v[0], v[1]), ffn_bf16x2(v[2], v[3]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < a.cols) p[i] = (uint16_t)ffn_bf16x2(v[i], 0.0f);
+        }
+      } else {
+        float* p = static_cast<float*>(m.p) + row * m.ld + c;
+        if (a.width && c + 4 <= a.cols) {
+          *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < a.cols) p[i] = v[i];
+        }
+      }
+    }
+  }
+}
+
+// Cluster blockIdx.x / a.splits takes that tile, its block of rank r the r-th
+// part of the K blocks.
+template <int MODE, int EPI>
+__global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant__ TileArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 1];
+  __shared__ uint32_t tmem_base;
+  __shared__ uint32_t gave_up_word;
+  volatile uint32_t* gave_up = &gave_up_word;
+  const uint32_t smem = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
+  float* part = reinterpret_cast<float*>(smem_raw + (smem - tc::smem_addr(smem_raw)));
+  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
+  const uint32_t acc_full = empty + 8 * kStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::bar_init(full + 8 * s, 1);
+      tc::bar_init(empty + 8 * s, 1);
+    }
+    tc::bar_init(acc_full, 1);
+    *gave_up = 0;
+    tc::bar_init_fence();
+  }
+  if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_base), kN);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  pdl_enter();
+  const uint32_t tmem = tmem_base;
+  const uint32_t rank = tc::cluster_rank();
+  uint32_t which, tm, tn;
+  tile_at(a, blockIdx.x / a.splits, &which, &tm, &tn);
+  const uint32_t k0 = (uint32_t)((uint64_t)a.blocks * rank / a.splits);
+  const uint32_t k1 = (uint32_t)((uint64_t)a.blocks * (rank + 1) / a.splits);
+
+  if (warp == 0 && lane == 0) {
+    uint32_t it = 0;
+    bool live = true;
+    for (uint32_t k = k0; k < k1; ++k, ++it) {
+      const uint32_t s = it % kStages;
+      if (!(live = tc::bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, gave_up))) break;
+      load_block<MODE>(a, which, tm, tn, k, smem + s * kStageBytes, full + 8 * s);
+    }
+    if (!live) {
+      const uint32_t first = it > kStages ? it - kStages : 0;
+      for (uint32_t i = first; i < it; ++i) tc::bar_poll(full + 8 * (i % kStages), i / kStages & 1);
+    }
+  } else if (warp == 1 && lane == 0) {
+    uint32_t it = 0;
+    for (uint32_t k = k0; k < k1; ++k, ++it) {
+      const uint32_t s = it % kStages;
+      if (!tc::bar_wait(full + 8 * s, it / kStages & 1, gave_up)) break;
+      tc::fence_after();
+      multiply_block<MODE>(tmem, smem + s * kStageBytes, k == k0);
+      tc::mma_commit(empty + 8 * s);
+    }
+    // every product issued: the buffers are free and the sums complete
+    tc::mma_commit(acc_full);
+    tc::bar_poll(acc_full, 0);
+  }
+  __syncwarp();
+  if (warp >= 2) {
+    if (lane == 0) tc::bar_wait(acc_full, 0, gave_up);
+    __syncwarp();
+    tc::fence_after();
+    const int quarter = warp & 3;
+    float* row = part + (quarter * 32 + lane) * kPartStride;
+    const bool any = k1 > k0;
+#pragma unroll 1
+    for (int c = 0; c < kN; c += 32) {
+      float v[32];
+      ld_acc(tmem + ((uint32_t)(quarter * 32) << 16) + c, any, v);
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        *reinterpret_cast<float4*>(row + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+    tc::fence_before();
+  }
+  tc::cluster_sync();
+  const int height = kM / (int)a.splits;
+  for (int r = warp; r < height; r += kTileThreads / 32) {
+    const int at = (int)rank * height + r;
+    const uint64_t row = (uint64_t)tm * kM + at;
+    if (row >= a.rows) break;
+    float lo[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t addr = smem + (uint32_t)(at * kPartStride + 4 * lane) * 4;
+    for (uint32_t p = 0; p < a.splits; ++p) {
+      const uint32_t from = tc::cluster_addr(addr, p);
+      const float4 x = tc::cluster_ld4(from), y = tc::cluster_ld4(from + kN / 2 * 4);
+      lo[0] += x.x, lo[1] += x.y, lo[2] += x.z, lo[3] += x.w;
+      hi[0] += y.x, hi[1] += y.y, hi[2] += y.z, hi[3] += y.w;
+    }
+    finish_row<MODE, EPI>(a, which, row, tn, lane, lo, hi);
+  }
+  tc::cluster_sync();  // no block leaves while another reads its partials
+  tc::fence_after();
+  if (threadIdx.x == 0 && *gave_up) atomicOr(&g_wait_word, 1u);
+  if (warp == 1) tc::tmem_free(tmem, kN);
 }
 
 // ---- host side ------------------------------------------------------------------------
@@ -367,24 +583,39 @@ uint32_t ceil_div(uint32_t a, uint32_t b) { return (uint32_t)(((uint64_t)a + b -
 // Bytes all rows of the outputs allow.
 int out_width(const Mat& m, uint32_t rows, size_t es) { return store_width(m.p, rows > 1 ? m.ld * es : 0); }
 
+// Blocks to share a tile: as many as leave no SM without one (tiles * splits
+// <= SMs) and each at least kMinBlocks K blocks, at most 8 (a portable cluster).
+constexpr uint32_t kMinBlocks = 4;
+
+uint32_t split_of(const TileArgs& a, int sms) {
+  uint32_t s = 1;
+  while (s < 8 && (uint64_t)a.tiles * s * 2 <= (uint64_t)sms && a.blocks >= s * 2 * kMinBlocks) s *= 2;
+  return s;
+}
+
 template <int MODE, int EPI>
 cudaError_t run_tiles(TileArgs& a, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_tiles<MODE, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+  a.splits = split_of(a, sms);
+  void (*kernel)(const TileArgs) = a.splits > 1 ? k_split<MODE, EPI> : k_tiles<MODE, EPI>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.tiles < (uint32_t)sms ? a.tiles : (uint32_t)sms);
+  cfg.gridDim = dim3(a.splits > 1 ? a.tiles * a.splits : std::min(a.tiles, (uint32_t)sms));
   cfg.blockDim = dim3(kTileThreads);
   cfg.dynamicSmemBytes = kTileSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_tiles<MODE, EPI>, a);
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 // Tiles of `outputs` outputs of rows x cols, `width` columns a tile.
