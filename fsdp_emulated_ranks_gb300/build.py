@@ -30,7 +30,8 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]
 SOURCES = ["api.cu", "api_buckets.cu", "api_optim.cu", "api_range.cu", "launch_util.cu", "k_collectives.cu", "k_fsdp.cu",
            "k_bucket.cu", "k_bucket_fused.cu", "k_fsdp2.cu", "k_accum.cu",
-           "k_hsdp.cu", "api_ffn.cu", "k_norm.cu", "k_q8.cu", "k_glu.cu", "reducer.cu", "fsdp_noalloc.cu", "check.cu", "plan.cpp",
+           "k_hsdp.cu", "api_ffn.cu", "k_norm.cu", "k_q8.cu", "k_glu.cu", "k_glu_few.cu",
+           "reducer.cu", "fsdp_noalloc.cu", "check.cu", "plan.cpp",
            "comm.cpp"]
 
 

@@ -230,12 +230,14 @@ def _ld(x, ld=None) -> int:
     for an absent matrix, and for a pointer or a vector)."""
     if ld is not None:
         return ld
-    if x is None or type(x) is int or x.dim() < 2:
+    if x is None or type(x) is int:
         return 0
-    rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    st = x.stride()
+    if len(st) < 2:
+        return 0
+    if st[1] != 1 and x.shape[1] > 1:
         raise ValueError("the columns of a matrix must be contiguous")
-    return x.stride(0) if rows > 1 else cols
+    return st[0]
 
 
 _PACK = {}  # length -> struct packer of that many native 64-bit pointers

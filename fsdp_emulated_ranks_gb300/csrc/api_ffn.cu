@@ -280,7 +280,6 @@ cr_status cr_rms_norm_backward(const void* dy, size_t lddy, const void* h, size_
   k.partial = dweight ? static_cast<float*>(workspace) : nullptr;
   k.rows = rows;
   k.cols = (uint32_t)cols;
-  k.parts = norm_back_parts(rows, k.cols);
   k.inv_cols = 1.0f / (float)cols;
   return launched(launch_rms_norm_back(dtype, dw_dtype, k, a.vec(), stream_of(stream)),
                   "cr_rms_norm_backward");
@@ -336,6 +335,12 @@ cr_status cr_glu(const void* x, size_t ldx, const void* wg, size_t ldwg, const v
   GluArgs k = {mat(x, ldx), mat(wg, ldwg), mat(wu, ldwu),   mat(a_out, lda), q8_of(g8),
                q8_of(u8),   (uint32_t)tokens, (uint32_t)dim, (uint32_t)ffn};
   const cudaStream_t s = stream_of(stream);
+  if (glu_few(tokens, dim, g8 || u8)) {
+    Args w;
+    w.matrix("wg", wg, ffn, dim, ldwg, 2, false);
+    w.matrix("wu", wu, ffn, dim, ldwu, 2, false);
+    return launched(launch_glu_few(act, k, w.vec16, s), "cr_glu");
+  }
   uint16_t* ws = static_cast<uint16_t*>(workspace);
   cudaError_t e = operand(&k.x, tokens, dim, ws, s);
   ws += padded(tokens, dim);

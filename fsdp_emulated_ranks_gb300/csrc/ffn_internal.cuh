@@ -84,7 +84,7 @@ struct GluBackArgs {
 cudaError_t launch_rms_norm(cr_dtype d, const NormArgs& a, bool vec, cudaStream_t s);
 // Row partials the backward pass writes for its dweight, at most.
 uint32_t norm_back_parts(uint64_t rows, uint32_t cols);
-cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, const NormBackArgs& a, bool vec,
+cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, NormBackArgs a, bool vec,
                                  cudaStream_t s);
 cudaError_t launch_q8_store(cr_dtype d, const Mat& x, const Q8& q, uint64_t rows, uint32_t cols,
                             bool vec, cudaStream_t s);
@@ -98,6 +98,11 @@ cudaError_t launch_copy_bf16(const Mat& src, const Mat& dst, uint64_t rows, uint
                              cudaStream_t s);
 cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, bool vec, cudaStream_t s);
 cudaError_t launch_glu(cr_act act, const GluArgs& a, cudaStream_t s);
+// Whether the block's call is one for k_glu_few.cu: few tokens, whose x fits
+// in shared memory, and no checkpoints (keeps).  Operands at any alignment;
+// vec: 16-byte aligned rows of both weights.
+bool glu_few(uint64_t tokens, uint64_t dim, bool keeps);
+cudaError_t launch_glu_few(cr_act act, const GluArgs& a, bool vec, cudaStream_t s);
 cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& a, cudaStream_t s);
 // Reads (and clears) the word a block sets that gave up a wait.
 cudaError_t glu_wait_word(bool clear, unsigned int* word);
@@ -150,41 +155,65 @@ __device__ __forceinline__ uint32_t chunk_col(uint32_t base, int lane, int i) {
   return VEC ? base + lane * kLaneVals + i : base + i * 32 + lane;
 }
 
-template <int DT>
-__device__ __forceinline__ float ld_value(const void* p, uint64_t e) {
-  if constexpr (DT == CR_BF16) return ffn_bf16(__ldg(static_cast<const uint16_t*>(p) + e));
-  return __ldg(static_cast<const float*>(p) + e);
-}
+// A chunk as loaded, before it is widened to fp32: what a kernel that loads
+// ahead keeps.  Values of columns past `cols` are zero.
+template <int DT, bool VEC>
+struct Raw {
+  static constexpr int kWords = DT == CR_BF16 ? (VEC ? 4 : 8) : 8;
+  uint32_t w[kWords];
 
-// Values of columns past `cols` are zero.  `row` points at the row's column 0.
+  // `row` points at the row's column 0.
+  __device__ __forceinline__ void load(const void* row, uint32_t base, uint32_t cols, int lane) {
+    const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
+    if constexpr (VEC) {
+      if (c0 + kLaneVals <= cols) {
+        if constexpr (DT == CR_BF16) {
+          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c0);
+          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + c0);
+          const uint4 q = p[0], r = p[1];
+          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+          w[4] = r.x, w[5] = r.y, w[6] = r.z, w[7] = r.w;
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kLaneVals; ++i) {
+      const uint32_t c = chunk_col<VEC>(base, lane, i);
+      if (c >= cols) continue;
+      if constexpr (DT == CR_F32)
+        w[i] = static_cast<const uint32_t*>(row)[c];
+      else if constexpr (VEC)
+        w[i / 2] |= (uint32_t) static_cast<const uint16_t*>(row)[c] << (16 * (i & 1));
+      else
+        w[i] = (uint32_t) static_cast<const uint16_t*>(row)[c] << 16;
+    }
+  }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (DT == CR_BF16 && VEC)
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    else
+      return __uint_as_float(w[i]);
+  }
+};
+
 template <int DT, bool VEC>
 __device__ __forceinline__ void ld_chunk(const void* row, uint32_t base, uint32_t cols, int lane,
                                          float* v) {
-  const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
-  if (VEC && c0 + kLaneVals <= cols) {
-    if constexpr (DT == CR_BF16) {
-      const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c0);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  Raw<DT, VEC> r;
+  r.load(row, base, cols, lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + c0);
-      const float4 q = p[0], r = p[1];
-      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w, v[4] = r.x, v[5] = r.y, v[6] = r.z, v[7] = r.w;
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < kLaneVals; ++i) {
-    const uint32_t c = chunk_col<VEC>(base, lane, i);
-    if constexpr (DT == CR_BF16)
-      v[i] = c < cols ? ffn_bf16(static_cast<const uint16_t*>(row)[c]) : 0.0f;
-    else
-      v[i] = c < cols ? static_cast<const float*>(row)[c] : 0.0f;
-  }
+  for (int i = 0; i < kLaneVals; ++i) v[i] = r.value(i);
 }
 
 template <int DT, bool VEC>
@@ -261,42 +290,67 @@ __device__ __forceinline__ void st_chunk_q8(const Q8& q, uint64_t row, uint32_t 
   }
 }
 
-// The values a chunk of an 8-bit matrix stands for (fp32, not rounded further).
+// A chunk of an 8-bit matrix as loaded.  VEC: 8 codes and the one scale of the
+// lane's half; otherwise a code a word and both scales.
 template <bool VEC>
-__device__ __forceinline__ void ld_chunk_q8(const Q8& q, uint64_t row, uint32_t base,
-                                            uint32_t cols, int lane, float* v) {
-  const uint8_t* codes = q.codes + row * q.ld;
-  const float* scales = q.scales + row * q.lds;
-  const uint32_t group = base / CR_Q8_GROUP;
-  if constexpr (VEC) {
+struct RawQ8 {
+  uint32_t w[VEC ? 2 : 8];
+  float s[VEC ? 1 : 2];
+
+  __device__ __forceinline__ void load(const Q8& q, uint64_t row, uint32_t base, uint32_t cols,
+                                       int lane) {
+    const uint8_t* codes = q.codes + row * q.ld;
+    const float* scales = q.scales + row * q.lds + base / CR_Q8_GROUP;
     const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
-    uint32_t w[2] = {0u, 0u};
-    float s = 0.0f;
-    if (c0 < cols) s = scales[group + (lane >> 4)];
-    if (c0 + kLaneVals <= cols) {
-      const uint2 t = *reinterpret_cast<const uint2*>(codes + c0);
-      w[0] = t.x, w[1] = t.y;
+    if constexpr (VEC) {
+      s[0] = c0 < cols ? scales[lane >> 4] : 0.0f;
+      w[0] = w[1] = 0;
+      if (c0 + kLaneVals <= cols) {
+        const uint2 t = *reinterpret_cast<const uint2*>(codes + c0);
+        w[0] = t.x, w[1] = t.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLaneVals; ++i)
+          if (c0 + i < cols) w[i >> 2] |= (uint32_t)codes[c0 + i] << (8 * (i & 3));
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i)
-        if (c0 + i < cols) w[i >> 2] |= (uint32_t)codes[c0 + i] << (8 * (i & 3));
-    }
+      for (int h = 0; h < 2; ++h) s[h] = base + h * CR_Q8_GROUP < cols ? scales[h] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = from_e4m3x2(w[i >> 1] >> (16 * (i & 1)));
-      v[2 * i] = f.x * s, v[2 * i + 1] = f.y * s;
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float s = base + h * CR_Q8_GROUP < cols ? scales[group + h] : 0.0f;
-#pragma unroll
-      for (int i = 4 * h; i < 4 * h + 4; ++i) {
+      for (int i = 0; i < kLaneVals; ++i) {
         const uint32_t c = chunk_col<VEC>(base, lane, i);
-        v[i] = c < cols ? from_e4m3x2(codes[c]).x * s : 0.0f;
+        w[i] = c < cols ? codes[c] : 0u;
       }
     }
   }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (VEC ? 2 : 8); ++i) w[i] = 0;
+    s[0] = s[VEC ? 0 : 1] = 0.0f;
+  }
+
+  // The values the codes stand for (fp32, not rounded further).
+  __device__ __forceinline__ void values(float* v) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = from_e4m3x2(w[i >> 1] >> (16 * (i & 1)));
+        v[2 * i] = f.x * s[0], v[2 * i + 1] = f.y * s[0];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLaneVals; ++i) v[i] = from_e4m3x2(w[i]).x * s[i / 4];
+    }
+  }
+};
+
+template <bool VEC>
+__device__ __forceinline__ void ld_chunk_q8(const Q8& q, uint64_t row, uint32_t base,
+                                            uint32_t cols, int lane, float* v) {
+  RawQ8<VEC> r;
+  r.load(q, row, base, cols, lane);
+  r.values(v);
 }
 
 // ---- the gate's activation -----------------------------------------------------------

@@ -15,6 +15,9 @@
 // kernel adds the partials in order.  Wide rows take a second pass over dy
 // and h for dweight.
 #include <algorithm>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "ffn_internal.cuh"
 #include "pdl.cuh"
@@ -23,9 +26,10 @@ namespace cr {
 
 namespace {
 
-constexpr int kRowThreads = 256;        // threads of a block that holds rows in registers
+constexpr int kRowThreads = 512;        // threads of a block that holds rows in registers, at most
 constexpr int kWideThreads = 1024;      // threads of a block on a wide row
-constexpr uint32_t kWideFrom = 8192;    // columns above which a row is wide: 8 warps x 4 chunks
+constexpr uint32_t kWideFrom = 8192;    // columns above which a row is wide: 16 warps x 2 chunks
+constexpr uint32_t kBackBlocks = 912;   // of the backward pass, at most: 6 on each of 152 SMs
 constexpr int kMaxWarps = kWideThreads / 32;
 
 // Sum over the row's warps (blockDim.x / 32 of them, row threadIdx.y of the
@@ -45,187 +49,251 @@ __device__ __forceinline__ float row_sum(float s, float (*part)[kMaxWarps], int 
   return s;
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void norm_ld(const NormArgs& a, uint64_t row, uint32_t base, int lane,
-                                        float* h) {
-  constexpr int es = DT == CR_BF16 ? 2 : 4;
-  ld_chunk<DT, VEC>(static_cast<const char*>(a.x.p) + row * a.x.ld * es, base, a.cols, lane, h);
-  if (a.residual.p) {
-    float r[kLaneVals];
-    ld_chunk<DT, VEC>(static_cast<const char*>(a.residual.p) + row * a.residual.ld * es, base,
-                      a.cols, lane, r);
-#pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) h[i] += r[i];
-  }
+template <int DT>
+__device__ __forceinline__ const void* row_of(const Mat& m, uint64_t row) {
+  return static_cast<const char*>(m.p) + row * m.ld * (DT == CR_BF16 ? 2 : 4);
 }
+
+template <int DT>
+__device__ __forceinline__ void* row_of_out(const Mat& m, uint64_t row) {
+  return static_cast<char*>(m.p) + row * m.ld * (DT == CR_BF16 ? 2 : 4);
+}
+
+// x and residual of a row's chunk.
+template <int DT, bool VEC>
+struct NormIn {
+  Raw<DT, VEC> x, r;
+
+  __device__ __forceinline__ void load(const NormArgs& a, uint64_t row, uint32_t base, int lane) {
+    x.load(row_of<DT>(a.x, row), base, a.cols, lane);
+    if (a.residual.p)
+      r.load(row_of<DT>(a.residual, row), base, a.cols, lane);
+    else
+      r.clear();
+  }
+  __device__ __forceinline__ void clear() { x.clear(), r.clear(); }
+  __device__ __forceinline__ void values(float* h) const {
+#pragma unroll
+    for (int i = 0; i < kLaneVals; ++i) h[i] = x.value(i) + r.value(i);
+  }
+};
 
 template <int DT, bool VEC>
 __device__ __forceinline__ void norm_st(const NormArgs& a, uint64_t row, uint32_t base, int lane,
-                                        float* h, float rstd) {
-  constexpr int es = DT == CR_BF16 ? 2 : 4;
-  if (a.sum.p)
-    st_chunk<DT, VEC>(static_cast<char*>(a.sum.p) + row * a.sum.ld * es, base, a.cols, lane, h);
-  float w[kLaneVals];
-  ld_chunk<DT, VEC>(a.weight, base, a.cols, lane, w);
+                                        float* h, const Raw<DT, VEC>& w, float rstd) {
+  if (a.sum.p) st_chunk<DT, VEC>(row_of_out<DT>(a.sum, row), base, a.cols, lane, h);
 #pragma unroll
-  for (int i = 0; i < kLaneVals; ++i) h[i] = h[i] * rstd * w[i];
-  if (a.y.p)
-    st_chunk<DT, VEC>(static_cast<char*>(a.y.p) + row * a.y.ld * es, base, a.cols, lane, h);
+  for (int i = 0; i < kLaneVals; ++i) h[i] = h[i] * rstd * w.value(i);
+  if (a.y.p) st_chunk<DT, VEC>(row_of_out<DT>(a.y, row), base, a.cols, lane, h);
   if (a.y8.codes) st_chunk_q8<VEC>(a.y8, row, base, a.cols, lane, h);
 }
 
-// Block (32 * warps per row, rows per block).
+// Block (32 * warps per row, rows per block), persistent.  The next row is
+// loaded while this one is reduced and written.
 template <int DT, int V, bool VEC>
-__global__ void __launch_bounds__(V ? kRowThreads : kWideThreads)
-    k_rms_norm(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kRowThreads) k_rms_norm(const __grid_constant__ NormArgs a) {
   pdl_enter();
   __shared__ float part[2][kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const uint64_t step = (uint64_t)gridDim.x * blockDim.y;
-  int buf = 0;
-  // every row of a block's iteration takes part in the barriers
-  for (uint64_t first = (uint64_t)blockIdx.x * blockDim.y; first < a.rows; first += step) {
-    const uint64_t row = first + threadIdx.y;
-    const bool live = row < a.rows;
-    float s = 0.0f;
-    if constexpr (V > 0) {
-      float h[V][kLaneVals];
+  uint32_t base[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const uint32_t base = (uint32_t)(warp + k * nw) * kChunk;
+  for (int k = 0; k < V; ++k) base[k] = (uint32_t)(warp + k * nw) * kChunk;
+  NormIn<DT, VEC> in[V];
+  Raw<DT, VEC> w[V];
+  const auto load = [&](uint64_t row) {
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) h[k][i] = 0.0f;
-        if (live && base < a.cols) norm_ld<DT, VEC>(a, row, base, lane, h[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-#pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) s = fmaf(h[k][i], h[k][i], s);
-      const float rstd = 1.0f / sqrtf(row_sum(s, part, buf) * a.inv_cols + a.eps);
-      if (live) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const uint32_t base = (uint32_t)(warp + k * nw) * kChunk;
-          if (base < a.cols) norm_st<DT, VEC>(a, row, base, lane, h[k], rstd);
-        }
-        if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-      }
-    } else {
-      float h[kLaneVals];
-      if (live)
-        for (uint64_t base = (uint64_t)warp * kChunk; base < a.cols; base += (uint64_t)nw * kChunk) {
-          norm_ld<DT, VEC>(a, row, (uint32_t)base, lane, h);
-#pragma unroll
-          for (int i = 0; i < kLaneVals; ++i) s = fmaf(h[i], h[i], s);
-        }
-      const float rstd = 1.0f / sqrtf(row_sum(s, part, buf) * a.inv_cols + a.eps);
-      if (live) {
-        for (uint64_t base = (uint64_t)warp * kChunk; base < a.cols; base += (uint64_t)nw * kChunk) {
-          norm_ld<DT, VEC>(a, row, (uint32_t)base, lane, h);
-          norm_st<DT, VEC>(a, row, (uint32_t)base, lane, h, rstd);
-        }
-        if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-      }
+    for (int k = 0; k < V; ++k) {
+      if (row < a.rows && base[k] < a.cols)
+        in[k].load(a, row, base[k], lane);
+      else
+        in[k].clear();
     }
-    buf ^= 1;
+  };
+  load((uint64_t)blockIdx.x * blockDim.y + threadIdx.y);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    w[k].clear();
+    if (base[k] < a.cols) w[k].load(a.weight, base[k], a.cols, lane);
+  }
+  int buf = 0;
+  // every row of a block's turn takes part in the barriers
+  for (uint64_t first = (uint64_t)blockIdx.x * blockDim.y; first < a.rows; first += step, buf ^= 1) {
+    const uint64_t row = first + threadIdx.y;
+    float h[V][kLaneVals], s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      in[k].values(h[k]);
+#pragma unroll
+      for (int i = 0; i < kLaneVals; ++i) s = fmaf(h[k][i], h[k][i], s);
+    }
+    load(row + step);
+    const float rstd = 1.0f / sqrtf(row_sum(s, part, buf) * a.inv_cols + a.eps);
+    if (row >= a.rows) continue;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (base[k] < a.cols) norm_st<DT, VEC>(a, row, base[k], lane, h[k], w[k], rstd);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+  }
+}
+
+// Wide rows, one block each, read twice: the second time from L2.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kWideThreads)
+    k_rms_norm_wide(const __grid_constant__ NormArgs a) {
+  pdl_enter();
+  __shared__ float part[2][kMaxWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int buf = 0;
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+    NormIn<DT, VEC> in;
+    float h[kLaneVals], s = 0.0f;
+    for (uint64_t base = (uint64_t)warp * kChunk; base < a.cols; base += (uint64_t)nw * kChunk) {
+      in.load(a, row, (uint32_t)base, lane);
+      in.values(h);
+#pragma unroll
+      for (int i = 0; i < kLaneVals; ++i) s = fmaf(h[i], h[i], s);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum(s, part, buf) * a.inv_cols + a.eps);
+    for (uint64_t base = (uint64_t)warp * kChunk; base < a.cols; base += (uint64_t)nw * kChunk) {
+      Raw<DT, VEC> w;
+      w.load(a.weight, (uint32_t)base, a.cols, lane);
+      in.load(a, row, (uint32_t)base, lane);
+      in.values(h);
+      norm_st<DT, VEC>(a, row, (uint32_t)base, lane, h, w, rstd);
+    }
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   }
 }
 
 // ---- backward -----------------------------------------------------------------------
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void back_ld(const NormBackArgs& a, uint64_t row, uint32_t base,
-                                        int lane, float* dy, float* h) {
-  constexpr int es = DT == CR_BF16 ? 2 : 4;
-  ld_chunk<DT, VEC>(static_cast<const char*>(a.dy.p) + row * a.dy.ld * es, base, a.cols, lane, dy);
-  if (a.h8.codes)
-    ld_chunk_q8<VEC>(a.h8, row, base, a.cols, lane, h);
-  else
-    ld_chunk<DT, VEC>(static_cast<const char*>(a.h.p) + row * a.h.ld * es, base, a.cols, lane, h);
-}
+// h of a chunk, from the matrix or from its 8-bit form.
+template <int DT, bool VEC, bool HELD8>
+struct HeldIn {
+  Raw<DT, VEC> r;
+  __device__ __forceinline__ void load(const NormBackArgs& a, uint64_t row, uint32_t base, int lane) {
+    r.load(row_of<DT>(a.h, row), base, a.cols, lane);
+  }
+  __device__ __forceinline__ void clear() { r.clear(); }
+  __device__ __forceinline__ void values(float* h) const {
+#pragma unroll
+    for (int i = 0; i < kLaneVals; ++i) h[i] = r.value(i);
+  }
+};
 
-// t = dy * weight in, dx out.
+template <int DT, bool VEC>
+struct HeldIn<DT, VEC, true> {
+  RawQ8<VEC> r;
+  __device__ __forceinline__ void load(const NormBackArgs& a, uint64_t row, uint32_t base, int lane) {
+    r.load(a.h8, row, base, a.cols, lane);
+  }
+  __device__ __forceinline__ void clear() { r.clear(); }
+  __device__ __forceinline__ void values(float* h) const { r.values(h); }
+};
+
+// t = dy * weight, n = h * rstd; res: dres, or zeros.
 template <int DT, bool VEC>
 __device__ __forceinline__ void back_st(const NormBackArgs& a, uint64_t row, uint32_t base,
-                                        int lane, const float* t, const float* n, float rstd,
-                                        float c) {
-  constexpr int es = DT == CR_BF16 ? 2 : 4;
+                                        int lane, const float* t, const float* n,
+                                        const Raw<DT, VEC>& res, float rstd, float c) {
   float dx[kLaneVals];
 #pragma unroll
-  for (int i = 0; i < kLaneVals; ++i) dx[i] = rstd * (t[i] - n[i] * c);
-  if (a.dres.p) {
-    float r[kLaneVals];
-    ld_chunk<DT, VEC>(static_cast<const char*>(a.dres.p) + row * a.dres.ld * es, base, a.cols,
-                      lane, r);
-#pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) dx[i] += r[i];
-  }
-  st_chunk<DT, VEC>(static_cast<char*>(a.dx.p) + row * a.dx.ld * es, base, a.cols, lane, dx);
+  for (int i = 0; i < kLaneVals; ++i) dx[i] = rstd * (t[i] - n[i] * c) + res.value(i);
+  st_chunk<DT, VEC>(row_of_out<DT>(a.dx, row), base, a.cols, lane, dx);
 }
 
-// Rows of at most kWideFrom columns: block (32 * warps per row, 1), rows
-// blockIdx.x, + gridDim.x, ...; partial row blockIdx.x of dweight.
-template <int DT, int V, bool VEC>
+// Rows of at most kWideFrom columns: block (32 * warps per row, rows per
+// block), persistent; partial row blockIdx.x * blockDim.y + threadIdx.y of
+// dweight.  Everything the next row needs is loaded while this one is reduced
+// and written; dweight's sums and the weights stay in registers.
+template <int DT, int V, bool VEC, bool HELD8>
 __global__ void __launch_bounds__(kRowThreads)
     k_rms_norm_back(const __grid_constant__ NormBackArgs a) {
   pdl_enter();
   __shared__ float part[2][kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const uint64_t step = (uint64_t)gridDim.x * blockDim.y;
+  uint32_t base[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) base[k] = (uint32_t)(warp + k * nw) * kChunk;
+  Raw<DT, VEC> dy[V], res[V], w[V];
+  HeldIn<DT, VEC, HELD8> held[V];
+  float next_rstd = 0.0f;
+  const auto load = [&](uint64_t row) {
+    if (row < a.rows) next_rstd = a.rstd[row];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (row < a.rows && base[k] < a.cols) {
+        dy[k].load(row_of<DT>(a.dy, row), base[k], a.cols, lane);
+        held[k].load(a, row, base[k], lane);
+        if (a.dres.p) res[k].load(row_of<DT>(a.dres, row), base[k], a.cols, lane);
+      } else {
+        dy[k].clear();
+        held[k].clear();
+      }
+    }
+  };
   float dw[V][kLaneVals];
 #pragma unroll
-  for (int k = 0; k < V; ++k)
+  for (int k = 0; k < V; ++k) {
 #pragma unroll
     for (int i = 0; i < kLaneVals; ++i) dw[k][i] = 0.0f;
-  int buf = 0;
-  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
-    const float rstd = a.rstd[row];
-    float t[V][kLaneVals], n[V][kLaneVals], s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const uint32_t base = (uint32_t)(warp + k * nw) * kChunk;
-      if (base < a.cols) {
-        back_ld<DT, VEC>(a, row, base, lane, t[k], n[k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) t[k][i] = n[k][i] = 0.0f;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const uint32_t base = (uint32_t)(warp + k * nw) * kChunk;
-      float w[kLaneVals];
-      if (base < a.cols) {
-        ld_chunk<DT, VEC>(a.weight, base, a.cols, lane, w);
-#pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) {
-          n[k][i] *= rstd;
-          dw[k][i] = fmaf(t[k][i], n[k][i], dw[k][i]);
-          t[k][i] *= w[i];
-          s = fmaf(t[k][i], n[k][i], s);
-        }
-      }
-    }
-    if (a.dx.p) {
-      const float c = row_sum(s, part, buf) * a.inv_cols;
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const uint32_t base = (uint32_t)(warp + k * nw) * kChunk;
-        if (base < a.cols) back_st<DT, VEC>(a, row, base, lane, t[k], n[k], rstd, c);
-      }
-    }
+    res[k].clear();
+    w[k].clear();
   }
-  if (a.partial) {
-    float* p = a.partial + (uint64_t)blockIdx.x * a.cols;
+  load((uint64_t)blockIdx.x * blockDim.y + threadIdx.y);
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (base[k] < a.cols && a.rows) w[k].load(a.weight, base[k], a.cols, lane);
+  int buf = 0;
+  // every row of a block's turn takes part in the barriers
+  for (uint64_t first = (uint64_t)blockIdx.x * blockDim.y; first < a.rows; first += step, buf ^= 1) {
+    const uint64_t row = first + threadIdx.y;
+    const float rstd = next_rstd;
+    float t[V][kLaneVals], n[V][kLaneVals], s = 0.0f;
+    Raw<DT, VEC> r[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const uint32_t base = (uint32_t)(warp + k * nw) * kChunk;
+      held[k].values(n[k]);
+      r[k] = res[k];
 #pragma unroll
       for (int i = 0; i < kLaneVals; ++i) {
-        const uint32_t c = chunk_col<VEC>(base, lane, i);
-        if (c < a.cols) p[c] = dw[k][i];
+        n[k][i] *= rstd;
+        const float d = dy[k].value(i);
+        dw[k][i] = fmaf(d, n[k][i], dw[k][i]);
+        t[k][i] = d * w[k].value(i);
+        s = fmaf(t[k][i], n[k][i], s);
       }
     }
+    load(row + step);
+    if (!a.dx.p) continue;
+    const float c = row_sum(s, part, buf) * a.inv_cols;
+    if (row >= a.rows) continue;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (base[k] < a.cols) back_st<DT, VEC>(a, row, base[k], lane, t[k], n[k], r[k], rstd, c);
   }
+  if (a.partial) {
+    float* p = a.partial + ((uint64_t)blockIdx.x * blockDim.y + threadIdx.y) * a.cols;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int i = 0; i < kLaneVals; ++i) {
+        const uint32_t c = chunk_col<VEC>(base[k], lane, i);
+        if (c < a.cols) p[c] = dw[k][i];
+      }
+  }
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void back_ld(const NormBackArgs& a, uint64_t row, uint32_t base,
+                                        int lane, float* dy, float* h) {
+  ld_chunk<DT, VEC>(row_of<DT>(a.dy, row), base, a.cols, lane, dy);
+  if (a.h8.codes)
+    ld_chunk_q8<VEC>(a.h8, row, base, a.cols, lane, h);
+  else
+    ld_chunk<DT, VEC>(row_of<DT>(a.h, row), base, a.cols, lane, h);
 }
 
 // Wide rows, dx: one block a row, read twice.
@@ -251,7 +319,12 @@ __global__ void __launch_bounds__(kWideThreads)
       ld_chunk<DT, VEC>(a.weight, (uint32_t)base, a.cols, lane, w);
 #pragma unroll
       for (int i = 0; i < kLaneVals; ++i) t[i] *= w[i], n[i] *= rstd;
-      back_st<DT, VEC>(a, row, (uint32_t)base, lane, t, n, rstd, c);
+      Raw<DT, VEC> res;
+      if (a.dres.p)
+        res.load(row_of<DT>(a.dres, row), (uint32_t)base, a.cols, lane);
+      else
+        res.clear();
+      back_st<DT, VEC>(a, row, (uint32_t)base, lane, t, n, res, rstd, c);
     }
   }
 }
@@ -259,11 +332,11 @@ __global__ void __launch_bounds__(kWideThreads)
 // Wide rows, dweight partials: warp (blockIdx.x, warp) takes one chunk of
 // columns, blockIdx.y every gridDim.y-th row.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kBlock)
     k_rms_norm_back_wide_dw(const __grid_constant__ NormBackArgs a) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const uint64_t base = ((uint64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kChunk;
+  const uint64_t base = ((uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5)) * kChunk;
   if (base >= a.cols) return;
   float dw[kLaneVals] = {0.0f};
   for (uint64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
@@ -281,23 +354,25 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// dweight = sum of the partial rows: block (32 columns, 8 row classes), each
+// dweight = sum of the partial rows: block (32 columns, 32 row classes), each
 // class in order, then the classes in order.
 template <int DW>
-__global__ void __launch_bounds__(256) k_norm_dw(const float* partial, uint32_t parts,
-                                                 uint32_t cols, void* dweight) {
+__global__ void __launch_bounds__(1024) k_norm_dw(const float* partial, uint32_t parts,
+                                                  uint32_t cols, void* dweight) {
   pdl_enter();
-  __shared__ float sum[8][32];
+  __shared__ float sum[32][33];
   const uint64_t c = (uint64_t)blockIdx.x * 32 + threadIdx.x;
   float s = 0.0f;
-  if (c < cols)
-    for (uint32_t k = threadIdx.y; k < parts; k += 8) s += partial[(uint64_t)k * cols + c];
+  if (c < cols) {
+#pragma unroll 4
+    for (uint32_t k = threadIdx.y; k < parts; k += 32) s += partial[(uint64_t)k * cols + c];
+  }
   sum[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && c < cols) {
     s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += sum[k][threadIdx.x];
+    for (int k = 0; k < 32; ++k) s += sum[k][threadIdx.x];
     if constexpr (DW == CR_BF16)
       static_cast<uint16_t*>(dweight)[c] = (uint16_t)ffn_bf16x2(s, 0.0f);
     else
@@ -306,18 +381,20 @@ __global__ void __launch_bounds__(256) k_norm_dw(const float* partial, uint32_t 
 }
 
 struct RowShape {
-  int v;          // chunks per warp; 0: wide
+  int v;           // chunks per warp; 0: wide
   unsigned warps;  // per row
-  unsigned rows;   // per block
+  unsigned rows;   // per block, at most the matrix's
 };
 
-// One chunk a warp up to 8 warps, then 2 and 4 chunks; wide rows 32 warps.
-RowShape row_shape(uint32_t cols) {
+// One chunk a warp up to 16 warps, then two; wide rows 32 warps.  Short rows
+// share a block of about 256 threads.
+RowShape row_shape(uint64_t rows, uint32_t cols) {
   const uint32_t chunks = (uint32_t)(((uint64_t)cols + kChunk - 1) / kChunk);
   if (cols > kWideFrom) return {0, kMaxWarps, 1};
-  const int v = chunks <= 8 ? 1 : chunks <= 16 ? 2 : 4;
+  const int v = chunks <= kRowThreads / 32 ? 1 : 2;
   const unsigned warps = (chunks + v - 1) / v;
-  return {v, warps, (kRowThreads / 32) / warps};
+  const unsigned fit = std::max(8 / warps, 1u);
+  return {v, warps, (unsigned)std::min<uint64_t>(fit, std::max<uint64_t>(rows, 1))};
 }
 
 template <typename... KArgs, typename... Args>
@@ -335,35 +412,86 @@ cudaError_t launch2(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int DT, bool VEC>
-cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.cols);
-  uint64_t g = (a.rows + r.rows - 1) / r.rows;
-  if (g > (1u << 30)) g = 1u << 30;
-  const dim3 grid((unsigned)g), block(r.warps * 32, r.rows);
-  switch (r.v) {
-    case 1: return launch2(k_rms_norm<DT, 1, VEC>, grid, block, s, a);
-    case 2: return launch2(k_rms_norm<DT, 2, VEC>, grid, block, s, a);
-    case 4: return launch2(k_rms_norm<DT, 4, VEC>, grid, block, s, a);
-    default: return launch2(k_rms_norm<DT, 0, VEC>, grid, block, s, a);
+// Blocks of `threads` that all SMs hold at once (cached: the query costs
+// microseconds).
+cudaError_t resident_blocks(const void* kernel, int threads, unsigned* blocks) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int>, unsigned> cache;
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const auto key = std::make_tuple(kernel, threads, dev);
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = cache.find(key);
+    if (it != cache.end()) {
+      *blocks = it->second;
+      return cudaSuccess;
+    }
   }
+  if ((e = sm_count(&sms)) != cudaSuccess) return e;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+  if (e != cudaSuccess) return e;
+  *blocks = (unsigned)(sms * std::max(per_sm, 1));
+  std::lock_guard<std::mutex> lock(mu);
+  cache[key] = *blocks;
+  return cudaSuccess;
+}
+
+// Blocks of r for `rows` rows: at most what the SMs hold at once.
+template <typename K>
+cudaError_t row_grid(K kernel, const RowShape& r, uint64_t rows, unsigned* grid) {
+  unsigned most = 0;
+  const cudaError_t e = resident_blocks(reinterpret_cast<const void*>(kernel), r.warps * 32 * r.rows, &most);
+  *grid = (unsigned)std::min<uint64_t>((rows + r.rows - 1) / r.rows, most);
+  return e;
+}
+
+template <int DT, int V, bool VEC>
+cudaError_t norm_run(const NormArgs& a, const RowShape& r, cudaStream_t s) {
+  unsigned grid = 0;
+  const cudaError_t e = row_grid(k_rms_norm<DT, V, VEC>, r, a.rows, &grid);
+  if (e != cudaSuccess) return e;
+  return launch2(k_rms_norm<DT, V, VEC>, dim3(grid), dim3(r.warps * 32, r.rows), s, a);
 }
 
 template <int DT, bool VEC>
-cudaError_t back_dispatch(const NormBackArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.cols);
-  const dim3 grid(a.parts), block(r.warps * 32);
+cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
+  const RowShape r = row_shape(a.rows, a.cols);
   switch (r.v) {
-    case 1: return launch2(k_rms_norm_back<DT, 1, VEC>, grid, block, s, a);
-    case 2: return launch2(k_rms_norm_back<DT, 2, VEC>, grid, block, s, a);
-    case 4: return launch2(k_rms_norm_back<DT, 4, VEC>, grid, block, s, a);
+    case 1: return norm_run<DT, 1, VEC>(a, r, s);
+    case 2: return norm_run<DT, 2, VEC>(a, r, s);
+    default: break;
+  }
+  const unsigned g = (unsigned)std::min<uint64_t>(a.rows, 1u << 30);
+  return launch2(k_rms_norm_wide<DT, VEC>, dim3(g), dim3(kWideThreads), s, a);
+}
+
+template <int DT, int V, bool VEC>
+cudaError_t back_run(NormBackArgs& a, const RowShape& r, cudaStream_t s) {
+  void (*kernel)(const NormBackArgs) =
+      a.h8.codes ? k_rms_norm_back<DT, V, VEC, true> : k_rms_norm_back<DT, V, VEC, false>;
+  unsigned grid = 0;
+  const cudaError_t e = row_grid(kernel, r, a.rows, &grid);
+  if (e != cudaSuccess) return e;
+  grid = std::min(std::max(grid, 1u), kBackBlocks);  // no rows: one block writes zeros
+  a.parts = grid * r.rows;
+  return launch2(kernel, dim3(grid), dim3(r.warps * 32, r.rows), s, a);
+}
+
+template <int DT, bool VEC>
+cudaError_t back_dispatch(NormBackArgs& a, cudaStream_t s) {
+  const RowShape r = row_shape(a.rows, a.cols);
+  const dim3 block(kWideThreads);
+  switch (r.v) {
+    case 1: return back_run<DT, 1, VEC>(a, r, s);
+    case 2: return back_run<DT, 2, VEC>(a, r, s);
     default: break;
   }
   // dweight first: dx may be written over dy or h
   if (a.partial) {
-    const unsigned gx = (a.cols / kChunk + 1 + kRowThreads / 32 - 1) / (kRowThreads / 32);
-    cudaError_t e = launch2(k_rms_norm_back_wide_dw<DT, VEC>, dim3(gx, a.parts), dim3(kRowThreads),
-                            s, a);
+    const unsigned gx = (a.cols / kChunk + 1 + kBlock / 32 - 1) / (kBlock / 32);
+    cudaError_t e = launch2(k_rms_norm_back_wide_dw<DT, VEC>, dim3(gx, a.parts), dim3(kBlock), s, a);
     if (e != cudaSuccess || !a.dx.p) return e;
   }
   const unsigned g = (unsigned)std::min<uint64_t>(a.rows, 1u << 30);
@@ -378,19 +506,22 @@ cudaError_t launch_rms_norm(cr_dtype d, const NormArgs& a, bool vec, cudaStream_
 }
 
 uint32_t norm_back_parts(uint64_t rows, uint32_t cols) {
-  const uint32_t most = cols > kWideFrom ? 64 : 608;  // 4 blocks on each of 152 SMs
-  return (uint32_t)std::min<uint64_t>(rows ? rows : 1, most);
+  const RowShape r = row_shape(rows, cols);
+  if (r.v == 0) return (uint32_t)std::min<uint64_t>(std::max<uint64_t>(rows, 1), 64);
+  const uint64_t blocks = std::max<uint64_t>((rows + r.rows - 1) / r.rows, 1);
+  return (uint32_t)std::min<uint64_t>(blocks, kBackBlocks) * r.rows;
 }
 
-cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, const NormBackArgs& a, bool vec,
+cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, NormBackArgs a, bool vec,
                                  cudaStream_t s) {
+  a.parts = norm_back_parts(a.rows, a.cols);
   cudaError_t e;
   if (d == CR_BF16)
     e = vec ? back_dispatch<CR_BF16, true>(a, s) : back_dispatch<CR_BF16, false>(a, s);
   else
     e = vec ? back_dispatch<CR_F32, true>(a, s) : back_dispatch<CR_F32, false>(a, s);
   if (e != cudaSuccess || !a.partial) return e;
-  const dim3 grid((a.cols + 31) / 32), block(32, 8);
+  const dim3 grid((a.cols + 31) / 32), block(32, 32);
   if (dw == CR_BF16)
     return launch2(k_norm_dw<CR_BF16>, grid, block, s, (const float*)a.partial, a.parts, a.cols, a.dweight);
   return launch2(k_norm_dw<CR_F32>, grid, block, s, (const float*)a.partial, a.parts, a.cols, a.dweight);
