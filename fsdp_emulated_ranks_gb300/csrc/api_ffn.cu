@@ -26,8 +26,9 @@ struct Arg {
 struct Args {
   Arg list[20];
   int n = 0;
-  bool vec16 = true;  // every bf16/fp32 pointer and pitch is a multiple of 16 bytes
-  bool vec8 = true;   // every code pointer and pitch is a multiple of 8 bytes
+  bool vec16 = true;  // every bf16/fp32 pointer and pitch, and every code pointer and
+                      // pitch, is a multiple of 16 bytes
+  bool vec32 = true;  // every bf16/fp32 pointer and pitch is a multiple of 32 bytes
   cr_status status = CR_OK;
 
   void fails(cr_status st) {
@@ -54,17 +55,21 @@ struct Args {
   void matrix(const char* name, const void* p, uint64_t rows, uint64_t cols, uint64_t ld, size_t es,
               bool out) {
     raw(name, p, rows, cols, ld, es, out);
-    if (rows && cols) vec16 = vec16 && aligned(p, 16) && (rows == 1 || ld * es % 16 == 0);
+    if (status != CR_OK || rows == 0 || cols == 0) return;
+    const uint64_t bits = reinterpret_cast<uintptr_t>(p) | (rows == 1 ? 0 : ld * es);
+    vec16 = vec16 && bits % 16 == 0;
+    vec32 = vec32 && bits % 32 == 0;
   }
 
   void q8(const char* name, const cr_q8* q, uint64_t rows, uint64_t cols, bool out) {
     if (status != CR_OK || rows == 0 || cols == 0) return;
     raw(name, q->codes, rows, cols, q->ld, 1, out);
     raw(name, q->scales, rows, (cols + CR_Q8_GROUP - 1) / CR_Q8_GROUP, q->lds, 4, out);
-    vec8 = vec8 && aligned(q->codes, 8) && (rows == 1 || q->ld % 8 == 0);
+    vec16 = vec16 && aligned(q->codes, 16) && (rows == 1 || q->ld % 16 == 0);
   }
 
-  bool vec() const { return vec16 && vec8; }
+  // The accesses the elementwise kernels may use (ffn_internal.cuh).
+  int vec() const { return !vec16 ? 0 : vec32 ? 2 : 1; }
 
   // Whether some row of x and some row of y share a byte.
   static bool meet(const Arg& x, const Arg& y) {
@@ -154,18 +159,23 @@ cr_status check_workspace(const void* p, size_t have, size_t need) {
 
 uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
-// bf16 elements of a workspace matrix whose rows start on 16-byte boundaries.
-uint64_t padded(uint64_t rows, uint64_t cols) { return rows * round_up(cols, 8); }
+// Row stride, and elements, of a bf16 workspace matrix: rows a multiple of 32
+// bytes apart.
+uint64_t padded_ld(uint64_t cols) { return round_up(cols, 16); }
+uint64_t padded(uint64_t rows, uint64_t cols) { return rows * padded_ld(cols); }
+
+// `vec`, for a call that reads or writes a workspace matrix at p too (the
+// workspace itself is 16-byte aligned).
+int vec_with(int vec, const void* p) { return vec == 2 && !aligned(p, 32) ? 1 : vec; }
 
 // TMA reads operands whose rows start on 16-byte boundaries; any other is
 // copied to `ws` first.
-cudaError_t operand(Mat* m, uint64_t rows, uint64_t cols, uint16_t* ws, cudaStream_t s) {
-  if (!m->p || rows == 0 || cols == 0) return cudaSuccess;
-  if (aligned(m->p, 16) && (rows == 1 || m->ld % 8 == 0)) return cudaSuccess;
-  const Mat copy = {ws, round_up(cols, 8)};
-  const cudaError_t e = launch_copy_bf16(*m, copy, rows, (uint32_t)cols, s);
+void operand(CopyBf16* copies, Mat* m, uint64_t rows, uint64_t cols, uint16_t* ws) {
+  if (!m->p || rows == 0 || cols == 0) return;
+  if (aligned(m->p, 16) && (rows == 1 || m->ld % 8 == 0)) return;
+  const Mat copy = {ws, padded_ld(cols)};
+  add_copy(copies, *m, copy, rows, (uint32_t)cols);
   *m = copy;
-  return e;
 }
 
 }  // namespace
@@ -339,14 +349,16 @@ cr_status cr_glu(const void* x, size_t ldx, const void* wg, size_t ldwg, const v
     Args w;
     w.matrix("wg", wg, ffn, dim, ldwg, 2, false);
     w.matrix("wu", wu, ffn, dim, ldwu, 2, false);
-    return launched(launch_glu_few(act, k, w.vec16, s), "cr_glu");
+    return launched(launch_glu_few(act, k, w.vec(), s), "cr_glu");
   }
   uint16_t* ws = static_cast<uint16_t*>(workspace);
-  cudaError_t e = operand(&k.x, tokens, dim, ws, s);
+  CopyBf16 copies = {};
+  operand(&copies, &k.x, tokens, dim, ws);
   ws += padded(tokens, dim);
-  if (e == cudaSuccess) e = operand(&k.wg, ffn, dim, ws, s);
+  operand(&copies, &k.wg, ffn, dim, ws);
   ws += padded(ffn, dim);
-  if (e == cudaSuccess) e = operand(&k.wu, ffn, dim, ws, s);
+  operand(&copies, &k.wu, ffn, dim, ws);
+  cudaError_t e = launch_copy_bf16(copies, s);
   if (e == cudaSuccess) e = launch_glu(act, k, s);
   return launched(e, "cr_glu");
 }
@@ -379,7 +391,7 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr
   a.q8("g8", g8, tokens, ffn, false);
   a.q8("u8", u8, tokens, ffn, false);
   if (a_out) a.matrix("a", a_out, tokens, ffn, lda, 2, true);
-  const bool act_vec = a.vec();
+  const int act_vec = a.vec();
   Args xa;
   if (dw && x8) {
     a.q8("x8", x8, tokens, dim, false);
@@ -399,13 +411,13 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr
 
   const cudaStream_t s = stream_of(stream);
   uint16_t* ws = static_cast<uint16_t*>(workspace);
-  const Mat dg = {ws, round_up(ffn, 8)};
-  const Mat du = {ws + padded(tokens, ffn), round_up(ffn, 8)};
+  const Mat dg = {ws, padded_ld(ffn)};
+  const Mat du = {ws + padded(tokens, ffn), padded_ld(ffn)};
   cudaError_t e = cudaSuccess;
   if (tokens && ffn) {
     ActBackArgs k = {mat(da, ldda), dg, du, mat(a_out, lda), q8_of(g8), q8_of(u8), tokens, (uint32_t)ffn};
     if (!dx && !dw) k.dg = k.du = Mat{nullptr, 0};
-    if (k.dg.p || k.a.p) e = launch_act_back(act, k, act_vec, s);
+    if (k.dg.p || k.a.p) e = launch_act_back(act, k, vec_with(act_vec, ws), s);
     if (e != cudaSuccess) return cuda_fail(e, "cr_glu_backward: activation");
   }
   if (dim == 0 || (!dw && !(dx && tokens))) return ok();
@@ -414,17 +426,19 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr
   k.x = mat(x, ldx);
   k.wg = mat(wg, ldwg), k.wu = mat(wu, ldwu);
   ws += 2 * padded(tokens, ffn);
+  CopyBf16 copies = {};
   if (dw && x8 && tokens) {
-    k.x = Mat{ws, round_up(dim, 8)};
-    k.x_lo = Mat{ws + padded(tokens, dim), round_up(dim, 8)};
-    e = launch_q8_split(q8_of(x8), k.x, k.x_lo, tokens, (uint32_t)dim, xa.vec(), s);
+    k.x = Mat{ws, padded_ld(dim)};
+    k.x_lo = Mat{ws + padded(tokens, dim), padded_ld(dim)};
+    e = launch_q8_split(q8_of(x8), k.x, k.x_lo, tokens, (uint32_t)dim, vec_with(xa.vec(), ws), s);
   } else if (dw) {
-    e = operand(&k.x, tokens, dim, ws, s);
+    operand(&copies, &k.x, tokens, dim, ws);
   }
   ws += 2 * padded(tokens, dim);
-  if (dx && e == cudaSuccess) e = operand(&k.wg, ffn, dim, ws, s);
+  if (dx) operand(&copies, &k.wg, ffn, dim, ws);
   ws += padded(ffn, dim);
-  if (dx && e == cudaSuccess) e = operand(&k.wu, ffn, dim, ws, s);
+  if (dx) operand(&copies, &k.wu, ffn, dim, ws);
+  if (e == cudaSuccess) e = launch_copy_bf16(copies, s);
   if (e != cudaSuccess) return cuda_fail(e, "cr_glu_backward: operands");
   k.dx = mat(tokens ? dx : nullptr, lddx);
   k.dwg = ffn ? dwg : nullptr;

@@ -1,12 +1,15 @@
 // ffn_internal.cuh -- types and device helpers shared by the feed-forward
 // operators (include/cr_ffn.h): strided matrices, 8-bit matrices, and the
-// 256-column chunk every elementwise kernel works in.
+// chunk of a row every elementwise kernel works in.
 //
-// A warp handles 256 consecutive columns of a row, 8 values a lane: two of
-// the 8-bit form's 128-column groups.  Where pointers and row strides allow
-// it (VEC) a lane owns 8 consecutive columns (16 bytes of bf16, 8 codes);
-// otherwise lane l owns columns l, l + 32, ..., so that scalar accesses of a
-// warp still cover consecutive addresses.
+// A warp handles a chunk of consecutive columns.  Where pointers and row
+// strides allow it (VEC: 1 for 16-byte vectors, 2 for 32-byte ones) a lane
+// owns 16 consecutive columns, 512 a chunk; otherwise (VEC 0) lane l owns
+// columns l, l + 32, ... of 256, so that a warp's scalar accesses still cover
+// consecutive addresses.  These kernels are bound by instructions before they
+// are by memory (with 8 columns a lane the norm issued 47 a value and
+// reached 73 % of its issue slots at 4.7 TB/s): hence the wide lanes, which
+// share addresses, reductions and divisions among more values.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -17,8 +20,9 @@
 
 namespace cr {
 
-constexpr int kChunk = 256;   // columns a warp handles at a time
-constexpr int kLaneVals = 8;  // values per lane of a chunk
+// Values of a lane, and columns of a chunk.
+__host__ __device__ constexpr int lane_vals(int vec) { return vec ? 16 : 8; }
+__host__ __device__ constexpr uint32_t chunk_cols(int vec) { return 32 * lane_vals(vec); }
 constexpr float kQ8Max = 448.0f;
 constexpr float kQ8InvMax = 1.0f / 448.0f;
 constexpr float kQ8Tiny = 1.17549435e-38f;  // 2^-126
@@ -80,29 +84,38 @@ struct GluBackArgs {
   uint32_t tokens, dim, ffn;
 };
 
-// vec: every pointer and row stride of the call allows the VEC accesses.
-cudaError_t launch_rms_norm(cr_dtype d, const NormArgs& a, bool vec, cudaStream_t s);
+// vec: the accesses every pointer and row stride of the call allows, 0 to 2.
+cudaError_t launch_rms_norm(cr_dtype d, const NormArgs& a, int vec, cudaStream_t s);
 // Row partials the backward pass writes for its dweight, at most.
 uint32_t norm_back_parts(uint64_t rows, uint32_t cols);
-cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, NormBackArgs a, bool vec,
+cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, NormBackArgs a, int vec,
                                  cudaStream_t s);
 cudaError_t launch_q8_store(cr_dtype d, const Mat& x, const Q8& q, uint64_t rows, uint32_t cols,
-                            bool vec, cudaStream_t s);
+                            int vec, cudaStream_t s);
 cudaError_t launch_q8_load(cr_dtype d, const Q8& q, const Mat& x, uint64_t rows, uint32_t cols,
-                           bool vec, cudaStream_t s);
+                           int vec, cudaStream_t s);
 // The values q stands for as bf16 hi + lo (lo: what the rounding of hi left).
 cudaError_t launch_q8_split(const Q8& q, const Mat& hi, const Mat& lo, uint64_t rows, uint32_t cols,
-                            bool vec, cudaStream_t s);
-// dst = src, rows x cols bf16 at any alignment.
-cudaError_t launch_copy_bf16(const Mat& src, const Mat& dst, uint64_t rows, uint32_t cols,
-                             cudaStream_t s);
-cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, bool vec, cudaStream_t s);
+                            int vec, cudaStream_t s);
+// dst = src for up to three bf16 matrices at any alignment, in one launch.
+struct CopyBf16 {
+  struct One {
+    Mat src, dst;
+    uint64_t chunks;
+    FastDiv per_row;
+    uint32_t cols;
+  } one[3];
+  int n;
+};
+void add_copy(CopyBf16* c, const Mat& src, const Mat& dst, uint64_t rows, uint32_t cols);
+cudaError_t launch_copy_bf16(const CopyBf16& c, cudaStream_t s);
+cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, int vec, cudaStream_t s);
 cudaError_t launch_glu(cr_act act, const GluArgs& a, cudaStream_t s);
 // Whether the block's call is one for k_glu_few.cu: few tokens, whose x fits
 // in shared memory, and no checkpoints (keeps).  Operands at any alignment;
-// vec: 16-byte aligned rows of both weights.
+// vec: the accesses both weights allow.
 bool glu_few(uint64_t tokens, uint64_t dim, bool keeps);
-cudaError_t launch_glu_few(cr_act act, const GluArgs& a, bool vec, cudaStream_t s);
+cudaError_t launch_glu_few(cr_act act, const GluArgs& a, int vec, cudaStream_t s);
 cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& a, cudaStream_t s);
 // Reads (and clears) the word a block sets that gave up a wait.
 cudaError_t glu_wait_word(bool clear, unsigned int* word);
@@ -137,60 +150,110 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
   return f;
 }
 
-__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __int_as_float(0x7f800000); }
-
-__device__ __forceinline__ float q8_magnitude(float v) { return finite(v) ? fabsf(v) : 0.0f; }
+constexpr float kFloatMax = 3.402823466e38f;
 
 __device__ __forceinline__ float q8_scale(float m) { return fmaxf(m * kQ8InvMax, kQ8Tiny); }
 
-// A value that is not finite becomes NaN, which e4m3x2 keeps.
-__device__ __forceinline__ float q8_scaled(float v, float inv) {
-  return finite(v) ? v * inv : __int_as_float(0x7fc00000);
+// Largest finite magnitude of a group held by several lanes, and the values
+// with infinities made NaN.  `reduce` takes a lane's maximum to the group's;
+// the whole warp calls.  fmaxf passes NaN over, so only an infinity needs
+// the second look, and NaN times anything stays NaN, which the codes keep.
+template <int N, typename Reduce>
+__device__ __forceinline__ float q8_magnitude(float* v, Reduce reduce) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
+  m = reduce(m);
+  if (__any_sync(~0u, m > kFloatMax)) {
+    m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (fabsf(v[i]) > kFloatMax) v[i] = __int_as_float(0x7fc00000);
+      m = fmaxf(m, fabsf(v[i]));
+    }
+    m = reduce(m);
+  }
+  return m;
 }
 
 // ---- chunks -----------------------------------------------------------------------
 
-template <bool VEC>
+template <int VEC>
 __device__ __forceinline__ uint32_t chunk_col(uint32_t base, int lane, int i) {
-  return VEC ? base + lane * kLaneVals + i : base + i * 32 + lane;
+  return VEC ? base + lane * lane_vals(VEC) + i : base + i * 32 + lane;
+}
+
+__device__ __forceinline__ void ld_words8(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+
+__device__ __forceinline__ void st_words8(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// 8 words at p, 32-byte (VEC 2) or 16-byte aligned.
+template <int VEC>
+__device__ __forceinline__ void ld_words(const void* p, uint32_t* w) {
+  if constexpr (VEC == 2) {
+    ld_words8(p, w);
+  } else {
+    const uint4 q = static_cast<const uint4*>(p)[0], r = static_cast<const uint4*>(p)[1];
+    w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    w[4] = r.x, w[5] = r.y, w[6] = r.z, w[7] = r.w;
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void st_words(void* p, const uint32_t* w) {
+  if constexpr (VEC == 2) {
+    st_words8(p, w);
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 // A chunk as loaded, before it is widened to fp32: what a kernel that loads
 // ahead keeps.  Values of columns past `cols` are zero.
-template <int DT, bool VEC>
+template <int DT, int VEC>
 struct Raw {
-  static constexpr int kWords = DT == CR_BF16 ? (VEC ? 4 : 8) : 8;
+  static constexpr int kVals = lane_vals(VEC);
+  static constexpr int kWords = DT == CR_BF16 && VEC ? kVals / 2 : kVals;
   uint32_t w[kWords];
 
   // `row` points at the row's column 0.
   __device__ __forceinline__ void load(const void* row, uint32_t base, uint32_t cols, int lane) {
     const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
+    const uint16_t* half = static_cast<const uint16_t*>(row) + c0;
+    const uint32_t* word = static_cast<const uint32_t*>(row) + c0;
     if constexpr (VEC) {
-      if (c0 + kLaneVals <= cols) {
+      if (c0 + kVals <= cols) {
         if constexpr (DT == CR_BF16) {
-          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c0);
-          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+          ld_words<VEC>(half, w);
         } else {
-          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + c0);
-          const uint4 q = p[0], r = p[1];
-          w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-          w[4] = r.x, w[5] = r.y, w[6] = r.z, w[7] = r.w;
+          ld_words<VEC>(word, w);
+          ld_words<VEC>(word + 8, w + 8);
         }
         return;
       }
     }
+    clear();
+    if (VEC && c0 >= cols) return;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) {
-      const uint32_t c = chunk_col<VEC>(base, lane, i);
-      if (c >= cols) continue;
+    for (int i = 0; i < kVals; ++i) {
+      const int at = VEC ? i : i * 32;
+      if (c0 + at >= cols) continue;
       if constexpr (DT == CR_F32)
-        w[i] = static_cast<const uint32_t*>(row)[c];
+        w[i] = word[at];
       else if constexpr (VEC)
-        w[i / 2] |= (uint32_t) static_cast<const uint16_t*>(row)[c] << (16 * (i & 1));
+        w[i / 2] |= (uint32_t)half[at] << (16 * (i & 1));
       else
-        w[i] = (uint32_t) static_cast<const uint16_t*>(row)[c] << 16;
+        w[i] = (uint32_t)half[at] << 16;
     }
   }
 
@@ -207,175 +270,175 @@ struct Raw {
   }
 };
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void ld_chunk(const void* row, uint32_t base, uint32_t cols, int lane,
-                                         float* v) {
-  Raw<DT, VEC> r;
-  r.load(row, base, cols, lane);
-#pragma unroll
-  for (int i = 0; i < kLaneVals; ++i) v[i] = r.value(i);
-}
-
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __device__ __forceinline__ void st_chunk(void* row, uint32_t base, uint32_t cols, int lane,
                                          const float* v) {
+  constexpr int vals = lane_vals(VEC);
   const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
-  if (VEC && c0 + kLaneVals <= cols) {
-    if constexpr (DT == CR_BF16) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + c0) =
-          make_uint4(ffn_bf16x2(v[0], v[1]), ffn_bf16x2(v[2], v[3]), ffn_bf16x2(v[4], v[5]),
-                     ffn_bf16x2(v[6], v[7]));
-    } else {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + c0);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-    return;
-  }
+  uint16_t* half = static_cast<uint16_t*>(row) + c0;
+  float* word = static_cast<float*>(row) + c0;
+  if constexpr (VEC) {
+    if (c0 + vals <= cols) {
+      uint32_t w[8];
+      if constexpr (DT == CR_BF16) {
 #pragma unroll
-  for (int i = 0; i < kLaneVals; ++i) {
-    const uint32_t c = chunk_col<VEC>(base, lane, i);
-    if (c >= cols) continue;
+        for (int i = 0; i < 8; ++i) w[i] = ffn_bf16x2(v[2 * i], v[2 * i + 1]);
+        st_words<VEC>(half, w);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+          st_words<VEC>(word + 8 * h, w);
+        }
+      }
+      return;
+    }
+  }
+  if (VEC && c0 >= cols) return;
+#pragma unroll
+  for (int i = 0; i < vals; ++i) {
+    const int at = VEC ? i : i * 32;
+    if (c0 + at >= cols) continue;
     if constexpr (DT == CR_BF16)
-      static_cast<uint16_t*>(row)[c] = (uint16_t)ffn_bf16x2(v[i], 0.0f);
+      half[at] = (uint16_t)ffn_bf16x2(v[i], 0.0f);
     else
-      static_cast<float*>(row)[c] = v[i];
+      word[at] = v[i];
   }
 }
 
-// 8-bit form of a chunk: every lane of the warp calls it.
-template <bool VEC>
+// 8-bit form of a chunk: every lane of the warp calls it.  v may be changed.
+template <int VEC>
 __device__ __forceinline__ void st_chunk_q8(const Q8& q, uint64_t row, uint32_t base,
-                                            uint32_t cols, int lane, const float* v) {
-  uint8_t* codes = q.codes + row * q.ld;
-  float* scales = q.scales + row * q.lds;
-  const uint32_t group = base / CR_Q8_GROUP;
-  if constexpr (VEC) {  // lanes 0-15 hold one group, 16-31 the next
-    float m = 0.0f;
+                                            uint32_t cols, int lane, float* v) {
+  const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
+  uint8_t* codes = q.codes + row * q.ld + c0;
+  float* scales = q.scales + row * q.lds + base / CR_Q8_GROUP;
+  if constexpr (VEC) {  // 8 lanes hold a group
+    const float m = q8_magnitude<16>(v, [](float x) {
 #pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) m = fmaxf(m, q8_magnitude(v[i]));
-#pragma unroll
-    for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+      for (int o = 4; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+      return x;
+    });
     const float s = q8_scale(m), inv = 1.0f / s;
-    const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
-    if ((lane & 15) == 0 && c0 < cols) scales[group + (lane >> 4)] = s;
+    if (c0 >= cols) return;
+    if ((lane & 7) == 0) scales[lane >> 3] = s;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w[i] = e4m3x2(q8_scaled(v[2 * i], inv), q8_scaled(v[2 * i + 1], inv));
-    const uint32_t lo = w[0] | w[1] << 16, hi = w[2] | w[3] << 16;
-    if (c0 + kLaneVals <= cols) {
-      *reinterpret_cast<uint2*>(codes + c0) = make_uint2(lo, hi);
+      w[i] = e4m3x2(v[4 * i] * inv, v[4 * i + 1] * inv) |
+             e4m3x2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+    if (c0 + 16 <= cols) {
+      *reinterpret_cast<uint4*>(codes) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i)
-        if (c0 + i < cols) codes[c0 + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+      for (int i = 0; i < 16; ++i)
+        if (c0 + i < cols) codes[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
     }
   } else {  // values 0-3 of every lane are one group, 4-7 the next
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float m = 0.0f;
+      const float m = q8_magnitude<4>(v + 4 * h, [](float x) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = fmaxf(m, q8_magnitude(v[4 * h + i]));
-#pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+        return x;
+      });
       const float s = q8_scale(m), inv = 1.0f / s;
-      if (lane == 0 && base + h * CR_Q8_GROUP < cols) scales[group + h] = s;
+      if (lane == 0 && base + h * CR_Q8_GROUP < cols) scales[h] = s;
 #pragma unroll
-      for (int i = 4 * h; i < 4 * h + 4; ++i) {
-        const uint32_t c = chunk_col<VEC>(base, lane, i);
-        if (c < cols) codes[c] = (uint8_t)e4m3x2(q8_scaled(v[i], inv), 0.0f);
-      }
+      for (int i = 4 * h; i < 4 * h + 4; ++i)
+        if (c0 + 32 * i < cols) codes[32 * i] = (uint8_t)e4m3x2(v[i] * inv, 0.0f);
     }
   }
 }
 
-// A chunk of an 8-bit matrix as loaded.  VEC: 8 codes and the one scale of the
-// lane's half; otherwise a code a word and both scales.
-template <bool VEC>
+// A chunk of an 8-bit matrix as loaded.  VEC: 16 codes and the one scale of
+// the lane's group; otherwise a code a word and both scales.
+template <int VEC>
 struct RawQ8 {
-  uint32_t w[VEC ? 2 : 8];
-  float s[VEC ? 1 : 2];
+  static constexpr int kWords = VEC ? 4 : 8, kScales = VEC ? 1 : 2;
+  uint32_t w[kWords];
+  float s[kScales];
 
   __device__ __forceinline__ void load(const Q8& q, uint64_t row, uint32_t base, uint32_t cols,
                                        int lane) {
-    const uint8_t* codes = q.codes + row * q.ld;
-    const float* scales = q.scales + row * q.lds + base / CR_Q8_GROUP;
     const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
+    const uint8_t* codes = q.codes + row * q.ld + c0;
+    const float* scales = q.scales + row * q.lds + base / CR_Q8_GROUP;
+    clear();
     if constexpr (VEC) {
-      s[0] = c0 < cols ? scales[lane >> 4] : 0.0f;
-      w[0] = w[1] = 0;
-      if (c0 + kLaneVals <= cols) {
-        const uint2 t = *reinterpret_cast<const uint2*>(codes + c0);
-        w[0] = t.x, w[1] = t.y;
+      if (c0 >= cols) return;
+      s[0] = scales[lane >> 3];
+      if (c0 + 16 <= cols) {
+        const uint4 t = *reinterpret_cast<const uint4*>(codes);
+        w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
       } else {
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i)
-          if (c0 + i < cols) w[i >> 2] |= (uint32_t)codes[c0 + i] << (8 * (i & 3));
+        for (int i = 0; i < 16; ++i)
+          if (c0 + i < cols) w[i >> 2] |= (uint32_t)codes[i] << (8 * (i & 3));
       }
     } else {
+      if (base < cols) s[0] = scales[0];
+      if (base + CR_Q8_GROUP < cols) s[1] = scales[1];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) s[h] = base + h * CR_Q8_GROUP < cols ? scales[h] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < kLaneVals; ++i) {
-        const uint32_t c = chunk_col<VEC>(base, lane, i);
-        w[i] = c < cols ? codes[c] : 0u;
-      }
+      for (int i = 0; i < 8; ++i)
+        if (c0 + 32 * i < cols) w[i] = codes[32 * i];
     }
   }
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < (VEC ? 2 : 8); ++i) w[i] = 0;
-    s[0] = s[VEC ? 0 : 1] = 0.0f;
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kScales; ++i) s[i] = 0.0f;
   }
 
   // The values the codes stand for (fp32, not rounded further).
   __device__ __forceinline__ void values(float* v) const {
     if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const float2 f = from_e4m3x2(w[i >> 1] >> (16 * (i & 1)));
         v[2 * i] = f.x * s[0], v[2 * i + 1] = f.y * s[0];
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i) v[i] = from_e4m3x2(w[i]).x * s[i / 4];
+      for (int i = 0; i < 8; ++i) v[i] = from_e4m3x2(w[i]).x * s[i / 4];
     }
   }
 };
 
-template <bool VEC>
-__device__ __forceinline__ void ld_chunk_q8(const Q8& q, uint64_t row, uint32_t base,
-                                            uint32_t cols, int lane, float* v) {
-  RawQ8<VEC> r;
-  r.load(q, row, base, cols, lane);
-  r.values(v);
-}
-
 // ---- the gate's activation -----------------------------------------------------------
 
 // act(g) = g p and act'(g), with p = 1 / (1 + exp(-z)): z = g for SiLU; for
-// GELU 1/2 (1 + tanh t) = 1 / (1 + exp(-2t)), so z = 2t.  exp and the
-// division are the fast ones, within a few fp32 ulps: the results are
-// rounded to bf16 (2^-9) right after.
+// GELU 1/2 (1 + tanh t) = 1 / (1 + exp(-2t)), so z = 2t.  2^x and 1/x are the
+// hardware's approximations, each within 2 fp32 ulps (results below 2^-126
+// become 0): what follows is rounded to bf16 (2^-9).
+__device__ __forceinline__ float logistic(float z) {
+  float e, p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * z));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.0f + e));
+  return p;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_gate(float g) {
-  float z = g;
-  if constexpr (ACT == CR_ACT_GELU) z = 1.5957691216f * (g + 0.044715f * g * g * g);
-  return __fdividef(g, 1.0f + __expf(-z));
+  if constexpr (ACT == CR_ACT_GELU)
+    return g * logistic(g * fmaf(0.0713548163f, g * g, 1.5957691216f));
+  return g * logistic(g);
 }
 
 template <int ACT>
 __device__ __forceinline__ float2 act_gate_slope(float g) {
   float z = g, dz = 1.0f;
   if constexpr (ACT == CR_ACT_GELU) {
-    z = 1.5957691216f * (g + 0.044715f * g * g * g);
-    dz = 1.5957691216f + 0.2140643f * g * g;
+    const float sq = g * g;
+    z = g * fmaf(0.0713548163f, sq, 1.5957691216f);
+    dz = fmaf(0.2140644488f, sq, 1.5957691216f);
   }
-  const float p = __fdividef(1.0f, 1.0f + __expf(-z));
-  const float a = g * p;
-  return make_float2(a, p + a * (1.0f - p) * dz);
+  const float p = logistic(z), a = g * p;
+  const float rest = ACT == CR_ACT_GELU ? (1.0f - p) * dz : 1.0f - p;
+  return make_float2(a, fmaf(a, rest, p));
 }
 
 #endif  // __CUDACC__

@@ -61,23 +61,12 @@ struct TileArgs {
   int width8;                 // the same for the codes
 };
 
-__device__ __forceinline__ void st32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 template <int WORDS>
-__device__ __forceinline__ void st_words(void* p, const uint32_t* w, int width) {
-  if (width == 32) {
+__device__ __forceinline__ void st_run(void* p, const uint32_t* w, int width) {
+  uint32_t* out = static_cast<uint32_t*>(p);
 #pragma unroll
-    for (int i = 0; i < WORDS; i += 8) st32(static_cast<uint32_t*>(p) + i, w + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < WORDS; i += 4)
-      *reinterpret_cast<uint4*>(static_cast<uint32_t*>(p) + i) =
-          make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-  }
+  for (int i = 0; i < WORDS; i += 8)
+    width == 32 ? st_words<2>(out + i, w + i) : st_words<1>(out + i, w + i);
 }
 
 constexpr int kSlab = 32 * 33;  // words of a warp's staging slab
@@ -95,7 +84,7 @@ __device__ __forceinline__ void st_square(T* out, uint64_t ld, uint64_t row0, ui
                                           const uint32_t* w, uint32_t* slab) {
   constexpr int per = 4 / sizeof(T), words = 32 / per;
   if (width && c + 32 <= cols) {
-    if (row0 + lane < rows) st_words<words>(out + (row0 + lane) * ld + c, w, width);
+    if (row0 + lane < rows) st_run<words>(out + (row0 + lane) * ld + c, w, width);
     return;
   }
   __syncwarp();
@@ -126,14 +115,21 @@ __device__ __forceinline__ void st_values(const Mat& m, uint64_t row0, uint32_t 
   }
 }
 
+// Infinities have been made NaN where there are any (`inf`, the same for the
+// whole warp); otherwise none is left to look at.
+__device__ __forceinline__ float code_value(float v, float inv, bool inf) {
+  if (inf && fabsf(v) > kFloatMax) return __int_as_float(0x7fc00000);
+  return v * inv;
+}
+
 __device__ __forceinline__ void st_codes(const Q8& q, uint64_t row0, uint32_t c, uint32_t rows,
                                          uint32_t cols, int width, int lane, const float* v,
-                                         float inv, uint32_t* slab) {
+                                         float inv, bool inf, uint32_t* slab) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    w[i] = e4m3x2(q8_scaled(v[4 * i], inv), q8_scaled(v[4 * i + 1], inv)) |
-           e4m3x2(q8_scaled(v[4 * i + 2], inv), q8_scaled(v[4 * i + 3], inv)) << 16;
+    w[i] = e4m3x2(code_value(v[4 * i], inv, inf), code_value(v[4 * i + 1], inv, inf)) |
+           e4m3x2(code_value(v[4 * i + 2], inv, inf), code_value(v[4 * i + 3], inv, inf)) << 16;
   st_square(q.codes, q.ld, row0, c, rows, cols, width, lane, w, slab);
 }
 
@@ -158,6 +154,37 @@ __device__ __forceinline__ void ld_acc(uint32_t addr, bool any, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = 0.0f;
 }
 
+__device__ __forceinline__ void ld_acc2(uint32_t addr, uint32_t addr2, bool any, float* v, float* v2) {
+  if (any) return tc::tmem_ld32x2(addr, addr2, v, v2);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = v2[i] = 0.0f;
+}
+
+// Largest finite magnitudes of a row's 128 columns of g and of u.  fmaxf
+// passes NaN over; only where some row of the warp holds an infinity
+// (returned) are the columns looked at again.  Columns past the matrix hold
+// zeros, which no magnitude is below.
+__device__ __forceinline__ bool row_magnitudes(uint32_t acc, bool any, float* mg, float* mu) {
+  bool inf = false;
+  for (int look = 0; look < 2; ++look) {
+    *mg = *mu = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < kN / 2; c += 32) {
+      float g[32], u[32];
+      ld_acc2(acc + c, acc + kN / 2 + c, any, g, u);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float x = fabsf(g[i]), y = fabsf(u[i]);
+        *mg = fmaxf(*mg, inf && x > kFloatMax ? 0.0f : x);
+        *mu = fmaxf(*mu, inf && y > kFloatMax ? 0.0f : y);
+      }
+    }
+    if (inf || !__any_sync(~0u, *mg > kFloatMax || *mu > kFloatMax)) break;
+    inf = true;
+  }
+  return inf;
+}
+
 // EPI: the activation (kGlu) or the output's dtype.
 template <int MODE, int EPI>
 __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32_t which,
@@ -171,18 +198,10 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32
   if constexpr (MODE == kGlu) {
     const uint32_t c0 = tn * (kN / 2);
     float inv_g = 0.0f, inv_u = 0.0f;
+    bool inf = false;
     if (a.g8.codes || a.u8.codes) {
-      // columns past the matrix hold zeros, which no magnitude is below
-      float mg = 0.0f, mu = 0.0f;
-#pragma unroll 1
-      for (int c = 0; c < kN / 2; c += 32) {
-        float g[32], u[32];
-        ld_acc(acc + c, any, g);
-        ld_acc(acc + kN / 2 + c, any, u);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          mg = fmaxf(mg, q8_magnitude(g[i])), mu = fmaxf(mu, q8_magnitude(u[i]));
-      }
+      float mg, mu;
+      inf = row_magnitudes(acc, any, &mg, &mu);
       const float sg = q8_scale(mg), su = q8_scale(mu);
       inv_g = 1.0f / sg, inv_u = 1.0f / su;
       if (live && a.g8.codes) a.g8.scales[(row0 + lane) * a.g8.lds + tn] = sg;
@@ -192,12 +211,11 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32
     for (uint32_t c = 0; c < kN / 2 && c0 + c < a.cols; c += 32) {
       float g[32], u[32];
       __syncwarp();  // the last square's stores leave rows past the matrix out
-      ld_acc(acc + c, any, g);
-      ld_acc(acc + kN / 2 + c, any, u);
+      ld_acc2(acc + c, acc + kN / 2 + c, any, g, u);
       if (a.g8.codes)
-        st_codes(a.g8, row0, c0 + c, a.rows, a.cols, a.width8, lane, g, inv_g, slab);
+        st_codes(a.g8, row0, c0 + c, a.rows, a.cols, a.width8, lane, g, inv_g, inf, slab);
       if (a.u8.codes)
-        st_codes(a.u8, row0, c0 + c, a.rows, a.cols, a.width8, lane, u, inv_u, slab);
+        st_codes(a.u8, row0, c0 + c, a.rows, a.cols, a.width8, lane, u, inv_u, inf, slab);
 #pragma unroll
       for (int i = 0; i < 32; ++i) g[i] = act_gate<EPI>(g[i]) * u[i];
       st_values<CR_BF16>(a.out[0], row0, c0 + c, a.rows, a.cols, a.width, lane, g, slab);
@@ -384,17 +402,18 @@ __device__ __forceinline__ void finish_row(const TileArgs& a, uint32_t which, ui
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const Q8& q = k ? a.u8 : a.g8;
-      const float* v = k ? hi : lo;
       if (!q.codes) continue;
-      float m = 0.0f;
+      float v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = fmaxf(m, q8_magnitude(v[i]));
+      for (int i = 0; i < 4; ++i) v[i] = k ? hi[i] : lo[i];
+      const float m = q8_magnitude<4>(v, [](float x) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+        return x;
+      });
       const float s = q8_scale(m), inv = 1.0f / s;
       if (lane == 0) q.scales[row * q.lds + tn] = s;
-      const uint32_t w = e4m3x2(q8_scaled(v[0], inv), q8_scaled(v[1], inv)) |
-                         e4m3x2(q8_scaled(v[2], inv), q8_scaled(v[3], inv)) << 16;
+      const uint32_t w = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
       uint8_t* codes = q.codes + row * q.ld + c;
       if (a.width8 && c + 4 <= a.cols) {
         *reinterpret_cast<uint32_t*>(codes) = w;

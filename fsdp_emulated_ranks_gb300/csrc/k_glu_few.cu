@@ -3,7 +3,7 @@
 // bytes and by how many of them are in flight.
 //
 // A warp takes one hidden unit at a time: rows f of Wg and of Wu, streamed in
-// 256-column chunks, kDeep of each in flight, against the tokens' x in shared
+// chunks (ffn_internal.cuh), kDeep of each in flight, against the tokens' x in shared
 // memory.  Sums stay in fp32 registers and meet in a shuffle reduction.
 #include <algorithm>
 
@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kDeep = 4;  // chunks of each weight row loaded before the first is used
 
-template <int T, bool VEC>
+template <int T, int VEC>
 __device__ __forceinline__ void add_chunk(const Raw<CR_BF16, VEC>& g, const Raw<CR_BF16, VEC>& u,
                                           const uint16_t* x, uint32_t pitch, uint32_t base,
                                           int lane, float* ag, float* au) {
@@ -24,37 +24,40 @@ __device__ __forceinline__ void add_chunk(const Raw<CR_BF16, VEC>& g, const Raw<
   for (int t = 0; t < T; ++t) {
     Raw<CR_BF16, VEC> v;
     if constexpr (VEC) {
-      const uint4 q = *reinterpret_cast<const uint4*>(x + t * pitch + base + lane * kLaneVals);
+      const uint4* p = reinterpret_cast<const uint4*>(x + t * pitch + base + lane * lane_vals(VEC));
+      const uint4 q = p[0], r = p[1];
       v.w[0] = q.x, v.w[1] = q.y, v.w[2] = q.z, v.w[3] = q.w;
+      v.w[4] = r.x, v.w[5] = r.y, v.w[6] = r.z, v.w[7] = r.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i)
-        v.w[i] = (uint32_t)x[t * pitch + chunk_col<false>(base, lane, i)] << 16;
+      for (int i = 0; i < lane_vals(VEC); ++i)
+        v.w[i] = (uint32_t)x[t * pitch + chunk_col<0>(base, lane, i)] << 16;
     }
 #pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) {
+    for (int i = 0; i < lane_vals(VEC); ++i) {
       ag[t] = fmaf(g.value(i), v.value(i), ag[t]);
       au[t] = fmaf(u.value(i), v.value(i), au[t]);
     }
   }
 }
 
-// x in shared memory is zero past dim, up to `pitch`, a multiple of kChunk.
-template <int ACT, int T, bool VEC>
+// x in shared memory is zero past dim, up to `pitch`, a multiple of any chunk.
+template <int ACT, int T, int VEC>
 __global__ void __launch_bounds__(kBlock) k_glu_few(const __grid_constant__ GluArgs a,
                                                     uint32_t pitch) {
-  extern __shared__ uint16_t x[];
+  extern __shared__ __align__(16) uint16_t x[];
   pdl_enter();
   // a warp a chunk, all of them loaded before the first is stored
-  for (uint32_t k = threadIdx.x >> 5; k < T * (pitch / kChunk); k += kBlock / 32) {
-    const uint32_t t = k / (pitch / kChunk), base = (k - t * (pitch / kChunk)) * kChunk;
-    Raw<CR_BF16, false> r;
+  const uint32_t per = pitch / chunk_cols(0);
+  for (uint32_t k = threadIdx.x >> 5; k < T * per; k += kBlock / 32) {
+    const uint32_t t = k / per, base = (k - t * per) * chunk_cols(0);
+    Raw<CR_BF16, 0> r;
     r.clear();
     if (t < a.tokens)
       r.load(static_cast<const uint16_t*>(a.x.p) + t * a.x.ld, base, a.dim, threadIdx.x & 31);
 #pragma unroll
-    for (int i = 0; i < kLaneVals; ++i)
-      x[t * pitch + chunk_col<false>(base, threadIdx.x & 31, i)] = (uint16_t)(r.w[i] >> 16);
+    for (int i = 0; i < lane_vals(0); ++i)
+      x[t * pitch + chunk_col<0>(base, threadIdx.x & 31, i)] = (uint16_t)(r.w[i] >> 16);
   }
   __syncthreads();
   const int lane = threadIdx.x & 31;
@@ -65,17 +68,17 @@ __global__ void __launch_bounds__(kBlock) k_glu_few(const __grid_constant__ GluA
     float g[T], u[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) g[t] = u[t] = 0.0f;
-    for (uint32_t base = 0; base < a.dim; base += kDeep * kChunk) {
+    for (uint32_t base = 0; base < a.dim; base += kDeep * chunk_cols(VEC)) {
       Raw<CR_BF16, VEC> rg[kDeep], ru[kDeep];
 #pragma unroll
       for (int j = 0; j < kDeep; ++j) {
-        rg[j].load(wg, base + j * kChunk, a.dim, lane);
-        ru[j].load(wu, base + j * kChunk, a.dim, lane);
+        rg[j].load(wg, base + j * chunk_cols(VEC), a.dim, lane);
+        ru[j].load(wu, base + j * chunk_cols(VEC), a.dim, lane);
       }
 #pragma unroll
       for (int j = 0; j < kDeep; ++j)
-        if (base + j * kChunk < a.dim)
-          add_chunk<T, VEC>(rg[j], ru[j], x, pitch, base + j * kChunk, lane, g, u);
+        if (base + j * chunk_cols(VEC) < a.dim)
+          add_chunk<T, VEC>(rg[j], ru[j], x, pitch, base + j * chunk_cols(VEC), lane, g, u);
     }
 #pragma unroll
     for (int t = 0; t < T; ++t) {
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kBlock) k_glu_few(const __grid_constant__ GluA
   }
 }
 
-template <int ACT, int T, bool VEC>
+template <int ACT, int T, int VEC>
 cudaError_t run(const GluArgs& a, uint32_t pitch, cudaStream_t s) {
   int full = 0;
   cudaError_t e = persistent_grid(reinterpret_cast<const void*>(k_glu_few<ACT, T, VEC>), ~0ull >> 8, &full);
@@ -110,7 +113,7 @@ cudaError_t run(const GluArgs& a, uint32_t pitch, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_glu_few<ACT, T, VEC>, a, pitch);
 }
 
-template <int ACT, bool VEC>
+template <int ACT, int VEC>
 cudaError_t by_tokens(const GluArgs& a, uint32_t pitch, cudaStream_t s) {
   if (a.tokens == 1) return run<ACT, 1, VEC>(a, pitch, s);
   if (a.tokens == 2) return run<ACT, 2, VEC>(a, pitch, s);
@@ -120,7 +123,7 @@ cudaError_t by_tokens(const GluArgs& a, uint32_t pitch, cudaStream_t s) {
 constexpr uint32_t kFewTokens = 4;
 constexpr uint32_t kFewSmem = 48 << 10;  // what a block gets without asking
 
-uint32_t pitch_of(uint32_t dim) { return (uint32_t)(((uint64_t)dim + kChunk - 1) / kChunk * kChunk); }
+uint32_t pitch_of(uint32_t dim) { return (dim + 511) / 512 * 512; }
 
 }  // namespace
 
@@ -130,11 +133,15 @@ bool glu_few(uint64_t tokens, uint64_t dim, bool keeps) {
   return rows * pitch_of((uint32_t)dim) * 2 <= kFewSmem;
 }
 
-cudaError_t launch_glu_few(cr_act act, const GluArgs& a, bool vec, cudaStream_t s) {
+template <int ACT>
+cudaError_t by_vec(const GluArgs& a, int vec, cudaStream_t s) {
   const uint32_t pitch = pitch_of(a.dim);
-  if (act == CR_ACT_SILU)
-    return vec ? by_tokens<CR_ACT_SILU, true>(a, pitch, s) : by_tokens<CR_ACT_SILU, false>(a, pitch, s);
-  return vec ? by_tokens<CR_ACT_GELU, true>(a, pitch, s) : by_tokens<CR_ACT_GELU, false>(a, pitch, s);
+  return vec == 2 ? by_tokens<ACT, 2>(a, pitch, s)
+                  : vec == 1 ? by_tokens<ACT, 1>(a, pitch, s) : by_tokens<ACT, 0>(a, pitch, s);
+}
+
+cudaError_t launch_glu_few(cr_act act, const GluArgs& a, int vec, cudaStream_t s) {
+  return act == CR_ACT_SILU ? by_vec<CR_ACT_SILU>(a, vec, s) : by_vec<CR_ACT_GELU>(a, vec, s);
 }
 
 }  // namespace cr

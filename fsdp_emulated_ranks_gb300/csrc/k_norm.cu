@@ -29,7 +29,8 @@ namespace {
 constexpr int kRowThreads = 512;        // threads of a block that holds rows in registers, at most
 constexpr int kWideThreads = 1024;      // threads of a block on a wide row
 constexpr uint32_t kWideFrom = 8192;    // columns above which a row is wide: 16 warps x 2 chunks
-constexpr uint32_t kBackBlocks = 912;   // of the backward pass, at most: 6 on each of 152 SMs
+constexpr uint32_t kBackParts = 912;    // partial rows of dweight, at most
+constexpr uint32_t kWideParts = 64;
 constexpr int kMaxWarps = kWideThreads / 32;
 
 // Sum over the row's warps (blockDim.x / 32 of them, row threadIdx.y of the
@@ -60,7 +61,7 @@ __device__ __forceinline__ void* row_of_out(const Mat& m, uint64_t row) {
 }
 
 // x and residual of a row's chunk.
-template <int DT, bool VEC>
+template <int DT, int VEC>
 struct NormIn {
   Raw<DT, VEC> x, r;
 
@@ -74,23 +75,23 @@ struct NormIn {
   __device__ __forceinline__ void clear() { x.clear(), r.clear(); }
   __device__ __forceinline__ void values(float* h) const {
 #pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) h[i] = x.value(i) + r.value(i);
+    for (int i = 0; i < lane_vals(VEC); ++i) h[i] = x.value(i) + r.value(i);
   }
 };
 
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __device__ __forceinline__ void norm_st(const NormArgs& a, uint64_t row, uint32_t base, int lane,
                                         float* h, const Raw<DT, VEC>& w, float rstd) {
   if (a.sum.p) st_chunk<DT, VEC>(row_of_out<DT>(a.sum, row), base, a.cols, lane, h);
 #pragma unroll
-  for (int i = 0; i < kLaneVals; ++i) h[i] = h[i] * rstd * w.value(i);
+  for (int i = 0; i < lane_vals(VEC); ++i) h[i] = h[i] * rstd * w.value(i);
   if (a.y.p) st_chunk<DT, VEC>(row_of_out<DT>(a.y, row), base, a.cols, lane, h);
   if (a.y8.codes) st_chunk_q8<VEC>(a.y8, row, base, a.cols, lane, h);
 }
 
 // Block (32 * warps per row, rows per block), persistent.  The next row is
 // loaded while this one is reduced and written.
-template <int DT, int V, bool VEC>
+template <int DT, int V, int VEC>
 __global__ void __launch_bounds__(kRowThreads) k_rms_norm(const __grid_constant__ NormArgs a) {
   pdl_enter();
   __shared__ float part[2][kMaxWarps];
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kRowThreads) k_rms_norm(const __grid_constant_
   const uint64_t step = (uint64_t)gridDim.x * blockDim.y;
   uint32_t base[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) base[k] = (uint32_t)(warp + k * nw) * kChunk;
+  for (int k = 0; k < V; ++k) base[k] = (uint32_t)(warp + k * nw) * chunk_cols(VEC);
   NormIn<DT, VEC> in[V];
   Raw<DT, VEC> w[V];
   const auto load = [&](uint64_t row) {
@@ -120,15 +121,15 @@ __global__ void __launch_bounds__(kRowThreads) k_rms_norm(const __grid_constant_
   // every row of a block's turn takes part in the barriers
   for (uint64_t first = (uint64_t)blockIdx.x * blockDim.y; first < a.rows; first += step, buf ^= 1) {
     const uint64_t row = first + threadIdx.y;
-    float h[V][kLaneVals], s = 0.0f;
+    float h[V][lane_vals(VEC)], s = 0.0f;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       in[k].values(h[k]);
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i) s = fmaf(h[k][i], h[k][i], s);
+      for (int i = 0; i < lane_vals(VEC); ++i) s = fmaf(h[k][i], h[k][i], s);
     }
     load(row + step);
-    const float rstd = 1.0f / sqrtf(row_sum(s, part, buf) * a.inv_cols + a.eps);
+    const float rstd = rsqrtf(fmaf(row_sum(s, part, buf), a.inv_cols, a.eps));
     if (row >= a.rows) continue;
 #pragma unroll
     for (int k = 0; k < V; ++k)
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kRowThreads) k_rms_norm(const __grid_constant_
 }
 
 // Wide rows, one block each, read twice: the second time from L2.
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __global__ void __launch_bounds__(kWideThreads)
     k_rms_norm_wide(const __grid_constant__ NormArgs a) {
   pdl_enter();
@@ -147,15 +148,15 @@ __global__ void __launch_bounds__(kWideThreads)
   int buf = 0;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
     NormIn<DT, VEC> in;
-    float h[kLaneVals], s = 0.0f;
-    for (uint64_t base = (uint64_t)warp * kChunk; base < a.cols; base += (uint64_t)nw * kChunk) {
+    float h[lane_vals(VEC)], s = 0.0f;
+    for (uint64_t base = (uint64_t)warp * chunk_cols(VEC); base < a.cols; base += (uint64_t)nw * chunk_cols(VEC)) {
       in.load(a, row, (uint32_t)base, lane);
       in.values(h);
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i) s = fmaf(h[i], h[i], s);
+      for (int i = 0; i < lane_vals(VEC); ++i) s = fmaf(h[i], h[i], s);
     }
-    const float rstd = 1.0f / sqrtf(row_sum(s, part, buf) * a.inv_cols + a.eps);
-    for (uint64_t base = (uint64_t)warp * kChunk; base < a.cols; base += (uint64_t)nw * kChunk) {
+    const float rstd = rsqrtf(fmaf(row_sum(s, part, buf), a.inv_cols, a.eps));
+    for (uint64_t base = (uint64_t)warp * chunk_cols(VEC); base < a.cols; base += (uint64_t)nw * chunk_cols(VEC)) {
       Raw<DT, VEC> w;
       w.load(a.weight, (uint32_t)base, a.cols, lane);
       in.load(a, row, (uint32_t)base, lane);
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kWideThreads)
 // ---- backward -----------------------------------------------------------------------
 
 // h of a chunk, from the matrix or from its 8-bit form.
-template <int DT, bool VEC, bool HELD8>
+template <int DT, int VEC, bool HELD8>
 struct HeldIn {
   Raw<DT, VEC> r;
   __device__ __forceinline__ void load(const NormBackArgs& a, uint64_t row, uint32_t base, int lane) {
@@ -178,11 +179,11 @@ struct HeldIn {
   __device__ __forceinline__ void clear() { r.clear(); }
   __device__ __forceinline__ void values(float* h) const {
 #pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) h[i] = r.value(i);
+    for (int i = 0; i < lane_vals(VEC); ++i) h[i] = r.value(i);
   }
 };
 
-template <int DT, bool VEC>
+template <int DT, int VEC>
 struct HeldIn<DT, VEC, true> {
   RawQ8<VEC> r;
   __device__ __forceinline__ void load(const NormBackArgs& a, uint64_t row, uint32_t base, int lane) {
@@ -193,13 +194,13 @@ struct HeldIn<DT, VEC, true> {
 };
 
 // t = dy * weight, n = h * rstd; res: dres, or zeros.
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __device__ __forceinline__ void back_st(const NormBackArgs& a, uint64_t row, uint32_t base,
                                         int lane, const float* t, const float* n,
                                         const Raw<DT, VEC>& res, float rstd, float c) {
-  float dx[kLaneVals];
+  float dx[lane_vals(VEC)];
 #pragma unroll
-  for (int i = 0; i < kLaneVals; ++i) dx[i] = rstd * (t[i] - n[i] * c) + res.value(i);
+  for (int i = 0; i < lane_vals(VEC); ++i) dx[i] = rstd * (t[i] - n[i] * c) + res.value(i);
   st_chunk<DT, VEC>(row_of_out<DT>(a.dx, row), base, a.cols, lane, dx);
 }
 
@@ -207,7 +208,7 @@ __device__ __forceinline__ void back_st(const NormBackArgs& a, uint64_t row, uin
 // block), persistent; partial row blockIdx.x * blockDim.y + threadIdx.y of
 // dweight.  Everything the next row needs is loaded while this one is reduced
 // and written; dweight's sums and the weights stay in registers.
-template <int DT, int V, bool VEC, bool HELD8>
+template <int DT, int V, int VEC, bool HELD8>
 __global__ void __launch_bounds__(kRowThreads)
     k_rms_norm_back(const __grid_constant__ NormBackArgs a) {
   pdl_enter();
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const uint64_t step = (uint64_t)gridDim.x * blockDim.y;
   uint32_t base[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) base[k] = (uint32_t)(warp + k * nw) * kChunk;
+  for (int k = 0; k < V; ++k) base[k] = (uint32_t)(warp + k * nw) * chunk_cols(VEC);
   Raw<DT, VEC> dy[V], res[V], w[V];
   HeldIn<DT, VEC, HELD8> held[V];
   float next_rstd = 0.0f;
@@ -234,11 +235,11 @@ __global__ void __launch_bounds__(kRowThreads)
       }
     }
   };
-  float dw[V][kLaneVals];
+  float dw[V][lane_vals(VEC)];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
 #pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) dw[k][i] = 0.0f;
+    for (int i = 0; i < lane_vals(VEC); ++i) dw[k][i] = 0.0f;
     res[k].clear();
     w[k].clear();
   }
@@ -251,14 +252,14 @@ __global__ void __launch_bounds__(kRowThreads)
   for (uint64_t first = (uint64_t)blockIdx.x * blockDim.y; first < a.rows; first += step, buf ^= 1) {
     const uint64_t row = first + threadIdx.y;
     const float rstd = next_rstd;
-    float t[V][kLaneVals], n[V][kLaneVals], s = 0.0f;
+    float t[V][lane_vals(VEC)], n[V][lane_vals(VEC)], s = 0.0f;
     Raw<DT, VEC> r[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       held[k].values(n[k]);
       r[k] = res[k];
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i) {
+      for (int i = 0; i < lane_vals(VEC); ++i) {
         n[k][i] *= rstd;
         const float d = dy[k].value(i);
         dw[k][i] = fmaf(d, n[k][i], dw[k][i]);
@@ -279,25 +280,37 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i) {
+      for (int i = 0; i < lane_vals(VEC); ++i) {
         const uint32_t c = chunk_col<VEC>(base[k], lane, i);
         if (c < a.cols) p[c] = dw[k][i];
       }
   }
 }
 
-template <int DT, bool VEC>
+template <int DT, int VEC>
+__device__ __forceinline__ void ld_chunk(const void* row, uint32_t base, uint32_t cols, int lane,
+                                         float* v) {
+  Raw<DT, VEC> r;
+  r.load(row, base, cols, lane);
+#pragma unroll
+  for (int i = 0; i < lane_vals(VEC); ++i) v[i] = r.value(i);
+}
+
+template <int DT, int VEC>
 __device__ __forceinline__ void back_ld(const NormBackArgs& a, uint64_t row, uint32_t base,
                                         int lane, float* dy, float* h) {
   ld_chunk<DT, VEC>(row_of<DT>(a.dy, row), base, a.cols, lane, dy);
-  if (a.h8.codes)
-    ld_chunk_q8<VEC>(a.h8, row, base, a.cols, lane, h);
-  else
+  if (a.h8.codes) {
+    RawQ8<VEC> r;
+    r.load(a.h8, row, base, a.cols, lane);
+    r.values(h);
+  } else {
     ld_chunk<DT, VEC>(row_of<DT>(a.h, row), base, a.cols, lane, h);
+  }
 }
 
 // Wide rows, dx: one block a row, read twice.
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __global__ void __launch_bounds__(kWideThreads)
     k_rms_norm_back_wide(const __grid_constant__ NormBackArgs a) {
   pdl_enter();
@@ -306,19 +319,19 @@ __global__ void __launch_bounds__(kWideThreads)
   int buf = 0;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
     const float rstd = a.rstd[row];
-    float t[kLaneVals], n[kLaneVals], w[kLaneVals], s = 0.0f;
-    for (uint64_t base = (uint64_t)warp * kChunk; base < a.cols; base += (uint64_t)nw * kChunk) {
+    float t[lane_vals(VEC)], n[lane_vals(VEC)], w[lane_vals(VEC)], s = 0.0f;
+    for (uint64_t base = (uint64_t)warp * chunk_cols(VEC); base < a.cols; base += (uint64_t)nw * chunk_cols(VEC)) {
       back_ld<DT, VEC>(a, row, (uint32_t)base, lane, t, n);
       ld_chunk<DT, VEC>(a.weight, (uint32_t)base, a.cols, lane, w);
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i) s = fmaf(t[i] * w[i], n[i] * rstd, s);
+      for (int i = 0; i < lane_vals(VEC); ++i) s = fmaf(t[i] * w[i], n[i] * rstd, s);
     }
     const float c = row_sum(s, part, buf) * a.inv_cols;
-    for (uint64_t base = (uint64_t)warp * kChunk; base < a.cols; base += (uint64_t)nw * kChunk) {
+    for (uint64_t base = (uint64_t)warp * chunk_cols(VEC); base < a.cols; base += (uint64_t)nw * chunk_cols(VEC)) {
       back_ld<DT, VEC>(a, row, (uint32_t)base, lane, t, n);
       ld_chunk<DT, VEC>(a.weight, (uint32_t)base, a.cols, lane, w);
 #pragma unroll
-      for (int i = 0; i < kLaneVals; ++i) t[i] *= w[i], n[i] *= rstd;
+      for (int i = 0; i < lane_vals(VEC); ++i) t[i] *= w[i], n[i] *= rstd;
       Raw<DT, VEC> res;
       if (a.dres.p)
         res.load(row_of<DT>(a.dres, row), (uint32_t)base, a.cols, lane);
@@ -331,24 +344,24 @@ __global__ void __launch_bounds__(kWideThreads)
 
 // Wide rows, dweight partials: warp (blockIdx.x, warp) takes one chunk of
 // columns, blockIdx.y every gridDim.y-th row.
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __global__ void __launch_bounds__(kBlock)
     k_rms_norm_back_wide_dw(const __grid_constant__ NormBackArgs a) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const uint64_t base = ((uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5)) * kChunk;
+  const uint64_t base = ((uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5)) * chunk_cols(VEC);
   if (base >= a.cols) return;
-  float dw[kLaneVals] = {0.0f};
+  float dw[lane_vals(VEC)] = {0.0f};
   for (uint64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    float dy[kLaneVals], h[kLaneVals];
+    float dy[lane_vals(VEC)], h[lane_vals(VEC)];
     back_ld<DT, VEC>(a, row, (uint32_t)base, lane, dy, h);
     const float rstd = a.rstd[row];
 #pragma unroll
-    for (int i = 0; i < kLaneVals; ++i) dw[i] = fmaf(dy[i], h[i] * rstd, dw[i]);
+    for (int i = 0; i < lane_vals(VEC); ++i) dw[i] = fmaf(dy[i], h[i] * rstd, dw[i]);
   }
   float* p = a.partial + (uint64_t)blockIdx.y * a.cols;
 #pragma unroll
-  for (int i = 0; i < kLaneVals; ++i) {
+  for (int i = 0; i < lane_vals(VEC); ++i) {
     const uint32_t c = chunk_col<VEC>((uint32_t)base, lane, i);
     if (c < a.cols) p[c] = dw[i];
   }
@@ -364,7 +377,7 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float* partial, uint32_t
   const uint64_t c = (uint64_t)blockIdx.x * 32 + threadIdx.x;
   float s = 0.0f;
   if (c < cols) {
-#pragma unroll 4
+#pragma unroll 10
     for (uint32_t k = threadIdx.y; k < parts; k += 32) s += partial[(uint64_t)k * cols + c];
   }
   sum[threadIdx.y][threadIdx.x] = s;
@@ -388,8 +401,8 @@ struct RowShape {
 
 // One chunk a warp up to 16 warps, then two; wide rows 32 warps.  Short rows
 // share a block of about 256 threads.
-RowShape row_shape(uint64_t rows, uint32_t cols) {
-  const uint32_t chunks = (uint32_t)(((uint64_t)cols + kChunk - 1) / kChunk);
+RowShape row_shape(uint64_t rows, uint32_t cols, int vec) {
+  const uint32_t chunks = (uint32_t)(((uint64_t)cols + chunk_cols(vec) - 1) / chunk_cols(vec));
   if (cols > kWideFrom) return {0, kMaxWarps, 1};
   const int v = chunks <= kRowThreads / 32 ? 1 : 2;
   const unsigned warps = (chunks + v - 1) / v;
@@ -447,7 +460,7 @@ cudaError_t row_grid(K kernel, const RowShape& r, uint64_t rows, unsigned* grid)
   return e;
 }
 
-template <int DT, int V, bool VEC>
+template <int DT, int V, int VEC>
 cudaError_t norm_run(const NormArgs& a, const RowShape& r, cudaStream_t s) {
   unsigned grid = 0;
   const cudaError_t e = row_grid(k_rms_norm<DT, V, VEC>, r, a.rows, &grid);
@@ -455,42 +468,38 @@ cudaError_t norm_run(const NormArgs& a, const RowShape& r, cudaStream_t s) {
   return launch2(k_rms_norm<DT, V, VEC>, dim3(grid), dim3(r.warps * 32, r.rows), s, a);
 }
 
-template <int DT, bool VEC>
+template <int DT, int VEC>
 cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.rows, a.cols);
-  switch (r.v) {
-    case 1: return norm_run<DT, 1, VEC>(a, r, s);
-    case 2: return norm_run<DT, 2, VEC>(a, r, s);
-    default: break;
-  }
+  const RowShape r = row_shape(a.rows, a.cols, VEC);
+  if (r.v == 1) return norm_run<DT, 1, VEC>(a, r, s);
+  if constexpr (VEC == 0)
+    if (r.v == 2) return norm_run<DT, 2, VEC>(a, r, s);
   const unsigned g = (unsigned)std::min<uint64_t>(a.rows, 1u << 30);
   return launch2(k_rms_norm_wide<DT, VEC>, dim3(g), dim3(kWideThreads), s, a);
 }
 
-template <int DT, int V, bool VEC>
+template <int DT, int V, int VEC>
 cudaError_t back_run(NormBackArgs& a, const RowShape& r, cudaStream_t s) {
   void (*kernel)(const NormBackArgs) =
       a.h8.codes ? k_rms_norm_back<DT, V, VEC, true> : k_rms_norm_back<DT, V, VEC, false>;
   unsigned grid = 0;
   const cudaError_t e = row_grid(kernel, r, a.rows, &grid);
   if (e != cudaSuccess) return e;
-  grid = std::min(std::max(grid, 1u), kBackBlocks);  // no rows: one block writes zeros
+  grid = std::min(std::max(grid, 1u), kBackParts / r.rows);  // no rows: one block writes zeros
   a.parts = grid * r.rows;
   return launch2(kernel, dim3(grid), dim3(r.warps * 32, r.rows), s, a);
 }
 
-template <int DT, bool VEC>
+template <int DT, int VEC>
 cudaError_t back_dispatch(NormBackArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.rows, a.cols);
+  const RowShape r = row_shape(a.rows, a.cols, VEC);
   const dim3 block(kWideThreads);
-  switch (r.v) {
-    case 1: return back_run<DT, 1, VEC>(a, r, s);
-    case 2: return back_run<DT, 2, VEC>(a, r, s);
-    default: break;
-  }
+  if (r.v == 1) return back_run<DT, 1, VEC>(a, r, s);
+  if constexpr (VEC == 0)
+    if (r.v == 2) return back_run<DT, 2, VEC>(a, r, s);
   // dweight first: dx may be written over dy or h
   if (a.partial) {
-    const unsigned gx = (a.cols / kChunk + 1 + kBlock / 32 - 1) / (kBlock / 32);
+    const unsigned gx = (a.cols / chunk_cols(VEC) + 1 + kBlock / 32 - 1) / (kBlock / 32);
     cudaError_t e = launch2(k_rms_norm_back_wide_dw<DT, VEC>, dim3(gx, a.parts), dim3(kBlock), s, a);
     if (e != cudaSuccess || !a.dx.p) return e;
   }
@@ -498,33 +507,42 @@ cudaError_t back_dispatch(NormBackArgs& a, cudaStream_t s) {
   return launch2(k_rms_norm_back_wide<DT, VEC>, dim3(g), block, s, a);
 }
 
+template <int DT>
+cudaError_t norm_by_vec(const NormArgs& a, int vec, cudaStream_t s) {
+  return vec == 2 ? norm_dispatch<DT, 2>(a, s)
+                  : vec == 1 ? norm_dispatch<DT, 1>(a, s) : norm_dispatch<DT, 0>(a, s);
+}
+
+template <int DT>
+cudaError_t back_by_vec(NormBackArgs& a, int vec, cudaStream_t s) {
+  return vec == 2 ? back_dispatch<DT, 2>(a, s)
+                  : vec == 1 ? back_dispatch<DT, 1>(a, s) : back_dispatch<DT, 0>(a, s);
+}
+
 }  // namespace
 
-cudaError_t launch_rms_norm(cr_dtype d, const NormArgs& a, bool vec, cudaStream_t s) {
-  if (d == CR_BF16) return vec ? norm_dispatch<CR_BF16, true>(a, s) : norm_dispatch<CR_BF16, false>(a, s);
-  return vec ? norm_dispatch<CR_F32, true>(a, s) : norm_dispatch<CR_F32, false>(a, s);
+cudaError_t launch_rms_norm(cr_dtype d, const NormArgs& a, int vec, cudaStream_t s) {
+  return d == CR_BF16 ? norm_by_vec<CR_BF16>(a, vec, s) : norm_by_vec<CR_F32>(a, vec, s);
 }
 
 uint32_t norm_back_parts(uint64_t rows, uint32_t cols) {
-  const RowShape r = row_shape(rows, cols);
-  if (r.v == 0) return (uint32_t)std::min<uint64_t>(std::max<uint64_t>(rows, 1), 64);
-  const uint64_t blocks = std::max<uint64_t>((rows + r.rows - 1) / r.rows, 1);
-  return (uint32_t)std::min<uint64_t>(blocks, kBackBlocks) * r.rows;
+  if (cols > kWideFrom) return (uint32_t)std::min<uint64_t>(std::max<uint64_t>(rows, 1), kWideParts);
+  uint32_t most = 0;
+  for (int vec : {0, 1}) {
+    const RowShape r = row_shape(rows, cols, vec);
+    const uint64_t blocks = std::max<uint64_t>((rows + r.rows - 1) / r.rows, 1);
+    most = std::max(most, (uint32_t)std::min<uint64_t>(blocks, kBackParts / r.rows) * r.rows);
+  }
+  return most;
 }
 
-cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, NormBackArgs a, bool vec,
-                                 cudaStream_t s) {
-  a.parts = norm_back_parts(a.rows, a.cols);
-  cudaError_t e;
-  if (d == CR_BF16)
-    e = vec ? back_dispatch<CR_BF16, true>(a, s) : back_dispatch<CR_BF16, false>(a, s);
-  else
-    e = vec ? back_dispatch<CR_F32, true>(a, s) : back_dispatch<CR_F32, false>(a, s);
+cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, NormBackArgs a, int vec, cudaStream_t s) {
+  if (a.cols > kWideFrom) a.parts = norm_back_parts(a.rows, a.cols);
+  const cudaError_t e = d == CR_BF16 ? back_by_vec<CR_BF16>(a, vec, s) : back_by_vec<CR_F32>(a, vec, s);
   if (e != cudaSuccess || !a.partial) return e;
   const dim3 grid((a.cols + 31) / 32), block(32, 32);
-  if (dw == CR_BF16)
-    return launch2(k_norm_dw<CR_BF16>, grid, block, s, (const float*)a.partial, a.parts, a.cols, a.dweight);
-  return launch2(k_norm_dw<CR_F32>, grid, block, s, (const float*)a.partial, a.parts, a.cols, a.dweight);
+  return launch2(dw == CR_BF16 ? k_norm_dw<CR_BF16> : k_norm_dw<CR_F32>, grid, block, s,
+                 (const float*)a.partial, a.parts, a.cols, a.dweight);
 }
 
 }  // namespace cr

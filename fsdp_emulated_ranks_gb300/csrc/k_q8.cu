@@ -1,10 +1,12 @@
 // k_q8.cu -- 8-bit activation checkpoints: store, load, and the gate's
 // backward pass, which reads gate and up from their checkpoints.
 //
-// All are one pass over memory, bound by HBM: a warp takes a 256-column chunk
-// of a row (ffn_internal.cuh), so the 128-column group's largest magnitude is
-// a shuffle reduction over 16 lanes.  A warp loads kAhead chunks before it
-// works on the first, to keep enough bytes in flight.
+// All are one pass over memory: a warp takes a chunk of a row
+// (ffn_internal.cuh), so the 128-column group's largest magnitude is a shuffle
+// reduction.  A warp that loads few bytes a chunk loads several chunks before
+// it works on the first.
+#include <type_traits>
+
 #include "ffn_internal.cuh"
 #include "pdl.cuh"
 
@@ -18,14 +20,14 @@ struct ChunkRange {
   FastDiv per_row;
 };
 
-ChunkRange chunk_range(uint64_t rows, uint32_t cols) {
-  const uint64_t per_row = ((uint64_t)cols + kChunk - 1) / kChunk;
+ChunkRange chunk_range(uint64_t rows, uint32_t cols, int vec) {
+  const uint64_t per_row = ((uint64_t)cols + chunk_cols(vec) - 1) / chunk_cols(vec);
   return {rows * per_row, fastdiv_make(per_row, rows * per_row)};
 }
 
 // Calls load(j, row, base) for up to AHEAD chunks, then work(j, row, base) for
 // the same: chunk w, w + W, ..., of the warp w of W in the grid.
-template <int AHEAD, typename Load, typename Work>
+template <int VEC, int AHEAD, typename Load, typename Work>
 __device__ __forceinline__ void for_chunks(const ChunkRange& r, Load load, Work work) {
   const uint64_t stride = (uint64_t)gridDim.x * (kBlock / 32);
   for (uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); k < r.chunks;
@@ -37,7 +39,7 @@ __device__ __forceinline__ void for_chunks(const ChunkRange& r, Load load, Work 
       const uint64_t c = k + j * stride;
       if (c >= r.chunks) break;
       row[j] = fastdiv_div(r.per_row, c);
-      base[j] = (uint32_t)(c - row[j] * r.per_row.d) * kChunk;
+      base[j] = (uint32_t)(c - row[j] * r.per_row.d) * chunk_cols(VEC);
       load(j, row[j], base[j]);
     }
 #pragma unroll
@@ -53,43 +55,43 @@ __device__ __forceinline__ char* row_at(const Mat& m, uint64_t row) {
   return static_cast<char*>(m.p) + row * m.ld * (DT == CR_BF16 ? 2 : 4);
 }
 
-constexpr int kAhead = 2;
+constexpr int kAhead = 2;  // chunks of a warp in flight, where a chunk is few bytes
 
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __global__ void __launch_bounds__(kBlock) k_q8_store(const __grid_constant__ Mat x,
                                                      const __grid_constant__ Q8 q, uint32_t cols,
                                                      const __grid_constant__ ChunkRange r) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
   Raw<DT, VEC> in[kAhead];
-  for_chunks<kAhead>(
+  for_chunks<VEC, kAhead>(
       r,
       [&](int j, uint64_t row, uint32_t base) { in[j].load(row_at<DT>(x, row), base, cols, lane); },
       [&](int j, uint64_t row, uint32_t base) {
-        float v[kLaneVals];
+        float v[lane_vals(VEC)];
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) v[i] = in[j].value(i);
+        for (int i = 0; i < lane_vals(VEC); ++i) v[i] = in[j].value(i);
         st_chunk_q8<VEC>(q, row, base, cols, lane, v);
       });
 }
 
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __global__ void __launch_bounds__(kBlock) k_q8_load(const __grid_constant__ Q8 q,
                                                     const __grid_constant__ Mat x, uint32_t cols,
                                                     const __grid_constant__ ChunkRange r) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  RawQ8<VEC> in[2 * kAhead];
-  for_chunks<2 * kAhead>(
+  RawQ8<VEC> in[kAhead];
+  for_chunks<VEC, kAhead>(
       r, [&](int j, uint64_t row, uint32_t base) { in[j].load(q, row, base, cols, lane); },
       [&](int j, uint64_t row, uint32_t base) {
-        float v[kLaneVals];
+        float v[lane_vals(VEC)];
         in[j].values(v);
         st_chunk<DT, VEC>(row_at<DT>(x, row), base, cols, lane, v);
       });
 }
 
-template <bool VEC>
+template <int VEC>
 __global__ void __launch_bounds__(kBlock) k_q8_split(const __grid_constant__ Q8 q,
                                                      const __grid_constant__ Mat hi,
                                                      const __grid_constant__ Mat lo, uint32_t cols,
@@ -97,47 +99,46 @@ __global__ void __launch_bounds__(kBlock) k_q8_split(const __grid_constant__ Q8 
   pdl_enter();
   const int lane = threadIdx.x & 31;
   RawQ8<VEC> in[kAhead];
-  for_chunks<kAhead>(
+  for_chunks<VEC, kAhead>(
       r, [&](int j, uint64_t row, uint32_t base) { in[j].load(q, row, base, cols, lane); },
       [&](int j, uint64_t row, uint32_t base) {
-        float v[kLaneVals], rest[kLaneVals];
+        float v[lane_vals(VEC)], rest[lane_vals(VEC)];
         in[j].values(v);
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i)
+        for (int i = 0; i < lane_vals(VEC); ++i)
           rest[i] = v[i] - ffn_bf16((uint16_t)ffn_bf16x2(v[i], 0.0f));
         st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(hi, row), base, cols, lane, v);
         st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(lo, row), base, cols, lane, rest);
       });
 }
 
-__global__ void __launch_bounds__(kBlock) k_copy_bf16(const __grid_constant__ Mat src,
-                                                      const __grid_constant__ Mat dst,
-                                                      uint32_t cols,
-                                                      const __grid_constant__ ChunkRange r) {
+// blockIdx.y: which copy.
+__global__ void __launch_bounds__(kBlock) k_copy_bf16(const __grid_constant__ CopyBf16 c) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  Raw<CR_BF16, false> in[kAhead];
-  for_chunks<kAhead>(
-      r,
+  const CopyBf16::One& m = c.one[blockIdx.y];
+  Raw<CR_BF16, 0> in[kAhead];
+  for_chunks<0, kAhead>(
+      ChunkRange{m.chunks, m.per_row},
       [&](int j, uint64_t row, uint32_t base) {
-        in[j].load(row_at<CR_BF16>(src, row), base, cols, lane);
+        in[j].load(row_at<CR_BF16>(m.src, row), base, m.cols, lane);
       },
       [&](int j, uint64_t row, uint32_t base) {
-        float v[kLaneVals];
+        float v[lane_vals(0)];
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) v[i] = in[j].value(i);
-        st_chunk<CR_BF16, false>(row_at<CR_BF16>(dst, row), base, cols, lane, v);
+        for (int i = 0; i < lane_vals(0); ++i) v[i] = in[j].value(i);
+        st_chunk<CR_BF16, 0>(row_at<CR_BF16>(m.dst, row), base, m.cols, lane, v);
       });
 }
 
-template <int ACT, bool VEC>
+template <int ACT, int VEC>
 __global__ void __launch_bounds__(kBlock) k_act_back(const __grid_constant__ ActBackArgs a,
                                                      const __grid_constant__ ChunkRange r) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  Raw<CR_BF16, VEC> in[kAhead];
-  RawQ8<VEC> gate[kAhead], up[kAhead];
-  for_chunks<kAhead>(
+  Raw<CR_BF16, VEC> in[1];
+  RawQ8<VEC> gate[1], up[1];
+  for_chunks<VEC, 1>(
       r,
       [&](int j, uint64_t row, uint32_t base) {
         in[j].load(row_at<CR_BF16>(a.da, row), base, a.cols, lane);
@@ -145,11 +146,11 @@ __global__ void __launch_bounds__(kBlock) k_act_back(const __grid_constant__ Act
         up[j].load(a.u8, row, base, a.cols, lane);
       },
       [&](int j, uint64_t row, uint32_t base) {
-        float g[kLaneVals], u[kLaneVals], dg[kLaneVals], du[kLaneVals];
+        float g[lane_vals(VEC)], u[lane_vals(VEC)], dg[lane_vals(VEC)], du[lane_vals(VEC)];
         gate[j].values(g);
         up[j].values(u);
 #pragma unroll
-        for (int i = 0; i < kLaneVals; ++i) {
+        for (int i = 0; i < lane_vals(VEC); ++i) {
           const float da = in[j].value(i);
           const float2 v = act_gate_slope<ACT>(g[i]);
           dg[i] = da * u[i] * v.y;
@@ -169,50 +170,62 @@ dim3 chunk_grid(const ChunkRange& r, int ahead) {
 
 }  // namespace
 
+// f(integral constant) for the access width.
+template <typename F>
+cudaError_t with_vec(int vec, F f) {
+  switch (vec) {
+    case 2: return f(std::integral_constant<int, 2>());
+    case 1: return f(std::integral_constant<int, 1>());
+    default: return f(std::integral_constant<int, 0>());
+  }
+}
+
 cudaError_t launch_q8_store(cr_dtype d, const Mat& x, const Q8& q, uint64_t rows, uint32_t cols,
-                            bool vec, cudaStream_t s) {
-  const ChunkRange r = chunk_range(rows, cols);
-  const dim3 grid = chunk_grid(r, kAhead);
-  if (d == CR_BF16)
-    return vec ? launch_pdl(k_q8_store<CR_BF16, true>, grid, kBlock, s, x, q, cols, r)
-               : launch_pdl(k_q8_store<CR_BF16, false>, grid, kBlock, s, x, q, cols, r);
-  return vec ? launch_pdl(k_q8_store<CR_F32, true>, grid, kBlock, s, x, q, cols, r)
-             : launch_pdl(k_q8_store<CR_F32, false>, grid, kBlock, s, x, q, cols, r);
+                            int vec, cudaStream_t s) {
+  const ChunkRange r = chunk_range(rows, cols, vec);
+  return with_vec(vec, [&](auto v) {
+    return launch_pdl(d == CR_BF16 ? k_q8_store<CR_BF16, v()> : k_q8_store<CR_F32, v()>,
+                      chunk_grid(r, kAhead), kBlock, s, x, q, cols, r);
+  });
 }
 
 cudaError_t launch_q8_load(cr_dtype d, const Q8& q, const Mat& x, uint64_t rows, uint32_t cols,
-                           bool vec, cudaStream_t s) {
-  const ChunkRange r = chunk_range(rows, cols);
-  const dim3 grid = chunk_grid(r, 2 * kAhead);
-  if (d == CR_BF16)
-    return vec ? launch_pdl(k_q8_load<CR_BF16, true>, grid, kBlock, s, q, x, cols, r)
-               : launch_pdl(k_q8_load<CR_BF16, false>, grid, kBlock, s, q, x, cols, r);
-  return vec ? launch_pdl(k_q8_load<CR_F32, true>, grid, kBlock, s, q, x, cols, r)
-             : launch_pdl(k_q8_load<CR_F32, false>, grid, kBlock, s, q, x, cols, r);
+                           int vec, cudaStream_t s) {
+  const ChunkRange r = chunk_range(rows, cols, vec);
+  return with_vec(vec, [&](auto v) {
+    return launch_pdl(d == CR_BF16 ? k_q8_load<CR_BF16, v()> : k_q8_load<CR_F32, v()>,
+                      chunk_grid(r, kAhead), kBlock, s, q, x, cols, r);
+  });
 }
 
 cudaError_t launch_q8_split(const Q8& q, const Mat& hi, const Mat& lo, uint64_t rows, uint32_t cols,
-                            bool vec, cudaStream_t s) {
-  const ChunkRange r = chunk_range(rows, cols);
-  const dim3 grid = chunk_grid(r, kAhead);
-  return vec ? launch_pdl(k_q8_split<true>, grid, kBlock, s, q, hi, lo, cols, r)
-             : launch_pdl(k_q8_split<false>, grid, kBlock, s, q, hi, lo, cols, r);
+                            int vec, cudaStream_t s) {
+  const ChunkRange r = chunk_range(rows, cols, vec);
+  return with_vec(vec, [&](auto v) {
+    return launch_pdl(k_q8_split<v()>, chunk_grid(r, kAhead), kBlock, s, q, hi, lo, cols, r);
+  });
 }
 
-cudaError_t launch_copy_bf16(const Mat& src, const Mat& dst, uint64_t rows, uint32_t cols,
-                             cudaStream_t s) {
-  const ChunkRange r = chunk_range(rows, cols);
-  return launch_pdl(k_copy_bf16, chunk_grid(r, kAhead), kBlock, s, src, dst, cols, r);
+void add_copy(CopyBf16* c, const Mat& src, const Mat& dst, uint64_t rows, uint32_t cols) {
+  const ChunkRange r = chunk_range(rows, cols, 0);
+  c->one[c->n++] = CopyBf16::One{src, dst, r.chunks, r.per_row, cols};
 }
 
-cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, bool vec, cudaStream_t s) {
-  const ChunkRange r = chunk_range(a.rows, a.cols);
-  const dim3 grid = chunk_grid(r, kAhead);
-  if (act == CR_ACT_SILU)
-    return vec ? launch_pdl(k_act_back<CR_ACT_SILU, true>, grid, kBlock, s, a, r)
-               : launch_pdl(k_act_back<CR_ACT_SILU, false>, grid, kBlock, s, a, r);
-  return vec ? launch_pdl(k_act_back<CR_ACT_GELU, true>, grid, kBlock, s, a, r)
-             : launch_pdl(k_act_back<CR_ACT_GELU, false>, grid, kBlock, s, a, r);
+cudaError_t launch_copy_bf16(const CopyBf16& c, cudaStream_t s) {
+  if (c.n == 0) return cudaSuccess;
+  uint64_t most = 0;
+  for (int k = 0; k < c.n; ++k) most = c.one[k].chunks > most ? c.one[k].chunks : most;
+  dim3 grid = chunk_grid(ChunkRange{most, FastDiv{}}, kAhead);
+  grid.y = c.n;
+  return launch_pdl(k_copy_bf16, grid, kBlock, s, c);
+}
+
+cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, int vec, cudaStream_t s) {
+  const ChunkRange r = chunk_range(a.rows, a.cols, vec);
+  return with_vec(vec, [&](auto v) {
+    return launch_pdl(act == CR_ACT_SILU ? k_act_back<CR_ACT_SILU, v()> : k_act_back<CR_ACT_GELU, v()>,
+                      chunk_grid(r, 1), kBlock, s, a, r);
+  });
 }
 
 }  // namespace cr
