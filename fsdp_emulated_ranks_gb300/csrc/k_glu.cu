@@ -92,10 +92,16 @@ __device__ __forceinline__ void st_square(T* out, uint64_t ld, uint64_t row0, ui
   for (int i = 0; i < words; ++i) slab[lane * 33 + i] = w[i];
   __syncwarp();
   const uint32_t height = rows - row0 < 32 ? (uint32_t)(rows - row0) : 32u;
-  if (c + lane < cols)
-    for (uint32_t r = 0; r < height; ++r)
-      out[(row0 + r) * ld + c + lane] =
-          (T)(slab[r * 33 + lane / per] >> (8 * sizeof(T) * (lane % per)));
+  if (c + lane >= cols) return;
+  T* p = out + row0 * ld + c + lane;
+  const uint32_t* from = slab + lane / per;
+  const int shift = 8 * sizeof(T) * (lane % per);
+  if (height == 32) {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) p[r * ld] = (T)(from[r * 33] >> shift);
+  } else {
+    for (uint32_t r = 0; r < height; ++r) p[r * ld] = (T)(from[r * 33] >> shift);
+  }
 }
 
 template <int DT>

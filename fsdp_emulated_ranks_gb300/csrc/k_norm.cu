@@ -3,10 +3,9 @@
 //
 // Forward, per row of h = x + residual:  v = h * rstd * weight with
 // rstd = 1/sqrt(mean h^2 + eps).  A row is held in registers between its one
-// read and its writes: warps x chunks of 256 columns (V chunks a warp), the
-// sum of squares reduced by shuffles and, across the row's warps, through
-// shared memory.  Rows too wide for that (V = 0) are read twice; the second
-// read comes from L2.
+// read and its writes, a chunk a warp, the sum of squares reduced by shuffles
+// and, across the row's warps, through shared memory.  Rows too wide for that
+// are read twice; the second read comes from L2.
 //
 // Backward, per row with n = h * rstd and c = mean(dy * weight * n):
 // dx = rstd * (dy * weight - n * c) + dres.  dweight sums dy * n down the
@@ -26,9 +25,9 @@ namespace cr {
 
 namespace {
 
-constexpr int kRowThreads = 512;        // threads of a block that holds rows in registers, at most
+constexpr int kBackThreads = 512;       // threads of the backward pass's blocks, at most
 constexpr int kWideThreads = 1024;      // threads of a block on a wide row
-constexpr uint32_t kWideFrom = 8192;    // columns above which a row is wide: 16 warps x 2 chunks
+constexpr uint32_t kWideFrom = 8192;    // columns above which a row of the forward pass is wide
 constexpr uint32_t kBackParts = 912;    // partial rows of dweight, at most
 constexpr uint32_t kWideParts = 64;
 constexpr int kMaxWarps = kWideThreads / 32;
@@ -89,51 +88,41 @@ __device__ __forceinline__ void norm_st(const NormArgs& a, uint64_t row, uint32_
   if (a.y8.codes) st_chunk_q8<VEC>(a.y8, row, base, a.cols, lane, h);
 }
 
+// Threads of a block that holds rows in registers, at most: a chunk a warp up
+// to kWideFrom columns.
+constexpr int row_threads(int vec) { return (int)(kWideFrom / chunk_cols(vec)) * 32; }
+
 // Block (32 * warps per row, rows per block), persistent.  The next row is
 // loaded while this one is reduced and written.
-template <int DT, int V, int VEC>
-__global__ void __launch_bounds__(kRowThreads) k_rms_norm(const __grid_constant__ NormArgs a) {
+template <int DT, int VEC>
+__global__ void __launch_bounds__(row_threads(VEC)) k_rms_norm(const __grid_constant__ NormArgs a) {
   pdl_enter();
   __shared__ float part[2][kMaxWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = (threadIdx.x >> 5) * chunk_cols(VEC);
   const uint64_t step = (uint64_t)gridDim.x * blockDim.y;
-  uint32_t base[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) base[k] = (uint32_t)(warp + k * nw) * chunk_cols(VEC);
-  NormIn<DT, VEC> in[V];
-  Raw<DT, VEC> w[V];
+  NormIn<DT, VEC> in;
+  Raw<DT, VEC> w;
   const auto load = [&](uint64_t row) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      if (row < a.rows && base[k] < a.cols)
-        in[k].load(a, row, base[k], lane);
-      else
-        in[k].clear();
-    }
+    if (row < a.rows)
+      in.load(a, row, base, lane);
+    else
+      in.clear();
   };
   load((uint64_t)blockIdx.x * blockDim.y + threadIdx.y);
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    w[k].clear();
-    if (base[k] < a.cols) w[k].load(a.weight, base[k], a.cols, lane);
-  }
+  w.load(a.weight, base, a.cols, lane);
   int buf = 0;
   // every row of a block's turn takes part in the barriers
   for (uint64_t first = (uint64_t)blockIdx.x * blockDim.y; first < a.rows; first += step, buf ^= 1) {
     const uint64_t row = first + threadIdx.y;
-    float h[V][lane_vals(VEC)], s = 0.0f;
+    float h[lane_vals(VEC)], s = 0.0f;
+    in.values(h);
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      in[k].values(h[k]);
-#pragma unroll
-      for (int i = 0; i < lane_vals(VEC); ++i) s = fmaf(h[k][i], h[k][i], s);
-    }
+    for (int i = 0; i < lane_vals(VEC); ++i) s = fmaf(h[i], h[i], s);
     load(row + step);
     const float rstd = rsqrtf(fmaf(row_sum(s, part, buf), a.inv_cols, a.eps));
     if (row >= a.rows) continue;
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (base[k] < a.cols) norm_st<DT, VEC>(a, row, base[k], lane, h[k], w[k], rstd);
+    norm_st<DT, VEC>(a, row, base, lane, h, w, rstd);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   }
 }
@@ -204,86 +193,75 @@ __device__ __forceinline__ void back_st(const NormBackArgs& a, uint64_t row, uin
   st_chunk<DT, VEC>(row_of_out<DT>(a.dx, row), base, a.cols, lane, dx);
 }
 
-// Rows of at most kWideFrom columns: block (32 * warps per row, rows per
+// Rows a block of 16 warps can hold: block (32 * warps per row, rows per
 // block), persistent; partial row blockIdx.x * blockDim.y + threadIdx.y of
-// dweight.  Everything the next row needs is loaded while this one is reduced
-// and written; dweight's sums and the weights stay in registers.
-template <int DT, int V, int VEC, bool HELD8>
-__global__ void __launch_bounds__(kRowThreads)
+// dweight, whose sums stay in registers.  With vectors, everything the next
+// row needs is loaded while this one is reduced and written; the scalar
+// kernel, whose loads take twice the registers, relies on more warps instead.
+template <int DT, int VEC, bool HELD8>
+__global__ void __launch_bounds__(kBackThreads)
     k_rms_norm_back(const __grid_constant__ NormBackArgs a) {
   pdl_enter();
   __shared__ float part[2][kMaxWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  constexpr bool kLoadAhead = VEC != 0;
+  constexpr int vals = lane_vals(VEC);
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = (threadIdx.x >> 5) * chunk_cols(VEC);
   const uint64_t step = (uint64_t)gridDim.x * blockDim.y;
-  uint32_t base[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) base[k] = (uint32_t)(warp + k * nw) * chunk_cols(VEC);
-  Raw<DT, VEC> dy[V], res[V], w[V];
-  HeldIn<DT, VEC, HELD8> held[V];
+  Raw<DT, VEC> dy, res, w;
+  HeldIn<DT, VEC, HELD8> held;
   float next_rstd = 0.0f;
   const auto load = [&](uint64_t row) {
-    if (row < a.rows) next_rstd = a.rstd[row];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      if (row < a.rows && base[k] < a.cols) {
-        dy[k].load(row_of<DT>(a.dy, row), base[k], a.cols, lane);
-        held[k].load(a, row, base[k], lane);
-        if (a.dres.p) res[k].load(row_of<DT>(a.dres, row), base[k], a.cols, lane);
-      } else {
-        dy[k].clear();
-        held[k].clear();
-      }
+    if (row < a.rows) {
+      next_rstd = a.rstd[row];
+      dy.load(row_of<DT>(a.dy, row), base, a.cols, lane);
+      held.load(a, row, base, lane);
+      if (a.dres.p) res.load(row_of<DT>(a.dres, row), base, a.cols, lane);
+    } else {
+      dy.clear();
+      held.clear();
     }
   };
-  float dw[V][lane_vals(VEC)];
+  float dw[vals];
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-#pragma unroll
-    for (int i = 0; i < lane_vals(VEC); ++i) dw[k][i] = 0.0f;
-    res[k].clear();
-    w[k].clear();
+  for (int i = 0; i < vals; ++i) dw[i] = 0.0f;
+  res.clear();
+  if (kLoadAhead) {
+    load((uint64_t)blockIdx.x * blockDim.y + threadIdx.y);
+    if (a.rows) w.load(a.weight, base, a.cols, lane);
   }
-  load((uint64_t)blockIdx.x * blockDim.y + threadIdx.y);
-#pragma unroll
-  for (int k = 0; k < V; ++k)
-    if (base[k] < a.cols && a.rows) w[k].load(a.weight, base[k], a.cols, lane);
   int buf = 0;
   // every row of a block's turn takes part in the barriers
   for (uint64_t first = (uint64_t)blockIdx.x * blockDim.y; first < a.rows; first += step, buf ^= 1) {
     const uint64_t row = first + threadIdx.y;
-    const float rstd = next_rstd;
-    float t[V][lane_vals(VEC)], n[V][lane_vals(VEC)], s = 0.0f;
-    Raw<DT, VEC> r[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      held[k].values(n[k]);
-      r[k] = res[k];
-#pragma unroll
-      for (int i = 0; i < lane_vals(VEC); ++i) {
-        n[k][i] *= rstd;
-        const float d = dy[k].value(i);
-        dw[k][i] = fmaf(d, n[k][i], dw[k][i]);
-        t[k][i] = d * w[k].value(i);
-        s = fmaf(t[k][i], n[k][i], s);
-      }
+    if (!kLoadAhead) {
+      load(row);
+      w.load(a.weight, base, a.cols, lane);
     }
-    load(row + step);
+    const float rstd = next_rstd;
+    float t[vals], n[vals], s = 0.0f;
+    held.values(n);
+    const Raw<DT, VEC> r = res;
+#pragma unroll
+    for (int i = 0; i < vals; ++i) {
+      n[i] *= rstd;
+      const float d = dy.value(i);
+      dw[i] = fmaf(d, n[i], dw[i]);
+      t[i] = d * w.value(i);
+      s = fmaf(t[i], n[i], s);
+    }
+    if (kLoadAhead) load(row + step);
     if (!a.dx.p) continue;
     const float c = row_sum(s, part, buf) * a.inv_cols;
-    if (row >= a.rows) continue;
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (base[k] < a.cols) back_st<DT, VEC>(a, row, base[k], lane, t[k], n[k], r[k], rstd, c);
+    if (row < a.rows) back_st<DT, VEC>(a, row, base, lane, t, n, r, rstd, c);
   }
   if (a.partial) {
     float* p = a.partial + ((uint64_t)blockIdx.x * blockDim.y + threadIdx.y) * a.cols;
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-#pragma unroll
-      for (int i = 0; i < lane_vals(VEC); ++i) {
-        const uint32_t c = chunk_col<VEC>(base[k], lane, i);
-        if (c < a.cols) p[c] = dw[k][i];
-      }
+    for (int i = 0; i < vals; ++i) {
+      const uint32_t c = chunk_col<VEC>(base, lane, i);
+      if (c < a.cols) p[c] = dw[i];
+    }
   }
 }
 
@@ -367,25 +345,27 @@ __global__ void __launch_bounds__(kBlock)
   }
 }
 
-// dweight = sum of the partial rows: block (32 columns, 32 row classes), each
+// dweight = sum of the partial rows: block (16 columns, 64 row classes), each
 // class in order, then the classes in order.
+constexpr int kDwCols = 16, kDwClasses = 64;
+
 template <int DW>
-__global__ void __launch_bounds__(1024) k_norm_dw(const float* partial, uint32_t parts,
-                                                  uint32_t cols, void* dweight) {
+__global__ void __launch_bounds__(kDwCols* kDwClasses)
+    k_norm_dw(const float* partial, uint32_t parts, uint32_t cols, void* dweight) {
   pdl_enter();
-  __shared__ float sum[32][33];
-  const uint64_t c = (uint64_t)blockIdx.x * 32 + threadIdx.x;
+  __shared__ float sum[kDwClasses][kDwCols + 1];
+  const uint64_t c = (uint64_t)blockIdx.x * kDwCols + threadIdx.x;
   float s = 0.0f;
   if (c < cols) {
-#pragma unroll 10
-    for (uint32_t k = threadIdx.y; k < parts; k += 32) s += partial[(uint64_t)k * cols + c];
+#pragma unroll 8
+    for (uint32_t k = threadIdx.y; k < parts; k += kDwClasses) s += partial[(uint64_t)k * cols + c];
   }
   sum[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && c < cols) {
     s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) s += sum[k][threadIdx.x];
+    for (int k = 0; k < kDwClasses; ++k) s += sum[k][threadIdx.x];
     if constexpr (DW == CR_BF16)
       static_cast<uint16_t*>(dweight)[c] = (uint16_t)ffn_bf16x2(s, 0.0f);
     else
@@ -394,21 +374,23 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float* partial, uint32_t
 }
 
 struct RowShape {
-  int v;           // chunks per warp; 0: wide
-  unsigned warps;  // per row
+  unsigned warps;  // per row, a chunk each
   unsigned rows;   // per block, at most the matrix's
 };
 
-// One chunk a warp up to 16 warps, then two; wide rows 32 warps.  Short rows
-// share a block of about 256 threads.
+// Short rows share a block of about 256 threads.
 RowShape row_shape(uint64_t rows, uint32_t cols, int vec) {
-  const uint32_t chunks = (uint32_t)(((uint64_t)cols + chunk_cols(vec) - 1) / chunk_cols(vec));
-  if (cols > kWideFrom) return {0, kMaxWarps, 1};
-  const int v = chunks <= kRowThreads / 32 ? 1 : 2;
-  const unsigned warps = (chunks + v - 1) / v;
+  const unsigned warps = (unsigned)(((uint64_t)cols + chunk_cols(vec) - 1) / chunk_cols(vec));
   const unsigned fit = std::max(8 / warps, 1u);
-  return {v, warps, (unsigned)std::min<uint64_t>(fit, std::max<uint64_t>(rows, 1))};
+  return {warps, (unsigned)std::min<uint64_t>(fit, std::max<uint64_t>(rows, 1))};
 }
+
+uint32_t wide_parts(uint64_t rows) {
+  return (uint32_t)std::min<uint64_t>(std::max<uint64_t>(rows, 1), kWideParts);
+}
+
+// Columns above which a row of the backward pass is wide.
+uint32_t back_wide_from(int vec) { return kBackThreads / 32 * chunk_cols(vec); }
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch2(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s,
@@ -460,28 +442,25 @@ cudaError_t row_grid(K kernel, const RowShape& r, uint64_t rows, unsigned* grid)
   return e;
 }
 
-template <int DT, int V, int VEC>
+template <int DT, int VEC>
 cudaError_t norm_run(const NormArgs& a, const RowShape& r, cudaStream_t s) {
   unsigned grid = 0;
-  const cudaError_t e = row_grid(k_rms_norm<DT, V, VEC>, r, a.rows, &grid);
+  const cudaError_t e = row_grid(k_rms_norm<DT, VEC>, r, a.rows, &grid);
   if (e != cudaSuccess) return e;
-  return launch2(k_rms_norm<DT, V, VEC>, dim3(grid), dim3(r.warps * 32, r.rows), s, a);
+  return launch2(k_rms_norm<DT, VEC>, dim3(grid), dim3(r.warps * 32, r.rows), s, a);
 }
 
 template <int DT, int VEC>
 cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.rows, a.cols, VEC);
-  if (r.v == 1) return norm_run<DT, 1, VEC>(a, r, s);
-  if constexpr (VEC == 0)
-    if (r.v == 2) return norm_run<DT, 2, VEC>(a, r, s);
+  if (a.cols <= kWideFrom) return norm_run<DT, VEC>(a, row_shape(a.rows, a.cols, VEC), s);
   const unsigned g = (unsigned)std::min<uint64_t>(a.rows, 1u << 30);
   return launch2(k_rms_norm_wide<DT, VEC>, dim3(g), dim3(kWideThreads), s, a);
 }
 
-template <int DT, int V, int VEC>
+template <int DT, int VEC>
 cudaError_t back_run(NormBackArgs& a, const RowShape& r, cudaStream_t s) {
   void (*kernel)(const NormBackArgs) =
-      a.h8.codes ? k_rms_norm_back<DT, V, VEC, true> : k_rms_norm_back<DT, V, VEC, false>;
+      a.h8.codes ? k_rms_norm_back<DT, VEC, true> : k_rms_norm_back<DT, VEC, false>;
   unsigned grid = 0;
   const cudaError_t e = row_grid(kernel, r, a.rows, &grid);
   if (e != cudaSuccess) return e;
@@ -492,11 +471,8 @@ cudaError_t back_run(NormBackArgs& a, const RowShape& r, cudaStream_t s) {
 
 template <int DT, int VEC>
 cudaError_t back_dispatch(NormBackArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.rows, a.cols, VEC);
-  const dim3 block(kWideThreads);
-  if (r.v == 1) return back_run<DT, 1, VEC>(a, r, s);
-  if constexpr (VEC == 0)
-    if (r.v == 2) return back_run<DT, 2, VEC>(a, r, s);
+  if (a.cols <= back_wide_from(VEC)) return back_run<DT, VEC>(a, row_shape(a.rows, a.cols, VEC), s);
+  a.parts = wide_parts(a.rows);
   // dweight first: dx may be written over dy or h
   if (a.partial) {
     const unsigned gx = (a.cols / chunk_cols(VEC) + 1 + kBlock / 32 - 1) / (kBlock / 32);
@@ -504,7 +480,7 @@ cudaError_t back_dispatch(NormBackArgs& a, cudaStream_t s) {
     if (e != cudaSuccess || !a.dx.p) return e;
   }
   const unsigned g = (unsigned)std::min<uint64_t>(a.rows, 1u << 30);
-  return launch2(k_rms_norm_back_wide<DT, VEC>, dim3(g), block, s, a);
+  return launch2(k_rms_norm_back_wide<DT, VEC>, dim3(g), dim3(kWideThreads), s, a);
 }
 
 template <int DT>
@@ -526,9 +502,9 @@ cudaError_t launch_rms_norm(cr_dtype d, const NormArgs& a, int vec, cudaStream_t
 }
 
 uint32_t norm_back_parts(uint64_t rows, uint32_t cols) {
-  if (cols > kWideFrom) return (uint32_t)std::min<uint64_t>(std::max<uint64_t>(rows, 1), kWideParts);
-  uint32_t most = 0;
+  uint32_t most = cols > back_wide_from(0) ? wide_parts(rows) : 1;
   for (int vec : {0, 1}) {
+    if (cols > back_wide_from(vec)) continue;
     const RowShape r = row_shape(rows, cols, vec);
     const uint64_t blocks = std::max<uint64_t>((rows + r.rows - 1) / r.rows, 1);
     most = std::max(most, (uint32_t)std::min<uint64_t>(blocks, kBackParts / r.rows) * r.rows);
@@ -537,10 +513,9 @@ uint32_t norm_back_parts(uint64_t rows, uint32_t cols) {
 }
 
 cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, NormBackArgs a, int vec, cudaStream_t s) {
-  if (a.cols > kWideFrom) a.parts = norm_back_parts(a.rows, a.cols);
   const cudaError_t e = d == CR_BF16 ? back_by_vec<CR_BF16>(a, vec, s) : back_by_vec<CR_F32>(a, vec, s);
   if (e != cudaSuccess || !a.partial) return e;
-  const dim3 grid((a.cols + 31) / 32), block(32, 32);
+  const dim3 grid((a.cols + kDwCols - 1) / kDwCols), block(kDwCols, kDwClasses);
   return launch2(dw == CR_BF16 ? k_norm_dw<CR_BF16> : k_norm_dw<CR_F32>, grid, block, s,
                  (const float*)a.partial, a.parts, a.cols, a.dweight);
 }

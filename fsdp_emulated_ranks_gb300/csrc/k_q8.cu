@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kBlock) k_copy_bf16(const __grid_constant__ Co
 }
 
 template <int ACT, int VEC>
-__global__ void __launch_bounds__(kBlock) k_act_back(const __grid_constant__ ActBackArgs a,
+__global__ void __launch_bounds__(kBlock, 4) k_act_back(const __grid_constant__ ActBackArgs a,
                                                      const __grid_constant__ ChunkRange r) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
