@@ -336,14 +336,29 @@ __device__ __forceinline__ void st_chunk_q8(const Q8& q, uint64_t row, uint32_t 
         if (c0 + i < cols) codes[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
     }
   } else {  // values 0-3 of every lane are one group, 4-7 the next
+    float m[2];
+    bool inf = false;
+    for (int look = 0; look < 2; ++look) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        m[h] = 0.0f;
+#pragma unroll
+        for (int i = 4 * h; i < 4 * h + 4; ++i) {
+          if (inf && fabsf(v[i]) > kFloatMax) v[i] = __int_as_float(0x7fc00000);
+          m[h] = fmaxf(m[h], fabsf(v[i]));
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        m[0] = fmaxf(m[0], __shfl_xor_sync(~0u, m[0], o));
+        m[1] = fmaxf(m[1], __shfl_xor_sync(~0u, m[1], o));
+      }
+      inf = fmaxf(m[0], m[1]) > kFloatMax;  // the same in every lane
+      if (!inf) break;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float m = q8_magnitude<4>(v + 4 * h, [](float x) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
-        return x;
-      });
-      const float s = q8_scale(m), inv = 1.0f / s;
+      const float s = q8_scale(m[h]), inv = 1.0f / s;
       if (lane == 0 && base + h * CR_Q8_GROUP < cols) scales[h] = s;
 #pragma unroll
       for (int i = 4 * h; i < 4 * h + 4; ++i)

@@ -44,8 +44,15 @@ __device__ __forceinline__ float row_sum(float s, float (*part)[kMaxWarps], int 
   const int w0 = threadIdx.y * nw;
   if ((threadIdx.x & 31) == 0) p[w0 + (threadIdx.x >> 5)] = s;
   __syncthreads();
-  s = 0.0f;
-  for (int w = 0; w < nw; ++w) s += p[w0 + w];
+  if (nw <= 4) {
+    s = 0.0f;
+    for (int w = 0; w < nw; ++w) s += p[w0 + w];
+    return s;
+  }
+  const int lane = threadIdx.x & 31;
+  s = lane < nw ? p[w0 + lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
   return s;
 }
 
@@ -92,12 +99,14 @@ __device__ __forceinline__ void norm_st(const NormArgs& a, uint64_t row, uint32_
 // to kWideFrom columns.
 constexpr int row_threads(int vec) { return (int)(kWideFrom / chunk_cols(vec)) * 32; }
 
-// Block (32 * warps per row, rows per block), persistent.  The next row is
-// loaded while this one is reduced and written.
+// Block (32 * warps per row, rows per block), persistent.  With vectors the
+// next row is loaded while this one is reduced and written; the scalar kernel
+// has fewer registers for it and relies on several blocks an SM instead.
 template <int DT, int VEC>
-__global__ void __launch_bounds__(row_threads(VEC)) k_rms_norm(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(row_threads(VEC)) __maxnreg__(VEC ? 128 : 40) k_rms_norm(const __grid_constant__ NormArgs a) {
   pdl_enter();
   __shared__ float part[2][kMaxWarps];
+  constexpr bool kLoadAhead = VEC != 0;
   const int lane = threadIdx.x & 31;
   const uint32_t base = (threadIdx.x >> 5) * chunk_cols(VEC);
   const uint64_t step = (uint64_t)gridDim.x * blockDim.y;
@@ -109,17 +118,23 @@ __global__ void __launch_bounds__(row_threads(VEC)) k_rms_norm(const __grid_cons
     else
       in.clear();
   };
-  load((uint64_t)blockIdx.x * blockDim.y + threadIdx.y);
-  w.load(a.weight, base, a.cols, lane);
+  if (kLoadAhead) {
+    load((uint64_t)blockIdx.x * blockDim.y + threadIdx.y);
+    w.load(a.weight, base, a.cols, lane);
+  }
   int buf = 0;
   // every row of a block's turn takes part in the barriers
   for (uint64_t first = (uint64_t)blockIdx.x * blockDim.y; first < a.rows; first += step, buf ^= 1) {
     const uint64_t row = first + threadIdx.y;
+    if (!kLoadAhead) {
+      load(row);
+      w.load(a.weight, base, a.cols, lane);
+    }
     float h[lane_vals(VEC)], s = 0.0f;
     in.values(h);
 #pragma unroll
     for (int i = 0; i < lane_vals(VEC); ++i) s = fmaf(h[i], h[i], s);
-    load(row + step);
+    if (kLoadAhead) load(row + step);
     const float rstd = rsqrtf(fmaf(row_sum(s, part, buf), a.inv_cols, a.eps));
     if (row >= a.rows) continue;
     norm_st<DT, VEC>(a, row, base, lane, h, w, rstd);
