@@ -1,29 +1,37 @@
 // k_glu.cu -- the gated feed-forward block: both projections, the activation
 // and the product in one kernel, and the products of its backward pass.
 //
-// One persistent kernel, three uses (T tokens, D dim, F ffn; a tile is 128
-// rows x 256 accumulator columns, K in blocks of 64):
-//   kGlu  a = act(x Wg^T) * (x Wu^T): a tile's 256 columns are the same 128
-//         columns of g and of u, so the epilogue has both in one thread's row,
-//         and a tile's width is the 8-bit checkpoints' group.
+// One kernel, three uses (T tokens, D dim, F ffn; K in blocks of 64):
+//   kGlu  a = act(x Wg^T) * (x Wu^T): a tile's 256 accumulator columns are the
+//         same 128 columns of g and of u, so the epilogue has both in one
+//         thread's row, and a tile's width is the 8-bit checkpoints' group.
 //   kDx   dx = dg Wg + du Wu: one accumulator over both products.
 //   kDw   dWg = dg^T x and dWu = du^T x: tiles of both in one launch.
 // Operands are read as they lie in memory: rows of K (x, W of kGlu, dg and du
 // of kDx) or rows of M or N (W of kDx, everything of kDw), which the tensor
 // cores take directly, so nothing is transposed.
 //
-// Block: warp 0 loads tiles by TMA into a ring of kStages buffers, warp 1
-// issues the tcgen05 products into one of two accumulators in tensor memory,
-// warps 2-5 read the other accumulator out and write the results.  TMA fills
-// rows and columns outside a matrix with zeros, so ragged sizes need no masks
-// before the epilogue.  Every wait is bounded (tc.cuh); a block that gives up
-// sets g_wait_word and leaves.
+// k_pairs, for many tiles: persistent pairs of blocks (cta_group::2), a tile
+// 256 x 256.  Each block of a pair loads its 128 rows of A and its 128 columns
+// of B and holds the accumulator of its rows, so that a byte loaded feeds
+// twice the products that a 128 x 256 tile's would.  Warp 0 loads by TMA into
+// a ring of kPairStages buffers, warp 1 of the first block issues the products
+// into one of two accumulators in tensor memory, warps 2-9 read the other one
+// out and write the results.  TMA fills rows and columns outside a matrix with
+// zeros, so ragged sizes need no masks before the epilogue.
 //
-// Where the tiles are too few for the SMs (k_split), the blocks of a cluster
-// share one tile: each takes a range of its K, leaves its partial sums in its
-// own shared memory, and then finishes a range of the tile's rows, reading
-// the partials of all in rank order.
+// k_split, where the tiles (128 x 256) are too few for the SMs and for the
+// tiles of k_pairs that would leave most SMs idle in its last turn: the blocks
+// of a cluster share one tile.  Each takes a range of its K, leaves its partial
+// sums in its own shared memory, and then finishes a range of the tile's rows,
+// reading the partials of all in rank order.
+//
+// Every wait is bounded (tc.cuh); a block that gives up sets g_wait_word and
+// leaves.
 #include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "ffn_internal.cuh"
 #include "pdl.cuh"
@@ -37,15 +45,10 @@ namespace {
 
 enum TileMode { kGlu = 0, kDx = 1, kDw = 2 };
 
-constexpr int kM = 128;       // rows of a tile
+constexpr int kM = 128;       // rows of a block's tile
 constexpr int kN = 256;       // accumulator columns of a tile
 constexpr int kK = 64;        // K of a block: 128 bytes of bf16
-constexpr int kStages = 4;
 constexpr uint32_t kABytes = kM * kK * 2, kBBytes = kN * kK * 2;
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr uint32_t kTileSmem = kStages * kStageBytes + 1024;  // + room to align to 1024
-constexpr int kTileThreads = 192;
-constexpr uint32_t kGroupM = 8;  // tile rows walked together, so that their operands stay in L2
 
 struct TileArgs {
   CUtensorMap a[2], b[2];
@@ -54,9 +57,11 @@ struct TileArgs {
   uint32_t rows, cols;        // of an output
   uint32_t seg_blocks;        // K blocks of one product
   uint32_t blocks;            // K blocks of a tile: one or two products
+  uint32_t tile_rows;         // kM, or 2 kM with k_pairs
   uint32_t tiles_m, tiles_n;  // of an output
-  uint32_t tiles;             // of all outputs
-  uint32_t splits;            // blocks that share a tile (k_split), a power of two
+  uint32_t tiles;             // k_pairs: tiles 0 .. tiles - 1 of all outputs
+  uint32_t first;             // k_split: its first tile
+  uint32_t splits;            // k_split: blocks that share a tile, a power of two
   int width;                  // bytes of the output stores all rows allow: 32, 16 or 0
   int width8;                 // the same for the codes
 };
@@ -69,15 +74,15 @@ __device__ __forceinline__ void st_run(void* p, const uint32_t* w, int width) {
     width == 32 ? st_words<2>(out + i, w + i) : st_words<1>(out + i, w + i);
 }
 
-constexpr int kSlab = 32 * 33;  // words of a warp's staging slab
+constexpr int kSlab = 32 * 17;  // words of a warp's staging slab
 
 // A warp's 32 rows x 32 columns of results, row `row0 + lane` in this
 // thread's w, 4 / sizeof(T) results a word; columns c .. c + 31.  Whole rows
 // go out as vectors, a thread its own row (full 32-byte sectors).  Where the
 // row stride or the pointer does not allow that, or columns are missing, the
-// warp turns the square round in shared memory and stores a row at a time,
-// consecutive lanes to consecutive columns: the scattered element stores this
-// replaces made the epilogue longer than the products.
+// warp turns the square round in shared memory, 16 words of a row at a time,
+// and stores consecutive columns from consecutive lanes: the scattered element
+// stores this replaces made the epilogue longer than the products.
 template <typename T>
 __device__ __forceinline__ void st_square(T* out, uint64_t ld, uint64_t row0, uint32_t c,
                                           uint32_t rows, uint32_t cols, int width, int lane,
@@ -87,20 +92,27 @@ __device__ __forceinline__ void st_square(T* out, uint64_t ld, uint64_t row0, ui
     if (row0 + lane < rows) st_run<words>(out + (row0 + lane) * ld + c, w, width);
     return;
   }
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < words; ++i) slab[lane * 33 + i] = w[i];
-  __syncwarp();
+  constexpr int part = words < 16 ? words : 16;          // words of a row a turn
+  constexpr int wide = part * per, high = 32 / wide;      // columns and rows a store covers
   const uint32_t height = rows - row0 < 32 ? (uint32_t)(rows - row0) : 32u;
-  if (c + lane >= cols) return;
-  T* p = out + row0 * ld + c + lane;
-  const uint32_t* from = slab + lane / per;
-  const int shift = 8 * sizeof(T) * (lane % per);
-  if (height == 32) {
+  const int x = lane % wide, y = lane / wide;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) p[r * ld] = (T)(from[r * 33] >> shift);
-  } else {
-    for (uint32_t r = 0; r < height; ++r) p[r * ld] = (T)(from[r * 33] >> shift);
+  for (int p = 0; p < words / part; ++p) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < part; ++i) slab[lane * 17 + i] = w[p * part + i];
+    __syncwarp();
+    const uint32_t col = c + p * wide + x;
+    T* to = out + (row0 + y) * ld + col;
+    const uint32_t* from = slab + y * 17 + x / per;
+    const int shift = 8 * sizeof(T) * (x % per);
+    if (col >= cols) continue;
+    if (height == 32) {
+#pragma unroll
+      for (int r = 0; r < 32; r += high) to[r * ld] = (T)(from[r * 17] >> shift);
+    } else {
+      for (uint32_t r = 0; r + y < height; r += high) to[r * ld] = (T)(from[r * 17] >> shift);
+    }
   }
 }
 
@@ -139,17 +151,17 @@ __device__ __forceinline__ void st_codes(const Q8& q, uint64_t row0, uint32_t c,
   st_square(q.codes, q.ld, row0, c, rows, cols, width, lane, w, slab);
 }
 
-// Tile `t` of an output, tile rows walked kGroupM at a time.
+// Tile `t`: its output, first row and tile column.  Tile rows are walked 1024
+// rows at a time, so that their operands stay in L2.
 __device__ __forceinline__ void tile_at(const TileArgs& a, uint32_t t, uint32_t* which,
-                                        uint32_t* tm, uint32_t* tn) {
-  const uint32_t per_out = a.tiles_m * a.tiles_n;
+                                        uint32_t* row, uint32_t* tn) {
+  const uint32_t per_out = a.tiles_m * a.tiles_n, walk = 8 * kM / a.tile_rows;
   *which = t / per_out;
   t -= *which * per_out;
-  const uint32_t per_group = kGroupM * a.tiles_n;
-  const uint32_t group = t / per_group, first = group * kGroupM;
-  const uint32_t height = min(kGroupM, a.tiles_m - first);
-  t -= group * per_group;
-  *tm = first + t % height;
+  const uint32_t group = t / (walk * a.tiles_n), first = group * walk;
+  const uint32_t height = min(walk, a.tiles_m - first);
+  t -= group * walk * a.tiles_n;
+  *row = (first + t % height) * a.tile_rows;
   *tn = t / height;
 }
 
@@ -166,16 +178,28 @@ __device__ __forceinline__ void ld_acc2(uint32_t addr, uint32_t addr2, bool any,
   for (int i = 0; i < 32; ++i) v[i] = v2[i] = 0.0f;
 }
 
+// What the two warps that share 32 rows of a tile tell each other: each
+// row's maxima over the 64 columns of g and of u that each has seen.  The
+// turns alternate between two places, so one barrier a turn is enough.
+struct Maxima {
+  float2 seen[2][2][kM];  // turn & 1, half, row of the tile
+  uint64_t bar[4];        // one for each 32 rows, an arrival of each warp
+};
+
 // Largest finite magnitudes of a row's 128 columns of g and of u.  fmaxf
 // passes NaN over; only where some row of the warp holds an infinity
 // (returned) are the columns looked at again.  Columns past the matrix hold
 // zeros, which no magnitude is below.
-__device__ __forceinline__ bool row_magnitudes(uint32_t acc, bool any, float* mg, float* mu) {
+__device__ __forceinline__ bool row_magnitudes(uint32_t acc, bool any, Maxima* m, uint32_t* turn,
+                                               volatile uint32_t* gave_up, int quarter, int half,
+                                               int lane, float* mg, float* mu) {
+  const int row = quarter * 32 + lane;
+  const uint32_t bar = tc::smem_addr(&m->bar[quarter]);
   bool inf = false;
   for (int look = 0; look < 2; ++look) {
     *mg = *mu = 0.0f;
 #pragma unroll 1
-    for (int c = 0; c < kN / 2; c += 32) {
+    for (int c = half * 64; c < half * 64 + 64; c += 32) {
       float g[32], u[32];
       ld_acc2(acc + c, acc + kN / 2 + c, any, g, u);
 #pragma unroll
@@ -185,18 +209,32 @@ __device__ __forceinline__ bool row_magnitudes(uint32_t acc, bool any, float* mg
         *mu = fmaxf(*mu, inf && y > kFloatMax ? 0.0f : y);
       }
     }
+    const uint32_t at = *turn & 1;
+    m->seen[at][half][row] = make_float2(*mg, *mu);
+    __syncwarp();
+    if (lane == 0) {
+      tc::bar_arrive(bar);
+      tc::bar_wait(bar, at, gave_up);  // if it gives up, the next tile's wait ends the warp
+    }
+    __syncwarp();
+    ++*turn;
+    const float2 other = m->seen[at][half ^ 1][row];
+    *mg = fmaxf(*mg, other.x), *mu = fmaxf(*mu, other.y);
+    // both warps hold the same maxima, and so decide alike
     if (inf || !__any_sync(~0u, *mg > kFloatMax || *mu > kFloatMax)) break;
     inf = true;
   }
   return inf;
 }
 
-// EPI: the activation (kGlu) or the output's dtype.
+// Half `half` of the columns of a tile's rows `row0` .. + 31, which are lanes
+// 32 * quarter .. + 31 of the accumulator.  EPI: the activation (kGlu) or the
+// output's dtype.
 template <int MODE, int EPI>
 __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32_t which,
-                                         uint32_t tm, uint32_t tn, int quarter, int lane,
-                                         uint32_t* slab) {
-  const uint64_t row0 = (uint64_t)tm * kM + quarter * 32;
+                                         uint64_t row0, uint32_t tn, int quarter, int half,
+                                         int lane, uint32_t* slab, Maxima* maxima, uint32_t* turn,
+                                         volatile uint32_t* gave_up) {
   if (row0 >= a.rows) return;
   const bool live = row0 + lane < a.rows;
   const bool any = a.blocks != 0;
@@ -207,14 +245,16 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32
     bool inf = false;
     if (a.g8.codes || a.u8.codes) {
       float mg, mu;
-      inf = row_magnitudes(acc, any, &mg, &mu);
+      inf = row_magnitudes(acc, any, maxima, turn, gave_up, quarter, half, lane, &mg, &mu);
       const float sg = q8_scale(mg), su = q8_scale(mu);
       inv_g = 1.0f / sg, inv_u = 1.0f / su;
-      if (live && a.g8.codes) a.g8.scales[(row0 + lane) * a.g8.lds + tn] = sg;
-      if (live && a.u8.codes) a.u8.scales[(row0 + lane) * a.u8.lds + tn] = su;
+      if (live && half == 0) {
+        if (a.g8.codes) a.g8.scales[(row0 + lane) * a.g8.lds + tn] = sg;
+        if (a.u8.codes) a.u8.scales[(row0 + lane) * a.u8.lds + tn] = su;
+      }
     }
 #pragma unroll 1
-    for (uint32_t c = 0; c < kN / 2 && c0 + c < a.cols; c += 32) {
+    for (uint32_t c = half * 64; c < half * 64u + 64 && c0 + c < a.cols; c += 32) {
       float g[32], u[32];
       __syncwarp();  // the last square's stores leave rows past the matrix out
       ld_acc2(acc + c, acc + kN / 2 + c, any, g, u);
@@ -229,7 +269,7 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32
   } else {
     const uint32_t c0 = tn * kN;
 #pragma unroll 1
-    for (uint32_t c = 0; c < kN && c0 + c < a.cols; c += 32) {
+    for (uint32_t c = half * 128; c < half * 128u + 128 && c0 + c < a.cols; c += 32) {
       float v[32];
       __syncwarp();
       ld_acc(acc + c, any, v);
@@ -239,153 +279,196 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32
   __syncwarp();
 }
 
-// One K block of a tile into buffer `sa`, arriving on `bar`: one thread.
+// The products of one K block, A at sa and B at sb: one thread.
+template <int MODE, int GROUP>
+__device__ __forceinline__ void multiply_block(uint32_t acc, uint32_t sa, uint32_t sb, bool first) {
+  constexpr bool a_mn = MODE == kDw, b_mn = MODE != kGlu;
+  constexpr uint32_t desc = tc::product_desc(GROUP * kM, kN, a_mn, b_mn);
+#pragma unroll
+  for (int j = 0; j < kK / 16; ++j) {
+    // 16 K: 32 bytes along a row, or 16 rows
+    const uint64_t da = a_mn ? tc::operand(sa + j * 2048, 8192, 1024) : tc::operand(sa + j * 32, 16, 1024);
+    const uint64_t db = b_mn ? tc::operand(sb + j * 2048, 8192, 1024) : tc::operand(sb + j * 32, 16, 1024);
+    tc::mma<GROUP>(acc, da, db, desc, !first || j);
+  }
+}
+
+// ---- many tiles: persistent pairs -------------------------------------------------------
+
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairStageBytes = 2 * kABytes;  // a block's half of A and of B: the same size
+constexpr uint32_t kPairSmem = kPairStages * kPairStageBytes + 1024;  // + room to align to 1024
+constexpr int kPairThreads = 320;
+static_assert(kABytes * 2 == kBBytes, "half of B is as large as a block's A");
+
+// This block's part of one K block of the pair's tile at `row`, into buffer
+// `sa`; bytes count on `bar`, the first block's.  One thread.
 template <int MODE>
-__device__ __forceinline__ void load_block(const TileArgs& a, uint32_t which, uint32_t tm,
+__device__ __forceinline__ void load_pair(const TileArgs& a, uint32_t which, uint32_t row,
+                                          uint32_t tn, uint32_t k, uint32_t rank, uint32_t sa,
+                                          uint32_t bar) {
+  const uint32_t seg = k >= a.seg_blocks, sb = sa + kABytes;
+  const int k0 = (int)((k - seg * a.seg_blocks) * kK), m0 = (int)(row + rank * kM);
+  if constexpr (MODE == kGlu) {
+    tc::tma_load_pair(sa, &a.a[0], k0, m0, bar);
+    // columns 0-127 of the accumulator are g's, 128-255 u's
+    tc::tma_load_pair(sb, &a.b[rank], k0, (int)(tn * (kN / 2)), bar);
+  } else {
+    if constexpr (MODE == kDx) {
+      tc::tma_load_pair(sa, &a.a[seg], k0, m0, bar);
+    } else {
+      tc::tma_load_pair(sa, &a.a[which], m0, k0, bar);
+      tc::tma_load_pair(sa + 8192, &a.a[which], m0 + 64, k0, bar);
+    }
+    const int n0 = (int)(tn * kN + rank * (kN / 2));
+    tc::tma_load_pair(sb, &a.b[seg], n0, k0, bar);
+    tc::tma_load_pair(sb + 8192, &a.b[seg], n0 + 64, k0, bar);
+  }
+}
+
+template <int MODE, int EPI>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    k_pairs(const __grid_constant__ TileArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kPairStages + 5];
+  __shared__ Maxima maxima;
+  __shared__ uint32_t tmem_base, slab[8 * kSlab];
+  __shared__ uint32_t gave_up_word;
+  volatile uint32_t* gave_up = &gave_up_word;
+  const uint32_t smem = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
+  // full and acc_empty count in the pair's first block, empty and acc_full in both
+  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kPairStages;
+  const uint32_t acc_full = empty + 8 * kPairStages, acc_empty = acc_full + 16;
+  const uint32_t drained = acc_empty + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank(), pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      tc::bar_init(full + 8 * s, 1);
+      tc::bar_init(empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::bar_init(acc_full + 8 * b, 1);
+      tc::bar_init(acc_empty + 8 * b, 16);  // a lane of each epilogue warp of the pair
+    }
+    for (int q = 0; q < 4; ++q) tc::bar_init(tc::smem_addr(&maxima.bar[q]), 2);
+    tc::bar_init(drained, 1);
+    *gave_up = 0;
+    tc::bar_init_fence();
+  }
+  if (warp == 1) tc::tmem_alloc<2>(tc::smem_addr(&tmem_base), 2 * kN);
+  tc::fence_before();
+  tc::cluster_sync();
+  tc::fence_after();
+  pdl_enter();
+  const uint32_t tmem = tmem_base;
+
+  if (warp == 0 && lane == 0) {
+    const uint32_t first_full = tc::cluster_addr(full, 0);
+    uint32_t it = 0;
+    bool live = true;
+    for (uint32_t t = pair; t < a.tiles && live; t += pairs) {
+      uint32_t which, row, tn;
+      tile_at(a, t, &which, &row, &tn);
+      for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
+        const uint32_t s = it % kPairStages;
+        if (!tc::bar_wait<true>(empty + 8 * s, (it / kPairStages & 1) ^ 1, gave_up)) {
+          live = false;
+          break;
+        }
+        if (rank == 0) tc::bar_expect(full + 8 * s, 2 * kPairStageBytes);
+        load_pair<MODE>(a, which, row, tn, k, rank, smem + s * kPairStageBytes, first_full + 8 * s);
+      }
+    }
+    if (!live && rank == 0) {
+      // leave no copy in flight behind: the last kPairStages blocks issued
+      const uint32_t first = it > kPairStages ? it - kPairStages : 0;
+      for (uint32_t i = first; i < it; ++i)
+        tc::bar_poll(full + 8 * (i % kPairStages), i / kPairStages & 1);
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    uint32_t it = 0, n = 0;
+    bool live = true;
+    for (uint32_t t = pair; t < a.tiles && live; t += pairs, ++n) {
+      const uint32_t buf = n & 1, acc = tmem + buf * kN;
+      if (!(live = tc::bar_wait<true>(acc_empty + 8 * buf, (n >> 1 & 1) ^ 1, gave_up))) break;
+      tc::fence_after();
+      for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
+        const uint32_t s = it % kPairStages;
+        if (!(live = tc::bar_wait<true>(full + 8 * s, it / kPairStages & 1, gave_up))) break;
+        tc::fence_after();
+        const uint32_t sa = smem + s * kPairStageBytes;
+        multiply_block<MODE, 2>(acc, sa, sa + kABytes, k == 0);
+        tc::mma_commit_pair(empty + 8 * s);
+      }
+      if (live) tc::mma_commit_pair(acc_full + 8 * buf);
+    }
+    if (!live) {  // leave no product in flight behind
+      tc::mma_commit_pair(drained);
+      tc::bar_poll(drained, 0);
+    }
+  } else if (warp >= 2) {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t first_empty = tc::cluster_addr(acc_empty, 0);
+    uint32_t n = 0, turn = 0;
+    for (uint32_t t = pair; t < a.tiles; t += pairs, ++n) {
+      const uint32_t buf = n & 1;
+      uint32_t which, row, tn;
+      tile_at(a, t, &which, &row, &tn);
+      // one lane polls, so that the warp stays whole for the tensor memory loads
+      bool got = true;
+      if (lane == 0) got = tc::bar_wait<true>(acc_full + 8 * buf, n >> 1 & 1, gave_up);
+      if (!__shfl_sync(~0u, got, 0)) break;
+      tc::fence_after();
+      epilogue<MODE, EPI>(a, tmem + buf * kN, which, (uint64_t)row + rank * kM + quarter * 32, tn,
+                          quarter, half, lane, slab + (warp - 2) * kSlab, &maxima, &turn, gave_up);
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive_cluster(first_empty + 8 * buf);
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  tc::cluster_sync();  // neither block leaves while the other reaches into it
+  tc::fence_after();
+  if (threadIdx.x == 0 && *gave_up) atomicOr(&g_wait_word, 1u);
+  if (warp == 1) tc::tmem_free<2>(tmem, 2 * kN);
+}
+
+// ---- few tiles: a cluster for each ------------------------------------------------------
+
+constexpr int kStages = 4;
+constexpr uint32_t kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kTileSmem = kStages * kStageBytes + 1024;  // + room to align to 1024
+constexpr int kTileThreads = 192;
+constexpr int kPartStride = kN + 4;  // floats: rows 16 bytes apart in the banks
+static_assert(kM * kPartStride * 4 <= kStages * kStageBytes, "partials reuse the buffers");
+
+// One K block of the tile at `row` into buffer `sa`, arriving on `bar`: one
+// thread.
+template <int MODE>
+__device__ __forceinline__ void load_block(const TileArgs& a, uint32_t which, uint32_t row,
                                            uint32_t tn, uint32_t k, uint32_t sa, uint32_t bar) {
   const uint32_t seg = k >= a.seg_blocks, sb = sa + kABytes;
-  const int k0 = (int)((k - seg * a.seg_blocks) * kK);
+  const int k0 = (int)((k - seg * a.seg_blocks) * kK), m0 = (int)row;
   tc::bar_expect(bar, kStageBytes);
   if constexpr (MODE == kGlu) {
-    tc::tma_load(sa, &a.a[0], k0, (int)(tm * kM), bar);
+    tc::tma_load(sa, &a.a[0], k0, m0, bar);
     tc::tma_load(sb, &a.b[0], k0, (int)(tn * (kN / 2)), bar);
     tc::tma_load(sb + kBBytes / 2, &a.b[1], k0, (int)(tn * (kN / 2)), bar);
   } else {
     if constexpr (MODE == kDx) {
-      tc::tma_load(sa, &a.a[seg], k0, (int)(tm * kM), bar);
+      tc::tma_load(sa, &a.a[seg], k0, m0, bar);
     } else {
-#pragma unroll
-      for (int j = 0; j < kM / 64; ++j)
-        tc::tma_load(sa + j * 8192, &a.a[which], (int)(tm * kM) + j * 64, k0, bar);
+      tc::tma_load(sa, &a.a[which], m0, k0, bar);
+      tc::tma_load(sa + 8192, &a.a[which], m0 + 64, k0, bar);
     }
 #pragma unroll
     for (int j = 0; j < kN / 64; ++j)
       tc::tma_load(sb + j * 8192, &a.b[seg], (int)(tn * kN) + j * 64, k0, bar);
   }
 }
-
-// The products of one K block: one thread.
-template <int MODE>
-__device__ __forceinline__ void multiply_block(uint32_t acc, uint32_t sa, bool first) {
-  constexpr bool a_mn = MODE == kDw, b_mn = MODE != kGlu;
-  constexpr uint32_t desc = tc::product_desc(kM, kN, a_mn, b_mn);
-  const uint32_t sb = sa + kABytes;
-#pragma unroll
-  for (int j = 0; j < kK / 16; ++j) {
-    // 16 K: 32 bytes along a row, or 16 rows
-    const uint64_t da = a_mn ? tc::operand(sa + j * 2048, 8192, 1024) : tc::operand(sa + j * 32, 16, 1024);
-    const uint64_t db = b_mn ? tc::operand(sb + j * 2048, 8192, 1024) : tc::operand(sb + j * 32, 16, 1024);
-    tc::mma(acc, da, db, desc, !first || j);
-  }
-}
-
-template <int MODE, int EPI>
-__global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant__ TileArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
-  __shared__ uint32_t tmem_base, slab[4 * kSlab];
-  __shared__ uint32_t gave_up_word;
-  volatile uint32_t* gave_up = &gave_up_word;
-  const uint32_t smem = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
-  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
-  const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16;
-  const uint32_t drained = acc_empty + 16;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      tc::bar_init(full + 8 * s, 1);
-      tc::bar_init(empty + 8 * s, 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      tc::bar_init(acc_full + 8 * b, 1);
-      tc::bar_init(acc_empty + 8 * b, 128);
-    }
-    tc::bar_init(drained, 1);
-    *gave_up = 0;
-    tc::bar_init_fence();
-  }
-  if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_base), 2 * kN);
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  pdl_enter();
-  const uint32_t tmem = tmem_base;
-
-  if (warp == 0 && lane == 0) {
-    uint32_t it = 0;
-    bool live = true;
-    for (uint32_t t = blockIdx.x; t < a.tiles && live; t += gridDim.x) {
-      uint32_t which, tm, tn;
-      tile_at(a, t, &which, &tm, &tn);
-      for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
-        const uint32_t s = it % kStages, bar = full + 8 * s;
-        if (!tc::bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, gave_up)) {
-          live = false;
-          break;
-        }
-        load_block<MODE>(a, which, tm, tn, k, smem + s * kStageBytes, bar);
-      }
-    }
-    if (!live) {
-      // leave no copy in flight behind: the last kStages blocks issued
-      const uint32_t first = it > kStages ? it - kStages : 0;
-      for (uint32_t i = first; i < it; ++i) tc::bar_poll(full + 8 * (i % kStages), i / kStages & 1);
-    }
-  } else if (warp == 1 && lane == 0) {
-    uint32_t it = 0, n = 0;
-    bool live = true;
-    for (uint32_t t = blockIdx.x; t < a.tiles && live; t += gridDim.x, ++n) {
-      const uint32_t buf = n & 1, acc = tmem + buf * kN;
-      if (!tc::bar_wait(acc_empty + 8 * buf, (n >> 1 & 1) ^ 1, gave_up)) {
-        live = false;
-        break;
-      }
-      tc::fence_after();
-      for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
-        const uint32_t s = it % kStages;
-        if (!tc::bar_wait(full + 8 * s, it / kStages & 1, gave_up)) {
-          live = false;
-          break;
-        }
-        tc::fence_after();
-        multiply_block<MODE>(acc, smem + s * kStageBytes, k == 0);
-        tc::mma_commit(empty + 8 * s);
-      }
-      if (live) tc::mma_commit(acc_full + 8 * buf);
-    }
-    if (!live) {  // leave no product in flight behind
-      tc::mma_commit(drained);
-      tc::bar_poll(drained, 0);
-    }
-  } else if (warp >= 2) {
-    uint32_t n = 0;
-    for (uint32_t t = blockIdx.x; t < a.tiles; t += gridDim.x, ++n) {
-      const uint32_t buf = n & 1;
-      uint32_t which, tm, tn;
-      tile_at(a, t, &which, &tm, &tn);
-      // one lane polls, so that the warp stays whole for the tensor memory loads
-      bool got = true;
-      if (lane == 0) got = tc::bar_wait(acc_full + 8 * buf, n >> 1 & 1, gave_up);
-      if (!__shfl_sync(~0u, got, 0)) break;
-      tc::fence_after();
-      epilogue<MODE, EPI>(a, tmem + buf * kN, which, tm, tn, warp & 3, lane, slab + (warp - 2) * kSlab);
-      tc::fence_before();
-      tc::bar_arrive(acc_empty + 8 * buf);
-    }
-  }
-  __syncwarp();
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  if (threadIdx.x == 0 && *gave_up) atomicOr(&g_wait_word, 1u);
-  if (warp == 1) tc::tmem_free(tmem, 2 * kN);
-}
-
-// ---- few tiles: a cluster for each ------------------------------------------------------
-
-constexpr int kPartStride = kN + 4;  // floats: rows 16 bytes apart in the banks
-static_assert(kM * kPartStride * 4 <= kStages * kStageBytes, "partials reuse the buffers");
 
 // One row of a tile, columns 4 * lane .. + 3 of each half (for kGlu, of g and
 // of u): whole warp.
@@ -458,8 +541,8 @@ __device__ __forceinline__ void finish_row(const TileArgs& a, uint32_t which, ui
   }
 }
 
-// Cluster blockIdx.x / a.splits takes that tile, its block of rank r the r-th
-// part of the K blocks.
+// Cluster blockIdx.x / a.splits takes one 128-row tile, its block of rank r the
+// r-th part of the K blocks.  Tiles of k_pairs (a.first and on) are two each.
 template <int MODE, int EPI>
 __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant__ TileArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -482,15 +565,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant
     *gave_up = 0;
     tc::bar_init_fence();
   }
-  if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_base), kN);
+  if (warp == 1) tc::tmem_alloc<1>(tc::smem_addr(&tmem_base), kN);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   pdl_enter();
   const uint32_t tmem = tmem_base;
   const uint32_t rank = tc::cluster_rank();
-  uint32_t which, tm, tn;
-  tile_at(a, blockIdx.x / a.splits, &which, &tm, &tn);
+  uint32_t which, row0, tn;
+  const uint32_t unit = blockIdx.x / a.splits, halves = a.tile_rows / kM;
+  tile_at(a, a.first + unit / halves, &which, &row0, &tn);
+  row0 += unit % halves * kM;
   const uint32_t k0 = (uint32_t)((uint64_t)a.blocks * rank / a.splits);
   const uint32_t k1 = (uint32_t)((uint64_t)a.blocks * (rank + 1) / a.splits);
 
@@ -500,7 +585,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant
     for (uint32_t k = k0; k < k1; ++k, ++it) {
       const uint32_t s = it % kStages;
       if (!(live = tc::bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, gave_up))) break;
-      load_block<MODE>(a, which, tm, tn, k, smem + s * kStageBytes, full + 8 * s);
+      load_block<MODE>(a, which, row0, tn, k, smem + s * kStageBytes, full + 8 * s);
     }
     if (!live) {
       const uint32_t first = it > kStages ? it - kStages : 0;
@@ -512,7 +597,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant
       const uint32_t s = it % kStages;
       if (!tc::bar_wait(full + 8 * s, it / kStages & 1, gave_up)) break;
       tc::fence_after();
-      multiply_block<MODE>(tmem, smem + s * kStageBytes, k == k0);
+      const uint32_t sa = smem + s * kStageBytes;
+      multiply_block<MODE, 1>(tmem, sa, sa + kABytes, k == k0);
       tc::mma_commit(empty + 8 * s);
     }
     // every product issued: the buffers are free and the sums complete
@@ -541,7 +627,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant
   const int height = kM / (int)a.splits;
   for (int r = warp; r < height; r += kTileThreads / 32) {
     const int at = (int)rank * height + r;
-    const uint64_t row = (uint64_t)tm * kM + at;
+    const uint64_t row = (uint64_t)row0 + at;
     if (row >= a.rows) break;
     float lo[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     const uint32_t addr = smem + (uint32_t)(at * kPartStride + 4 * lane) * 4;
@@ -556,7 +642,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant
   tc::cluster_sync();  // no block leaves while another reads its partials
   tc::fence_after();
   if (threadIdx.x == 0 && *gave_up) atomicOr(&g_wait_word, 1u);
-  if (warp == 1) tc::tmem_free(tmem, kN);
+  if (warp == 1) tc::tmem_free<1>(tmem, kN);
 }
 
 // ---- host side ------------------------------------------------------------------------
@@ -608,50 +694,112 @@ uint32_t ceil_div(uint32_t a, uint32_t b) { return (uint32_t)(((uint64_t)a + b -
 // Bytes all rows of the outputs allow.
 int out_width(const Mat& m, uint32_t rows, size_t es) { return store_width(m.p, rows > 1 ? m.ld * es : 0); }
 
-// Blocks to share a tile: as many as leave no SM without one (tiles * splits
-// <= SMs) and each at least kMinBlocks K blocks, at most 8 (a portable cluster).
-constexpr uint32_t kMinBlocks = 4;
-
-uint32_t split_of(const TileArgs& a, int sms) {
+// Blocks to share a tile: as many as leave no SM without one (units * splits
+// <= SMs) and each at least `least` K blocks, at most 8 (a portable cluster).
+uint32_t splits_of(uint32_t units, uint32_t blocks, int sms, uint32_t least) {
   uint32_t s = 1;
-  while (s < 8 && (uint64_t)a.tiles * s * 2 <= (uint64_t)sms && a.blocks >= s * 2 * kMinBlocks) s *= 2;
+  while (s < 8 && (uint64_t)units * s * 2 <= (uint64_t)sms && blocks >= s * 2 * least) s *= 2;
   return s;
 }
 
-template <int MODE, int EPI>
-cudaError_t run_tiles(TileArgs& a, cudaStream_t s) {
-  int sms = 0;
-  cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
-  a.splits = split_of(a, sms);
-  void (*kernel)(const TileArgs) = a.splits > 1 ? k_split<MODE, EPI> : k_tiles<MODE, EPI>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
-  if (e != cudaSuccess) return e;
+using Kernel = void (*)(const TileArgs);
+
+struct Launch {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.splits > 1 ? a.tiles * a.splits : std::min(a.tiles, (uint32_t)sms));
-  cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = kTileSmem;
-  cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = a.splits;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+
+  Launch(uint32_t grid, uint32_t threads, uint32_t smem, uint32_t cluster, cudaStream_t s) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+// Pairs of k_pairs the device holds at once (cached), after allowing both
+// kernels their shared memory.
+cudaError_t resident_pairs(Kernel pairs_kernel, Kernel split_kernel, uint32_t* pairs) {
+  static std::mutex mu;
+  static std::map<std::pair<Kernel, int>, uint32_t> cache;
+  int dev = 0, n = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_pair(pairs_kernel, dev);
+  const auto it = cache.find(key);
+  if (it != cache.end()) {
+    *pairs = it->second;
+    return cudaSuccess;
+  }
+  e = cudaFuncSetAttribute(pairs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+  if (e != cudaSuccess) return e;
+  Launch l(2, kPairThreads, kPairSmem, 2, nullptr);
+  l.cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(&n, pairs_kernel, &l.cfg);
+  if (e != cudaSuccess) return e;
+  *pairs = cache[key] = (uint32_t)std::max(n, 1);
+  return cudaSuccess;
 }
 
-// Tiles of `outputs` outputs of rows x cols, `width` columns a tile.
+constexpr uint32_t kMinBlocks = 4;    // K blocks worth a block of a cluster
+constexpr uint32_t kTailBlocks = 32;  // K blocks for which splitting the last turn is worth a launch
+
+// Rows in tiles of 128 as long as every tile finds an SM of its own; else in
+// tiles of 256, the last turn's split where they would leave most SMs idle.
+template <int MODE, int EPI>
+cudaError_t run_tiles(TileArgs& a, uint32_t outputs, cudaStream_t s) {
+  const Kernel pairs_kernel = k_pairs<MODE, EPI>, split_kernel = k_split<MODE, EPI>;
+  int sms = 0;
+  uint32_t pairs = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e == cudaSuccess) e = resident_pairs(pairs_kernel, split_kernel, &pairs);
+  if (e != cudaSuccess) return e;
+  const auto run_split = [&](uint32_t units) {
+    const Launch l(units * a.splits, kTileThreads, kTileSmem, a.splits, s);
+    return cudaLaunchKernelEx(&l.cfg, split_kernel, a);
+  };
+  const auto tiles = [&](uint32_t tile_rows) {
+    a.tile_rows = tile_rows;
+    a.tiles_m = ceil_div(a.rows, tile_rows);
+    return (uint64_t)a.tiles_m * a.tiles_n * outputs;
+  };
+  uint64_t n = tiles(kM);
+  if (n <= (uint64_t)sms) {
+    a.splits = splits_of((uint32_t)n, a.blocks, sms, kMinBlocks);
+    return run_split((uint32_t)n);
+  }
+  n = tiles(2 * kM);
+  if (n >= 1ull << 31) return cudaErrorInvalidValue;
+  const uint32_t rest = (uint32_t)(n % pairs);
+  a.tiles = (uint32_t)n;
+  if (n > pairs && rest) {
+    a.splits = splits_of(2 * rest, a.blocks, sms, kTailBlocks);
+    if (a.splits > 1) a.tiles -= rest;
+  }
+  const Launch l(2 * std::min(a.tiles, pairs), kPairThreads, kPairSmem, 2, s);
+  e = cudaLaunchKernelEx(&l.cfg, pairs_kernel, a);
+  if (e != cudaSuccess || a.tiles == n) return e;
+  a.first = a.tiles;
+  return run_split(2 * rest);
+}
+
+// An output of rows x cols, `width` columns a tile, of `products` products
+// over k.
 cudaError_t shape(TileArgs& a, uint32_t rows, uint32_t cols, uint32_t width, uint32_t k,
-                  uint32_t products, uint32_t outputs) {
+                  uint32_t products) {
   a.rows = rows, a.cols = cols;
-  a.tiles_m = ceil_div(rows, kM), a.tiles_n = ceil_div(cols, width);
-  const uint64_t tiles = (uint64_t)a.tiles_m * a.tiles_n * outputs;
+  a.tiles_n = ceil_div(cols, width);
   const uint64_t blocks = (uint64_t)ceil_div(k, kK) * products;
-  if (tiles >= 1ull << 31 || blocks >= 1ull << 31) return cudaErrorInvalidValue;
-  a.tiles = (uint32_t)tiles;
+  if (blocks >= 1ull << 31) return cudaErrorInvalidValue;
   a.seg_blocks = ceil_div(k, kK);
   a.blocks = (uint32_t)blocks;
   return cudaSuccess;
@@ -661,7 +809,7 @@ cudaError_t shape(TileArgs& a, uint32_t rows, uint32_t cols, uint32_t width, uin
 
 cudaError_t launch_glu(cr_act act, const GluArgs& g, cudaStream_t s) {
   TileArgs a = {};
-  cudaError_t e = shape(a, g.tokens, g.ffn, kN / 2, g.dim, 1, 1);
+  cudaError_t e = shape(a, g.tokens, g.ffn, kN / 2, g.dim, 1);
   if (e == cudaSuccess) e = encode(&a.a[0], g.x, g.tokens, g.dim, kM);
   if (e == cudaSuccess) e = encode(&a.b[0], g.wg, g.ffn, g.dim, kN / 2);
   if (e == cudaSuccess) e = encode(&a.b[1], g.wu, g.ffn, g.dim, kN / 2);
@@ -672,13 +820,14 @@ cudaError_t launch_glu(cr_act act, const GluArgs& g, cudaStream_t s) {
   a.width8 = 32;
   for (const Q8* q : {&g.g8, &g.u8})
     if (q->codes) a.width8 = std::min(a.width8, store_width(q->codes, g.tokens > 1 ? q->ld : 0));
-  return act == CR_ACT_SILU ? run_tiles<kGlu, CR_ACT_SILU>(a, s) : run_tiles<kGlu, CR_ACT_GELU>(a, s);
+  return act == CR_ACT_SILU ? run_tiles<kGlu, CR_ACT_SILU>(a, 1, s)
+                            : run_tiles<kGlu, CR_ACT_GELU>(a, 1, s);
 }
 
 cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& g, cudaStream_t s) {
   if (g.dx.p) {
     TileArgs a = {};
-    cudaError_t e = shape(a, g.tokens, g.dim, kN, g.ffn, 2, 1);
+    cudaError_t e = shape(a, g.tokens, g.dim, kN, g.ffn, 2);
     const Mat left[2] = {g.dg, g.du}, right[2] = {g.wg, g.wu};
     for (int k = 0; k < 2 && e == cudaSuccess; ++k) {
       e = encode(&a.a[k], left[k], g.tokens, g.ffn, kM);
@@ -687,12 +836,12 @@ cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     a.out[0] = g.dx;
     a.width = out_width(g.dx, g.tokens, 2);
-    if ((e = run_tiles<kDx, CR_BF16>(a, s)) != cudaSuccess) return e;
+    if ((e = run_tiles<kDx, CR_BF16>(a, 1, s)) != cudaSuccess) return e;
   }
   if (!g.dwg && !g.dwu) return cudaSuccess;
   TileArgs a = {};
   const uint32_t outputs = g.dwg && g.dwu ? 2 : 1;
-  cudaError_t e = shape(a, g.ffn, g.dim, kN, g.tokens, g.x_lo.p ? 2 : 1, outputs);
+  cudaError_t e = shape(a, g.ffn, g.dim, kN, g.tokens, g.x_lo.p ? 2 : 1);
   if (e != cudaSuccess) return e;
   a.width = 32;
   uint32_t n = 0;
@@ -705,7 +854,8 @@ cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& g, cudaStream_t s) {
   }
   if ((e = encode(&a.b[0], g.x, g.tokens, g.dim, kK)) != cudaSuccess) return e;
   if ((e = encode(&a.b[1], g.x_lo, g.tokens, g.dim, kK)) != cudaSuccess) return e;
-  return dw == CR_BF16 ? run_tiles<kDw, CR_BF16>(a, s) : run_tiles<kDw, CR_F32>(a, s);
+  return dw == CR_BF16 ? run_tiles<kDw, CR_BF16>(a, outputs, s)
+                       : run_tiles<kDw, CR_F32>(a, outputs, s);
 }
 
 cudaError_t glu_wait_word(bool clear, unsigned int* word) {

@@ -377,6 +377,29 @@ def test_glu_integers_are_exact(tokens, dim, ffn):
         assert torch.equal(codes, codes2) and torch.equal(scales, scales2)
 
 
+# More tiles than SMs, with ragged edges, and (the last two) few in the last turn.
+MANY_TILES = [(2600, 72, 3000), (1531, 1001, 2731), (1800, 4100, 1664), (2000, 2570, 2100)]
+
+
+@pytest.mark.parametrize("tokens,dim,ffn", MANY_TILES)
+def test_glu_many_tiles(tokens, dim, ffn):
+    check_glu(tokens, dim, ffn, "silu", 0, 0)
+
+
+@pytest.mark.parametrize("held,dw_dt", [("full", "f32"), ("q8", "bf16")])
+@pytest.mark.parametrize("tokens,dim,ffn", MANY_TILES)
+def test_glu_backward_many_tiles(tokens, dim, ffn, held, dw_dt):
+    check_glu_backward(tokens, dim, ffn, held, dw_dt, "gelu", 0, 0)
+
+
+def test_glu_integers_are_exact_with_many_tiles():
+    test_glu_integers_are_exact(3000, 256, 1500)
+
+
+def test_glu_rows_and_columns_stay_apart_with_many_tiles():
+    test_glu_rows_and_columns_stay_apart(20000)
+
+
 @pytest.mark.parametrize("tokens", [3, 130])
 def test_glu_rows_and_columns_stay_apart(tokens):
     """NaN in one token reaches that token alone, NaN in one weight row that column alone."""
@@ -545,6 +568,11 @@ def test_gradients_against_differences():
         want = (loss(*up) - loss(*dn)) / (2 * h)
         terms = grad.double() * d
         assert abs(float(terms.sum()) - want) <= 4 * (2.0 ** -4 + 4 * R.U16) * float(terms.norm()), n
+
+
+def test_no_wait_ran_out():
+    """Runs after the tests of the block's kernels: none of their waits gave up."""
+    assert cr.cr_glu_wait_word() == 0
 
 
 # ---- streams, repeats, prepared calls and graphs ----------------------------------------------------
