@@ -314,7 +314,8 @@ cr_status cr_glu_act_backward(const void* da, size_t ldda, const cr_q8* g8, cons
   if (tokens == 0 || ffn == 0 || (!dg && !du && !a_out)) return ok();
   ActBackArgs k = {mat(da, ldda), mat(dg, lddg), mat(du, lddu), mat(a_out, lda),
                    q8_of(g8),     q8_of(u8),     tokens,        (uint32_t)ffn};
-  return launched(launch_act_back(act, k, a.vec(), stream_of(stream)), "cr_glu_act_backward");
+  return launched(launch_act_back(act, k, nullptr, a.vec(), stream_of(stream)),
+                  "cr_glu_act_backward");
 }
 
 size_t cr_glu_workspace_bytes(size_t tokens, size_t dim, size_t ffn) {
@@ -413,11 +414,17 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr
   uint16_t* ws = static_cast<uint16_t*>(workspace);
   const Mat dg = {ws, padded_ld(ffn)};
   const Mat du = {ws + padded(tokens, ffn), padded_ld(ffn)};
+  uint16_t* const xs = ws + 2 * padded(tokens, ffn);
   cudaError_t e = cudaSuccess;
+  const SplitArgs split = {q8_of(x8), Mat{xs, padded_ld(dim)},
+                           Mat{xs + padded(tokens, dim), padded_ld(dim)}, tokens, (uint32_t)dim,
+                           xa.vec()};
+  const bool splits = dw && x8 && tokens && dim;
   if (tokens && ffn) {
     ActBackArgs k = {mat(da, ldda), dg, du, mat(a_out, lda), q8_of(g8), q8_of(u8), tokens, (uint32_t)ffn};
     if (!dx && !dw) k.dg = k.du = Mat{nullptr, 0};
-    if (k.dg.p || k.a.p) e = launch_act_back(act, k, vec_with(act_vec, ws), s);
+    if (k.dg.p || k.a.p)
+      e = launch_act_back(act, k, splits ? &split : nullptr, vec_with(act_vec, ws), s);
     if (e != cudaSuccess) return cuda_fail(e, "cr_glu_backward: activation");
   }
   if (dim == 0 || (!dw && !(dx && tokens))) return ok();
@@ -425,12 +432,10 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr
   k.dg = dg, k.du = du;
   k.x = mat(x, ldx);
   k.wg = mat(wg, ldwg), k.wu = mat(wu, ldwu);
-  ws += 2 * padded(tokens, ffn);
+  ws = xs;
   CopyBf16 copies = {};
-  if (dw && x8 && tokens) {
-    k.x = Mat{ws, padded_ld(dim)};
-    k.x_lo = Mat{ws + padded(tokens, dim), padded_ld(dim)};
-    e = launch_q8_split(q8_of(x8), k.x, k.x_lo, tokens, (uint32_t)dim, vec_with(xa.vec(), ws), s);
+  if (splits) {
+    k.x = split.hi, k.x_lo = split.lo;
   } else if (dw) {
     operand(&copies, &k.x, tokens, dim, ws);
   }

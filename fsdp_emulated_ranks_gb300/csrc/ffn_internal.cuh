@@ -71,6 +71,15 @@ struct ActBackArgs {
   uint32_t cols;
 };
 
+// The values q stands for as bf16 hi + lo (lo: what the rounding of hi left).
+struct SplitArgs {
+  Q8 q;
+  Mat hi, lo;
+  uint64_t rows;
+  uint32_t cols;
+  int vec;  // the accesses q allows
+};
+
 // Operands of the products (x, wg, wu, dg, du): 16-byte aligned rows.
 struct GluArgs {
   Mat x, wg, wu, a;
@@ -94,9 +103,6 @@ cudaError_t launch_q8_store(cr_dtype d, const Mat& x, const Q8& q, uint64_t rows
                             int vec, cudaStream_t s);
 cudaError_t launch_q8_load(cr_dtype d, const Q8& q, const Mat& x, uint64_t rows, uint32_t cols,
                            int vec, cudaStream_t s);
-// The values q stands for as bf16 hi + lo (lo: what the rounding of hi left).
-cudaError_t launch_q8_split(const Q8& q, const Mat& hi, const Mat& lo, uint64_t rows, uint32_t cols,
-                            int vec, cudaStream_t s);
 // dst = src for up to three bf16 matrices at any alignment, in one launch.
 struct CopyBf16 {
   struct One {
@@ -109,7 +115,9 @@ struct CopyBf16 {
 };
 void add_copy(CopyBf16* c, const Mat& src, const Mat& dst, uint64_t rows, uint32_t cols);
 cudaError_t launch_copy_bf16(const CopyBf16& c, cudaStream_t s);
-cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, int vec, cudaStream_t s);
+// The gate's backward pass and, in the same launch, x's split (or nullptr).
+cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, const SplitArgs* x, int vec,
+                            cudaStream_t s);
 cudaError_t launch_glu(cr_act act, const GluArgs& a, cudaStream_t s);
 // Whether the block's call is one for k_glu_few.cu: few tokens, whose x fits
 // in shared memory, and no checkpoints (keeps).  Operands at any alignment;

@@ -11,20 +11,21 @@
 // of kDx) or rows of M or N (W of kDx, everything of kDw), which the tensor
 // cores take directly, so nothing is transposed.
 //
-// k_pairs, for many tiles: persistent pairs of blocks (cta_group::2), a tile
-// 256 x 256.  Each block of a pair loads its 128 rows of A and its 128 columns
-// of B and holds the accumulator of its rows, so that a byte loaded feeds
-// twice the products that a 128 x 256 tile's would.  Warp 0 loads by TMA into
-// a ring of kPairStages buffers, warp 1 of the first block issues the products
-// into one of two accumulators in tensor memory, warps 2-9 read the other one
-// out and write the results.  TMA fills rows and columns outside a matrix with
-// zeros, so ragged sizes need no masks before the epilogue.
+// k_tiles, for many tiles: persistent blocks, a tile 128 x 256.  Warp 0 loads by
+// TMA into a ring of kStages buffers, warp 1 issues the products into one of
+// two accumulators in tensor memory, warps 2-9 read the other one out and write
+// the results.  TMA fills rows and columns outside a matrix with zeros, so
+// ragged sizes need no masks before the epilogue.
 //
-// k_split, where the tiles (128 x 256) are too few for the SMs and for the
-// tiles of k_pairs that would leave most SMs idle in its last turn: the blocks
-// of a cluster share one tile.  Each takes a range of its K, leaves its partial
+// k_split, where the tiles are too few for the SMs, and for the tiles that
+// would leave most SMs idle in the last turn of k_tiles: the blocks of a
+// cluster share one tile.  Each takes a range of its K, leaves its partial
 // sums in its own shared memory, and then finishes a range of the tile's rows,
-// reading the partials of all in rank order.
+// reading the partials of all in rank order.  k_split_back runs the tiles of dx
+// and of dW in one launch.
+//
+// Both let the next kernel's blocks onto their SMs only as they end: a waiting
+// block beside them would have nothing to do for most of their time.
 //
 // Every wait is bounded (tc.cuh); a block that gives up sets g_wait_word and
 // leaves.
@@ -45,10 +46,14 @@ namespace {
 
 enum TileMode { kGlu = 0, kDx = 1, kDw = 2 };
 
-constexpr int kM = 128;       // rows of a block's tile
+constexpr int kM = 128;       // rows of a tile
 constexpr int kN = 256;       // accumulator columns of a tile
 constexpr int kK = 64;        // K of a block: 128 bytes of bf16
+constexpr int kStages = 4;
 constexpr uint32_t kABytes = kM * kK * 2, kBBytes = kN * kK * 2;
+constexpr uint32_t kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kTileSmem = kStages * kStageBytes + 1024;  // + room to align to 1024
+constexpr int kTileThreads = 320;
 
 struct TileArgs {
   CUtensorMap a[2], b[2];
@@ -57,9 +62,8 @@ struct TileArgs {
   uint32_t rows, cols;        // of an output
   uint32_t seg_blocks;        // K blocks of one product
   uint32_t blocks;            // K blocks of a tile: one or two products
-  uint32_t tile_rows;         // kM, or 2 kM with k_pairs
   uint32_t tiles_m, tiles_n;  // of an output
-  uint32_t tiles;             // k_pairs: tiles 0 .. tiles - 1 of all outputs
+  uint32_t tiles;             // k_tiles: tiles 0 .. tiles - 1 of all outputs
   uint32_t first;             // k_split: its first tile
   uint32_t splits;            // k_split: blocks that share a tile, a power of two
   int width;                  // bytes of the output stores all rows allow: 32, 16 or 0
@@ -151,17 +155,18 @@ __device__ __forceinline__ void st_codes(const Q8& q, uint64_t row0, uint32_t c,
   st_square(q.codes, q.ld, row0, c, rows, cols, width, lane, w, slab);
 }
 
-// Tile `t`: its output, first row and tile column.  Tile rows are walked 1024
-// rows at a time, so that their operands stay in L2.
+// Tile `t`: its output, first row and tile column.  Tile rows are walked 8 at a
+// time, so that their operands stay in L2.
 __device__ __forceinline__ void tile_at(const TileArgs& a, uint32_t t, uint32_t* which,
                                         uint32_t* row, uint32_t* tn) {
-  const uint32_t per_out = a.tiles_m * a.tiles_n, walk = 8 * kM / a.tile_rows;
+  constexpr uint32_t walk = 8;
+  const uint32_t per_out = a.tiles_m * a.tiles_n;
   *which = t / per_out;
   t -= *which * per_out;
   const uint32_t group = t / (walk * a.tiles_n), first = group * walk;
   const uint32_t height = min(walk, a.tiles_m - first);
   t -= group * walk * a.tiles_n;
-  *row = (first + t % height) * a.tile_rows;
+  *row = (first + t % height) * kM;
   *tn = t / height;
 }
 
@@ -280,170 +285,18 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32
 }
 
 // The products of one K block, A at sa and B at sb: one thread.
-template <int MODE, int GROUP>
+template <int MODE>
 __device__ __forceinline__ void multiply_block(uint32_t acc, uint32_t sa, uint32_t sb, bool first) {
   constexpr bool a_mn = MODE == kDw, b_mn = MODE != kGlu;
-  constexpr uint32_t desc = tc::product_desc(GROUP * kM, kN, a_mn, b_mn);
+  constexpr uint32_t desc = tc::product_desc(kM, kN, a_mn, b_mn);
 #pragma unroll
   for (int j = 0; j < kK / 16; ++j) {
     // 16 K: 32 bytes along a row, or 16 rows
     const uint64_t da = a_mn ? tc::operand(sa + j * 2048, 8192, 1024) : tc::operand(sa + j * 32, 16, 1024);
     const uint64_t db = b_mn ? tc::operand(sb + j * 2048, 8192, 1024) : tc::operand(sb + j * 32, 16, 1024);
-    tc::mma<GROUP>(acc, da, db, desc, !first || j);
+    tc::mma(acc, da, db, desc, !first || j);
   }
 }
-
-// ---- many tiles: persistent pairs -------------------------------------------------------
-
-constexpr int kPairStages = 6;
-constexpr uint32_t kPairStageBytes = 2 * kABytes;  // a block's half of A and of B: the same size
-constexpr uint32_t kPairSmem = kPairStages * kPairStageBytes + 1024;  // + room to align to 1024
-constexpr int kPairThreads = 320;
-static_assert(kABytes * 2 == kBBytes, "half of B is as large as a block's A");
-
-// This block's part of one K block of the pair's tile at `row`, into buffer
-// `sa`; bytes count on `bar`, the first block's.  One thread.
-template <int MODE>
-__device__ __forceinline__ void load_pair(const TileArgs& a, uint32_t which, uint32_t row,
-                                          uint32_t tn, uint32_t k, uint32_t rank, uint32_t sa,
-                                          uint32_t bar) {
-  const uint32_t seg = k >= a.seg_blocks, sb = sa + kABytes;
-  const int k0 = (int)((k - seg * a.seg_blocks) * kK), m0 = (int)(row + rank * kM);
-  if constexpr (MODE == kGlu) {
-    tc::tma_load_pair(sa, &a.a[0], k0, m0, bar);
-    // columns 0-127 of the accumulator are g's, 128-255 u's
-    tc::tma_load_pair(sb, &a.b[rank], k0, (int)(tn * (kN / 2)), bar);
-  } else {
-    if constexpr (MODE == kDx) {
-      tc::tma_load_pair(sa, &a.a[seg], k0, m0, bar);
-    } else {
-      tc::tma_load_pair(sa, &a.a[which], m0, k0, bar);
-      tc::tma_load_pair(sa + 8192, &a.a[which], m0 + 64, k0, bar);
-    }
-    const int n0 = (int)(tn * kN + rank * (kN / 2));
-    tc::tma_load_pair(sb, &a.b[seg], n0, k0, bar);
-    tc::tma_load_pair(sb + 8192, &a.b[seg], n0 + 64, k0, bar);
-  }
-}
-
-template <int MODE, int EPI>
-__global__ void __launch_bounds__(kPairThreads, 1)
-    k_pairs(const __grid_constant__ TileArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kPairStages + 5];
-  __shared__ Maxima maxima;
-  __shared__ uint32_t tmem_base, slab[8 * kSlab];
-  __shared__ uint32_t gave_up_word;
-  volatile uint32_t* gave_up = &gave_up_word;
-  const uint32_t smem = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
-  // full and acc_empty count in the pair's first block, empty and acc_full in both
-  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kPairStages;
-  const uint32_t acc_full = empty + 8 * kPairStages, acc_empty = acc_full + 16;
-  const uint32_t drained = acc_empty + 16;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = tc::cluster_rank(), pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
-      tc::bar_init(full + 8 * s, 1);
-      tc::bar_init(empty + 8 * s, 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      tc::bar_init(acc_full + 8 * b, 1);
-      tc::bar_init(acc_empty + 8 * b, 16);  // a lane of each epilogue warp of the pair
-    }
-    for (int q = 0; q < 4; ++q) tc::bar_init(tc::smem_addr(&maxima.bar[q]), 2);
-    tc::bar_init(drained, 1);
-    *gave_up = 0;
-    tc::bar_init_fence();
-  }
-  if (warp == 1) tc::tmem_alloc<2>(tc::smem_addr(&tmem_base), 2 * kN);
-  tc::fence_before();
-  tc::cluster_sync();
-  tc::fence_after();
-  pdl_enter();
-  const uint32_t tmem = tmem_base;
-
-  if (warp == 0 && lane == 0) {
-    const uint32_t first_full = tc::cluster_addr(full, 0);
-    uint32_t it = 0;
-    bool live = true;
-    for (uint32_t t = pair; t < a.tiles && live; t += pairs) {
-      uint32_t which, row, tn;
-      tile_at(a, t, &which, &row, &tn);
-      for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
-        const uint32_t s = it % kPairStages;
-        if (!tc::bar_wait<true>(empty + 8 * s, (it / kPairStages & 1) ^ 1, gave_up)) {
-          live = false;
-          break;
-        }
-        if (rank == 0) tc::bar_expect(full + 8 * s, 2 * kPairStageBytes);
-        load_pair<MODE>(a, which, row, tn, k, rank, smem + s * kPairStageBytes, first_full + 8 * s);
-      }
-    }
-    if (!live && rank == 0) {
-      // leave no copy in flight behind: the last kPairStages blocks issued
-      const uint32_t first = it > kPairStages ? it - kPairStages : 0;
-      for (uint32_t i = first; i < it; ++i)
-        tc::bar_poll(full + 8 * (i % kPairStages), i / kPairStages & 1);
-    }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    uint32_t it = 0, n = 0;
-    bool live = true;
-    for (uint32_t t = pair; t < a.tiles && live; t += pairs, ++n) {
-      const uint32_t buf = n & 1, acc = tmem + buf * kN;
-      if (!(live = tc::bar_wait<true>(acc_empty + 8 * buf, (n >> 1 & 1) ^ 1, gave_up))) break;
-      tc::fence_after();
-      for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
-        const uint32_t s = it % kPairStages;
-        if (!(live = tc::bar_wait<true>(full + 8 * s, it / kPairStages & 1, gave_up))) break;
-        tc::fence_after();
-        const uint32_t sa = smem + s * kPairStageBytes;
-        multiply_block<MODE, 2>(acc, sa, sa + kABytes, k == 0);
-        tc::mma_commit_pair(empty + 8 * s);
-      }
-      if (live) tc::mma_commit_pair(acc_full + 8 * buf);
-    }
-    if (!live) {  // leave no product in flight behind
-      tc::mma_commit_pair(drained);
-      tc::bar_poll(drained, 0);
-    }
-  } else if (warp >= 2) {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t first_empty = tc::cluster_addr(acc_empty, 0);
-    uint32_t n = 0, turn = 0;
-    for (uint32_t t = pair; t < a.tiles; t += pairs, ++n) {
-      const uint32_t buf = n & 1;
-      uint32_t which, row, tn;
-      tile_at(a, t, &which, &row, &tn);
-      // one lane polls, so that the warp stays whole for the tensor memory loads
-      bool got = true;
-      if (lane == 0) got = tc::bar_wait<true>(acc_full + 8 * buf, n >> 1 & 1, gave_up);
-      if (!__shfl_sync(~0u, got, 0)) break;
-      tc::fence_after();
-      epilogue<MODE, EPI>(a, tmem + buf * kN, which, (uint64_t)row + rank * kM + quarter * 32, tn,
-                          quarter, half, lane, slab + (warp - 2) * kSlab, &maxima, &turn, gave_up);
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive_cluster(first_empty + 8 * buf);
-    }
-  }
-  __syncwarp();
-  tc::fence_before();
-  tc::cluster_sync();  // neither block leaves while the other reaches into it
-  tc::fence_after();
-  if (threadIdx.x == 0 && *gave_up) atomicOr(&g_wait_word, 1u);
-  if (warp == 1) tc::tmem_free<2>(tmem, 2 * kN);
-}
-
-// ---- few tiles: a cluster for each ------------------------------------------------------
-
-constexpr int kStages = 4;
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr uint32_t kTileSmem = kStages * kStageBytes + 1024;  // + room to align to 1024
-constexpr int kTileThreads = 192;
-constexpr int kPartStride = kN + 4;  // floats: rows 16 bytes apart in the banks
-static_assert(kM * kPartStride * 4 <= kStages * kStageBytes, "partials reuse the buffers");
 
 // One K block of the tile at `row` into buffer `sa`, arriving on `bar`: one
 // thread.
@@ -469,6 +322,113 @@ __device__ __forceinline__ void load_block(const TileArgs& a, uint32_t which, ui
       tc::tma_load(sb + j * 8192, &a.b[seg], (int)(tn * kN) + j * 64, k0, bar);
   }
 }
+
+// ---- many tiles: persistent blocks ------------------------------------------------------
+
+template <int MODE, int EPI>
+__global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant__ TileArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+  __shared__ Maxima maxima;
+  __shared__ uint32_t tmem_base, slab[8 * kSlab];
+  __shared__ uint32_t gave_up_word;
+  volatile uint32_t* gave_up = &gave_up_word;
+  const uint32_t smem = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
+  const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16;
+  const uint32_t drained = acc_empty + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::bar_init(full + 8 * s, 1);
+      tc::bar_init(empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::bar_init(acc_full + 8 * b, 1);
+      tc::bar_init(acc_empty + 8 * b, 8);  // a lane of each epilogue warp
+    }
+    for (int q = 0; q < 4; ++q) tc::bar_init(tc::smem_addr(&maxima.bar[q]), 2);
+    tc::bar_init(drained, 1);
+    *gave_up = 0;
+    tc::bar_init_fence();
+  }
+  if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_base), 2 * kN);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  pdl_wait_prerequisites();
+  const uint32_t tmem = tmem_base;
+
+  if (warp == 0 && lane == 0) {
+    uint32_t it = 0;
+    bool live = true;
+    for (uint32_t t = blockIdx.x; t < a.tiles && live; t += gridDim.x) {
+      uint32_t which, row, tn;
+      tile_at(a, t, &which, &row, &tn);
+      for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
+        const uint32_t s = it % kStages;
+        if (!(live = tc::bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, gave_up))) break;
+        load_block<MODE>(a, which, row, tn, k, smem + s * kStageBytes, full + 8 * s);
+      }
+    }
+    if (!live) {
+      // leave no copy in flight behind: the last kStages blocks issued
+      const uint32_t first = it > kStages ? it - kStages : 0;
+      for (uint32_t i = first; i < it; ++i) tc::bar_poll(full + 8 * (i % kStages), i / kStages & 1);
+    }
+  } else if (warp == 1 && lane == 0) {
+    uint32_t it = 0, n = 0;
+    bool live = true;
+    for (uint32_t t = blockIdx.x; t < a.tiles && live; t += gridDim.x, ++n) {
+      const uint32_t buf = n & 1, acc = tmem + buf * kN;
+      if (!(live = tc::bar_wait(acc_empty + 8 * buf, (n >> 1 & 1) ^ 1, gave_up))) break;
+      tc::fence_after();
+      for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
+        const uint32_t s = it % kStages;
+        if (!(live = tc::bar_wait(full + 8 * s, it / kStages & 1, gave_up))) break;
+        tc::fence_after();
+        const uint32_t sa = smem + s * kStageBytes;
+        multiply_block<MODE>(acc, sa, sa + kABytes, k == 0);
+        tc::mma_commit(empty + 8 * s);
+      }
+      if (live) tc::mma_commit(acc_full + 8 * buf);
+    }
+    if (!live) {  // leave no product in flight behind
+      tc::mma_commit(drained);
+      tc::bar_poll(drained, 0);
+    }
+  } else if (warp >= 2) {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint32_t n = 0, turn = 0;
+    for (uint32_t t = blockIdx.x; t < a.tiles; t += gridDim.x, ++n) {
+      const uint32_t buf = n & 1;
+      uint32_t which, row, tn;
+      tile_at(a, t, &which, &row, &tn);
+      // one lane polls, so that the warp stays whole for the tensor memory loads
+      bool got = true;
+      if (lane == 0) got = tc::bar_wait(acc_full + 8 * buf, n >> 1 & 1, gave_up);
+      if (!__shfl_sync(~0u, got, 0)) break;
+      tc::fence_after();
+      epilogue<MODE, EPI>(a, tmem + buf * kN, which, (uint64_t)row + quarter * 32, tn, quarter,
+                          half, lane, slab + (warp - 2) * kSlab, &maxima, &turn, gave_up);
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (threadIdx.x == 0 && *gave_up) atomicOr(&g_wait_word, 1u);
+  if (warp == 1) tc::tmem_free(tmem, 2 * kN);
+}
+
+// ---- few tiles: a cluster for each ------------------------------------------------------
+
+constexpr int kPartStride = kN + 4;  // floats: rows 16 bytes apart in the banks
+static_assert(kM * kPartStride * 4 <= kStages * kStageBytes, "partials reuse the buffers");
 
 // One row of a tile, columns 4 * lane .. + 3 of each half (for kGlu, of g and
 // of u): whole warp.
@@ -541,43 +501,34 @@ __device__ __forceinline__ void finish_row(const TileArgs& a, uint32_t which, ui
   }
 }
 
-// Cluster blockIdx.x / a.splits takes one 128-row tile, its block of rank r the
-// r-th part of the K blocks.  Tiles of k_pairs (a.first and on) are two each.
+// What every kernel of split tiles keeps in shared memory beside its buffers.
+struct SplitShared {
+  uint64_t bars[2 * kStages + 1];
+  uint32_t tmem_base;
+  uint32_t gave_up;
+};
+
+// Block `rank` of the a.splits that share tile a.first + `unit`: the rank-th part of its K blocks, then the rank-th part of its rows.  They are
+// blocks `peer` .. + splits - 1 of the cluster.  A unit past the last (`units`)
+// only takes part in the cluster's barriers.
 template <int MODE, int EPI>
-__global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant__ TileArgs a) {
+__device__ __forceinline__ void split_tile(const TileArgs& a, SplitShared* sh, uint32_t unit,
+                                           uint32_t units, uint32_t rank, uint32_t peer) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 1];
-  __shared__ uint32_t tmem_base;
-  __shared__ uint32_t gave_up_word;
-  volatile uint32_t* gave_up = &gave_up_word;
+  volatile uint32_t* gave_up = &sh->gave_up;
   const uint32_t smem = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
   float* part = reinterpret_cast<float*>(smem_raw + (smem - tc::smem_addr(smem_raw)));
-  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
+  const uint32_t full = tc::smem_addr(sh->bars), empty = full + 8 * kStages;
   const uint32_t acc_full = empty + 8 * kStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      tc::bar_init(full + 8 * s, 1);
-      tc::bar_init(empty + 8 * s, 1);
-    }
-    tc::bar_init(acc_full, 1);
-    *gave_up = 0;
-    tc::bar_init_fence();
+  const uint32_t tmem = sh->tmem_base;
+  const bool mine = unit < units;
+  uint32_t which = 0, row0 = 0, tn = 0, k0 = 0, k1 = 0;
+  if (mine) {
+    tile_at(a, a.first + unit, &which, &row0, &tn);
+    k0 = (uint32_t)((uint64_t)a.blocks * rank / a.splits);
+    k1 = (uint32_t)((uint64_t)a.blocks * (rank + 1) / a.splits);
   }
-  if (warp == 1) tc::tmem_alloc<1>(tc::smem_addr(&tmem_base), kN);
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  pdl_enter();
-  const uint32_t tmem = tmem_base;
-  const uint32_t rank = tc::cluster_rank();
-  uint32_t which, row0, tn;
-  const uint32_t unit = blockIdx.x / a.splits, halves = a.tile_rows / kM;
-  tile_at(a, a.first + unit / halves, &which, &row0, &tn);
-  row0 += unit % halves * kM;
-  const uint32_t k0 = (uint32_t)((uint64_t)a.blocks * rank / a.splits);
-  const uint32_t k1 = (uint32_t)((uint64_t)a.blocks * (rank + 1) / a.splits);
 
   if (warp == 0 && lane == 0) {
     uint32_t it = 0;
@@ -588,6 +539,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant
       load_block<MODE>(a, which, row0, tn, k, smem + s * kStageBytes, full + 8 * s);
     }
     if (!live) {
+      // leave no copy in flight behind: the last kStages blocks issued
       const uint32_t first = it > kStages ? it - kStages : 0;
       for (uint32_t i = first; i < it; ++i) tc::bar_poll(full + 8 * (i % kStages), i / kStages & 1);
     }
@@ -598,7 +550,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant
       if (!tc::bar_wait(full + 8 * s, it / kStages & 1, gave_up)) break;
       tc::fence_after();
       const uint32_t sa = smem + s * kStageBytes;
-      multiply_block<MODE, 1>(tmem, sa, sa + kABytes, k == k0);
+      multiply_block<MODE>(tmem, sa, sa + kABytes, k == k0);
       tc::mma_commit(empty + 8 * s);
     }
     // every product issued: the buffers are free and the sums complete
@@ -606,15 +558,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant
     tc::bar_poll(acc_full, 0);
   }
   __syncwarp();
-  if (warp >= 2) {
+  if (warp >= 2 && mine) {
     if (lane == 0) tc::bar_wait(acc_full, 0, gave_up);
     __syncwarp();
     tc::fence_after();
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
     float* row = part + (quarter * 32 + lane) * kPartStride;
     const bool any = k1 > k0;
 #pragma unroll 1
-    for (int c = 0; c < kN; c += 32) {
+    for (int c = half * 128; c < half * 128 + 128; c += 32) {
       float v[32];
       ld_acc(tmem + ((uint32_t)(quarter * 32) << 16) + c, any, v);
 #pragma unroll
@@ -623,26 +575,94 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant
     }
     tc::fence_before();
   }
+  __syncwarp();
   tc::cluster_sync();
-  const int height = kM / (int)a.splits;
-  for (int r = warp; r < height; r += kTileThreads / 32) {
-    const int at = (int)rank * height + r;
-    const uint64_t row = (uint64_t)row0 + at;
-    if (row >= a.rows) break;
-    float lo[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const uint32_t addr = smem + (uint32_t)(at * kPartStride + 4 * lane) * 4;
-    for (uint32_t p = 0; p < a.splits; ++p) {
-      const uint32_t from = tc::cluster_addr(addr, p);
-      const float4 x = tc::cluster_ld4(from), y = tc::cluster_ld4(from + kN / 2 * 4);
-      lo[0] += x.x, lo[1] += x.y, lo[2] += x.z, lo[3] += x.w;
-      hi[0] += y.x, hi[1] += y.y, hi[2] += y.z, hi[3] += y.w;
+  if (mine) {
+    // kRows rows a warp at a time, so that as many reads are in flight
+    constexpr int kRows = 4, kWarps = kTileThreads / 32;
+    const int height = kM / (int)a.splits, at0 = (int)rank * height;
+    for (int r = warp; r < height; r += kRows * kWarps) {
+      float4 lo[kRows], hi[kRows];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) lo[j] = hi[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (uint32_t p = 0; p < a.splits; ++p) {
+        const uint32_t from = tc::cluster_addr(smem, peer + p) + 16 * lane;
+        float4 x[kRows], y[kRows];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          // rows past this block's part are read again from its last, and dropped
+          const int at = at0 + min(r + j * kWarps, height - 1);
+          x[j] = tc::cluster_ld4(from + (uint32_t)(at * kPartStride) * 4);
+          y[j] = tc::cluster_ld4(from + (uint32_t)(at * kPartStride + kN / 2) * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          lo[j].x += x[j].x, lo[j].y += x[j].y, lo[j].z += x[j].z, lo[j].w += x[j].w;
+          hi[j].x += y[j].x, hi[j].y += y[j].y, hi[j].z += y[j].z, hi[j].w += y[j].w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const uint64_t row = (uint64_t)row0 + at0 + r + j * kWarps;
+        if (r + j * kWarps < height && row < a.rows)
+          finish_row<MODE, EPI>(a, which, row, tn, lane, &lo[j].x, &hi[j].x);
+      }
     }
-    finish_row<MODE, EPI>(a, which, row, tn, lane, lo, hi);
   }
+  __syncwarp();
   tc::cluster_sync();  // no block leaves while another reads its partials
+}
+
+__device__ __forceinline__ void split_begin(SplitShared* sh) {
+  if (threadIdx.x == 0) {
+    const uint32_t bars = tc::smem_addr(sh->bars);
+    for (int b = 0; b < 2 * kStages + 1; ++b) tc::bar_init(bars + 8 * b, 1);
+    sh->gave_up = 0;
+    tc::bar_init_fence();
+  }
+  if (threadIdx.x >> 5 == 1) tc::tmem_alloc(tc::smem_addr(&sh->tmem_base), kN);
+  tc::fence_before();
+  __syncthreads();
   tc::fence_after();
-  if (threadIdx.x == 0 && *gave_up) atomicOr(&g_wait_word, 1u);
-  if (warp == 1) tc::tmem_free<1>(tmem, kN);
+  pdl_wait_prerequisites();
+}
+
+__device__ __forceinline__ void split_end(SplitShared* sh) {
+  tc::fence_after();
+  if (threadIdx.x == 0 && sh->gave_up) atomicOr(&g_wait_word, 1u);
+  if (threadIdx.x >> 5 == 1) tc::tmem_free(sh->tmem_base, kN);
+}
+
+// A cluster of a.splits blocks for each tile from a.first on.
+template <int MODE, int EPI>
+__global__ void __launch_bounds__(kTileThreads, 1) k_split(const __grid_constant__ TileArgs a) {
+  __shared__ __align__(8) SplitShared sh;
+  split_begin(&sh);
+  split_tile<MODE, EPI>(a, &sh, blockIdx.x / a.splits, ~0u, tc::cluster_rank(), 0);
+  split_end(&sh);
+}
+
+// dx and dW at once, where both together have few tiles: blocks 0 ..
+// dx_blocks - 1 work on dx, the others on dW.  The cluster is as large as the
+// larger of the two splits.
+struct BackArgs {
+  TileArgs dx, dw;
+  uint32_t dx_blocks, dx_units, dw_units;
+};
+
+template <int DW>
+__global__ void __launch_bounds__(kTileThreads, 1) k_split_back(const __grid_constant__ BackArgs b) {
+  __shared__ __align__(8) SplitShared sh;
+  split_begin(&sh);
+  const uint32_t crank = tc::cluster_rank();
+  if (blockIdx.x < b.dx_blocks) {
+    const uint32_t rank = crank % b.dx.splits;
+    split_tile<kDx, CR_BF16>(b.dx, &sh, blockIdx.x / b.dx.splits, b.dx_units, rank, crank - rank);
+  } else {
+    const uint32_t rank = crank % b.dw.splits, at = blockIdx.x - b.dx_blocks;
+    split_tile<kDw, DW>(b.dw, &sh, at / b.dw.splits, b.dw_units, rank, crank - rank);
+  }
+  split_end(&sh);
 }
 
 // ---- host side ------------------------------------------------------------------------
@@ -694,14 +714,6 @@ uint32_t ceil_div(uint32_t a, uint32_t b) { return (uint32_t)(((uint64_t)a + b -
 // Bytes all rows of the outputs allow.
 int out_width(const Mat& m, uint32_t rows, size_t es) { return store_width(m.p, rows > 1 ? m.ld * es : 0); }
 
-// Blocks to share a tile: as many as leave no SM without one (units * splits
-// <= SMs) and each at least `least` K blocks, at most 8 (a portable cluster).
-uint32_t splits_of(uint32_t units, uint32_t blocks, int sms, uint32_t least) {
-  uint32_t s = 1;
-  while (s < 8 && (uint64_t)units * s * 2 <= (uint64_t)sms && blocks >= s * 2 * least) s *= 2;
-  return s;
-}
-
 using Kernel = void (*)(const TileArgs);
 
 struct Launch {
@@ -723,73 +735,132 @@ struct Launch {
   }
 };
 
-// Pairs of k_pairs the device holds at once (cached), after allowing both
-// kernels their shared memory.
-cudaError_t resident_pairs(Kernel pairs_kernel, Kernel split_kernel, uint32_t* pairs) {
+// Blocks of these kernels the device holds at once (an SM holds one), by log2
+// of the cluster, whose SMs lie in one part of the chip.
+struct Capacity {
+  uint32_t blocks[4];
+};
+
+// Cached per device.  Every kernel is allowed its shared memory here.
+cudaError_t capacity(Capacity* out) {
   static std::mutex mu;
-  static std::map<std::pair<Kernel, int>, uint32_t> cache;
+  static std::map<int, Capacity> cache;
   int dev = 0, n = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_pair(pairs_kernel, dev);
-  const auto it = cache.find(key);
+  const auto it = cache.find(dev);
   if (it != cache.end()) {
-    *pairs = it->second;
+    *out = it->second;
     return cudaSuccess;
   }
-  e = cudaFuncSetAttribute(pairs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
-  if (e != cudaSuccess) return e;
-  Launch l(2, kPairThreads, kPairSmem, 2, nullptr);
-  l.cfg.numAttrs = 1;
-  e = cudaOccupancyMaxActiveClusters(&n, pairs_kernel, &l.cfg);
-  if (e != cudaSuccess) return e;
-  *pairs = cache[key] = (uint32_t)std::max(n, 1);
+  for (Kernel k : {k_tiles<kGlu, CR_ACT_SILU>, k_tiles<kGlu, CR_ACT_GELU>, k_tiles<kDx, CR_BF16>,
+                   k_tiles<kDw, CR_BF16>, k_tiles<kDw, CR_F32>, k_split<kGlu, CR_ACT_SILU>,
+                   k_split<kGlu, CR_ACT_GELU>, k_split<kDx, CR_BF16>, k_split<kDw, CR_BF16>,
+                   k_split<kDw, CR_F32>}) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+    if (e != cudaSuccess) return e;
+  }
+  for (auto k : {k_split_back<CR_BF16>, k_split_back<CR_F32>}) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+    if (e != cudaSuccess) return e;
+  }
+  Capacity c;
+  for (int log = 0; log < 4; ++log) {
+    Launch split(1u << log, kTileThreads, kTileSmem, 1u << log, nullptr);
+    split.cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, k_split<kGlu, CR_ACT_SILU>, &split.cfg);
+    if (e != cudaSuccess) return e;
+    c.blocks[log] = (uint32_t)std::max(n, 1) << log;
+  }
+  *out = cache[dev] = c;
   return cudaSuccess;
+}
+
+// Blocks to share a tile: as many as find an SM each, all units at once, and
+// have at least `least` K blocks; at most 8 (a portable cluster).
+uint32_t splits_of(uint32_t units, uint32_t blocks, const Capacity& c, uint32_t least) {
+  int log = 0;
+  while (log < 3 && (uint64_t)units << (log + 1) <= c.blocks[log + 1] && blocks >= (least << (log + 1)))
+    ++log;
+  return 1u << log;
 }
 
 constexpr uint32_t kMinBlocks = 4;    // K blocks worth a block of a cluster
 constexpr uint32_t kTailBlocks = 32;  // K blocks for which splitting the last turn is worth a launch
 
-// Rows in tiles of 128 as long as every tile finds an SM of its own; else in
-// tiles of 256, the last turn's split where they would leave most SMs idle.
+// Clusters for a tile each as long as every tile finds an SM of its own; else
+// persistent blocks, the last turn's tiles split where they would leave most
+// SMs idle.
 template <int MODE, int EPI>
 cudaError_t run_tiles(TileArgs& a, uint32_t outputs, cudaStream_t s) {
-  const Kernel pairs_kernel = k_pairs<MODE, EPI>, split_kernel = k_split<MODE, EPI>;
-  int sms = 0;
-  uint32_t pairs = 0;
-  cudaError_t e = sm_count(&sms);
-  if (e == cudaSuccess) e = resident_pairs(pairs_kernel, split_kernel, &pairs);
+  Capacity cap;
+  cudaError_t e = capacity(&cap);
   if (e != cudaSuccess) return e;
-  const auto run_split = [&](uint32_t units) {
-    const Launch l(units * a.splits, kTileThreads, kTileSmem, a.splits, s);
-    return cudaLaunchKernelEx(&l.cfg, split_kernel, a);
-  };
-  const auto tiles = [&](uint32_t tile_rows) {
-    a.tile_rows = tile_rows;
-    a.tiles_m = ceil_div(a.rows, tile_rows);
-    return (uint64_t)a.tiles_m * a.tiles_n * outputs;
-  };
-  uint64_t n = tiles(kM);
-  if (n <= (uint64_t)sms) {
-    a.splits = splits_of((uint32_t)n, a.blocks, sms, kMinBlocks);
-    return run_split((uint32_t)n);
-  }
-  n = tiles(2 * kM);
+  const uint64_t n = (uint64_t)a.tiles_m * a.tiles_n * outputs;
   if (n >= 1ull << 31) return cudaErrorInvalidValue;
-  const uint32_t rest = (uint32_t)(n % pairs);
+  const uint32_t sms = cap.blocks[0], rest = (uint32_t)(n % sms);
+  uint32_t units = 0;
   a.tiles = (uint32_t)n;
-  if (n > pairs && rest) {
-    a.splits = splits_of(2 * rest, a.blocks, sms, kTailBlocks);
-    if (a.splits > 1) a.tiles -= rest;
+  if (n <= sms) {
+    units = (uint32_t)n;
+    a.splits = splits_of(units, a.blocks, cap, kMinBlocks);
+  } else if (rest) {
+    a.splits = splits_of(rest, a.blocks, cap, kTailBlocks);
+    if (a.splits > 1) units = rest;
   }
-  const Launch l(2 * std::min(a.tiles, pairs), kPairThreads, kPairSmem, 2, s);
-  e = cudaLaunchKernelEx(&l.cfg, pairs_kernel, a);
-  if (e != cudaSuccess || a.tiles == n) return e;
+  a.tiles -= units;
+  if (a.tiles) {
+    const Launch l(std::min(a.tiles, sms), kTileThreads, kTileSmem, 1, s);
+    if ((e = cudaLaunchKernelEx(&l.cfg, k_tiles<MODE, EPI>, a)) != cudaSuccess) return e;
+  }
+  if (!units) return cudaSuccess;
   a.first = a.tiles;
-  return run_split(2 * rest);
+  const Launch l(units * a.splits, kTileThreads, kTileSmem, a.splits, s);
+  return cudaLaunchKernelEx(&l.cfg, k_split<MODE, EPI>, a);
+}
+
+// dx and dW in one launch, if their tiles together leave an SM for each.  The blocks left over go to whichever has the more K blocks a block.
+template <int DW>
+cudaError_t run_split_back(BackArgs& b, uint32_t outputs, bool* done, cudaStream_t s) {
+  Capacity cap;
+  cudaError_t e = capacity(&cap);
+  if (e != cudaSuccess) return e;
+  TileArgs* const both[2] = {&b.dx, &b.dw};
+  uint64_t units[2];
+  for (int k = 0; k < 2; ++k) {
+    TileArgs& a = *both[k];
+    a.splits = 1;
+    units[k] = (uint64_t)a.tiles_m * a.tiles_n * (k ? outputs : 1);
+  }
+  if (units[0] + units[1] > cap.blocks[0]) return cudaSuccess;
+  b.dx_units = (uint32_t)units[0], b.dw_units = (uint32_t)units[1];
+  const auto blocks = [&](int k, uint32_t cluster) {  // whole clusters of them
+    return ceil_div((uint32_t)units[k] * both[k]->splits, cluster) * cluster;
+  };
+  uint32_t cluster = 1;
+  const auto log2 = [](uint32_t c) { return c == 8 ? 3 : c == 4 ? 2 : c == 2 ? 1 : 0; };
+  for (;;) {
+    int k = both[0]->blocks / both[0]->splits >= both[1]->blocks / both[1]->splits ? 0 : 1;
+    bool grown = false;
+    for (int look = 0; look < 2 && !grown; ++look, k ^= 1) {
+      TileArgs& a = *both[k];
+      if (a.splits == 8 || a.blocks < a.splits * 2 * kMinBlocks) continue;
+      a.splits *= 2;
+      const uint32_t c = std::max(cluster, a.splits);
+      if (blocks(0, c) + blocks(1, c) <= cap.blocks[log2(c)]) {
+        cluster = c;
+        grown = true;
+      } else {
+        a.splits /= 2;
+      }
+    }
+    if (!grown) break;
+  }
+  b.dx_blocks = blocks(0, cluster);
+  *done = true;
+  const Launch l(b.dx_blocks + blocks(1, cluster), kTileThreads, kTileSmem, cluster, s);
+  return cudaLaunchKernelEx(&l.cfg, k_split_back<DW>, b);
 }
 
 // An output of rows x cols, `width` columns a tile, of `products` products
@@ -797,7 +868,7 @@ cudaError_t run_tiles(TileArgs& a, uint32_t outputs, cudaStream_t s) {
 cudaError_t shape(TileArgs& a, uint32_t rows, uint32_t cols, uint32_t width, uint32_t k,
                   uint32_t products) {
   a.rows = rows, a.cols = cols;
-  a.tiles_n = ceil_div(cols, width);
+  a.tiles_m = ceil_div(rows, kM), a.tiles_n = ceil_div(cols, width);
   const uint64_t blocks = (uint64_t)ceil_div(k, kK) * products;
   if (blocks >= 1ull << 31) return cudaErrorInvalidValue;
   a.seg_blocks = ceil_div(k, kK);
@@ -825,9 +896,11 @@ cudaError_t launch_glu(cr_act act, const GluArgs& g, cudaStream_t s) {
 }
 
 cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& g, cudaStream_t s) {
+  BackArgs b = {};
+  cudaError_t e = cudaSuccess;
   if (g.dx.p) {
-    TileArgs a = {};
-    cudaError_t e = shape(a, g.tokens, g.dim, kN, g.ffn, 2);
+    TileArgs& a = b.dx;
+    e = shape(a, g.tokens, g.dim, kN, g.ffn, 2);
     const Mat left[2] = {g.dg, g.du}, right[2] = {g.wg, g.wu};
     for (int k = 0; k < 2 && e == cudaSuccess; ++k) {
       e = encode(&a.a[k], left[k], g.tokens, g.ffn, kM);
@@ -836,26 +909,34 @@ cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     a.out[0] = g.dx;
     a.width = out_width(g.dx, g.tokens, 2);
-    if ((e = run_tiles<kDx, CR_BF16>(a, 1, s)) != cudaSuccess) return e;
   }
-  if (!g.dwg && !g.dwu) return cudaSuccess;
-  TileArgs a = {};
-  const uint32_t outputs = g.dwg && g.dwu ? 2 : 1;
-  cudaError_t e = shape(a, g.ffn, g.dim, kN, g.tokens, g.x_lo.p ? 2 : 1);
-  if (e != cudaSuccess) return e;
-  a.width = 32;
-  uint32_t n = 0;
-  for (int k = 0; k < 2; ++k) {
-    void* out = k ? g.dwu : g.dwg;
-    if (!out) continue;
-    a.out[n] = Mat{out, g.dim};
-    a.width = std::min(a.width, out_width(a.out[n], g.ffn, dw == CR_BF16 ? 2 : 4));
-    if ((e = encode(&a.a[n++], k ? g.du : g.dg, g.tokens, g.ffn, kK)) != cudaSuccess) return e;
+  const uint32_t outputs = (g.dwg ? 1 : 0) + (g.dwu ? 1 : 0);
+  if (outputs) {
+    TileArgs& a = b.dw;
+    e = shape(a, g.ffn, g.dim, kN, g.tokens, g.x_lo.p ? 2 : 1);
+    a.width = 32;
+    uint32_t n = 0;
+    for (int k = 0; k < 2 && e == cudaSuccess; ++k) {
+      void* out = k ? g.dwu : g.dwg;
+      if (!out) continue;
+      a.out[n] = Mat{out, g.dim};
+      a.width = std::min(a.width, out_width(a.out[n], g.ffn, dw == CR_BF16 ? 2 : 4));
+      e = encode(&a.a[n++], k ? g.du : g.dg, g.tokens, g.ffn, kK);
+    }
+    if (e == cudaSuccess) e = encode(&a.b[0], g.x, g.tokens, g.dim, kK);
+    if (e == cudaSuccess) e = encode(&a.b[1], g.x_lo, g.tokens, g.dim, kK);
+    if (e != cudaSuccess) return e;
   }
-  if ((e = encode(&a.b[0], g.x, g.tokens, g.dim, kK)) != cudaSuccess) return e;
-  if ((e = encode(&a.b[1], g.x_lo, g.tokens, g.dim, kK)) != cudaSuccess) return e;
-  return dw == CR_BF16 ? run_tiles<kDw, CR_BF16>(a, outputs, s)
-                       : run_tiles<kDw, CR_F32>(a, outputs, s);
+  if (g.dx.p && outputs) {
+    bool done = false;
+    e = dw == CR_BF16 ? run_split_back<CR_BF16>(b, outputs, &done, s)
+                      : run_split_back<CR_F32>(b, outputs, &done, s);
+    if (e != cudaSuccess || done) return e;
+  }
+  if (g.dx.p && (e = run_tiles<kDx, CR_BF16>(b.dx, 1, s)) != cudaSuccess) return e;
+  if (!outputs) return cudaSuccess;
+  return dw == CR_BF16 ? run_tiles<kDw, CR_BF16>(b.dw, outputs, s)
+                       : run_tiles<kDw, CR_F32>(b.dw, outputs, s);
 }
 
 cudaError_t glu_wait_word(bool clear, unsigned int* word) {

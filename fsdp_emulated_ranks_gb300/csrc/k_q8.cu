@@ -5,6 +5,7 @@
 // (ffn_internal.cuh), so the 128-column group's largest magnitude is a shuffle
 // reduction.  A warp that loads few bytes a chunk loads several chunks before
 // it works on the first.
+#include <algorithm>
 #include <type_traits>
 
 #include "ffn_internal.cuh"
@@ -55,7 +56,8 @@ __device__ __forceinline__ char* row_at(const Mat& m, uint64_t row) {
   return static_cast<char*>(m.p) + row * m.ld * (DT == CR_BF16 ? 2 : 4);
 }
 
-constexpr int kAhead = 2;  // chunks of a warp in flight, where a chunk is few bytes
+// Chunks of a warp in flight, where a chunk is few bytes.
+constexpr int ahead(int vec) { return vec ? 2 : 4; }
 
 template <int DT, int VEC>
 __global__ void __launch_bounds__(kBlock) k_q8_store(const __grid_constant__ Mat x,
@@ -63,8 +65,8 @@ __global__ void __launch_bounds__(kBlock) k_q8_store(const __grid_constant__ Mat
                                                      const __grid_constant__ ChunkRange r) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  Raw<DT, VEC> in[kAhead];
-  for_chunks<VEC, kAhead>(
+  Raw<DT, VEC> in[ahead(VEC)];
+  for_chunks<VEC, ahead(VEC)>(
       r,
       [&](int j, uint64_t row, uint32_t base) { in[j].load(row_at<DT>(x, row), base, cols, lane); },
       [&](int j, uint64_t row, uint32_t base) {
@@ -81,8 +83,8 @@ __global__ void __launch_bounds__(kBlock) k_q8_load(const __grid_constant__ Q8 q
                                                     const __grid_constant__ ChunkRange r) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  RawQ8<VEC> in[kAhead];
-  for_chunks<VEC, kAhead>(
+  RawQ8<VEC> in[ahead(VEC)];
+  for_chunks<VEC, ahead(VEC)>(
       r, [&](int j, uint64_t row, uint32_t base) { in[j].load(q, row, base, cols, lane); },
       [&](int j, uint64_t row, uint32_t base) {
         float v[lane_vals(VEC)];
@@ -91,24 +93,21 @@ __global__ void __launch_bounds__(kBlock) k_q8_load(const __grid_constant__ Q8 q
       });
 }
 
+// The values of q's chunks as hi + lo.
 template <int VEC>
-__global__ void __launch_bounds__(kBlock) k_q8_split(const __grid_constant__ Q8 q,
-                                                     const __grid_constant__ Mat hi,
-                                                     const __grid_constant__ Mat lo, uint32_t cols,
-                                                     const __grid_constant__ ChunkRange r) {
-  pdl_enter();
+__device__ __forceinline__ void split_chunks(const SplitArgs& a, const ChunkRange& r) {
   const int lane = threadIdx.x & 31;
-  RawQ8<VEC> in[kAhead];
-  for_chunks<VEC, kAhead>(
-      r, [&](int j, uint64_t row, uint32_t base) { in[j].load(q, row, base, cols, lane); },
+  RawQ8<VEC> in[1];
+  for_chunks<VEC, 1>(
+      r, [&](int j, uint64_t row, uint32_t base) { in[j].load(a.q, row, base, a.cols, lane); },
       [&](int j, uint64_t row, uint32_t base) {
         float v[lane_vals(VEC)], rest[lane_vals(VEC)];
         in[j].values(v);
 #pragma unroll
         for (int i = 0; i < lane_vals(VEC); ++i)
           rest[i] = v[i] - ffn_bf16((uint16_t)ffn_bf16x2(v[i], 0.0f));
-        st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(hi, row), base, cols, lane, v);
-        st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(lo, row), base, cols, lane, rest);
+        st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(a.hi, row), base, a.cols, lane, v);
+        st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(a.lo, row), base, a.cols, lane, rest);
       });
 }
 
@@ -117,8 +116,8 @@ __global__ void __launch_bounds__(kBlock) k_copy_bf16(const __grid_constant__ Co
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const CopyBf16::One& m = c.one[blockIdx.y];
-  Raw<CR_BF16, 0> in[kAhead];
-  for_chunks<0, kAhead>(
+  Raw<CR_BF16, 0> in[ahead(0)];
+  for_chunks<0, ahead(0)>(
       ChunkRange{m.chunks, m.per_row},
       [&](int j, uint64_t row, uint32_t base) {
         in[j].load(row_at<CR_BF16>(m.src, row), base, m.cols, lane);
@@ -131,10 +130,14 @@ __global__ void __launch_bounds__(kBlock) k_copy_bf16(const __grid_constant__ Co
       });
 }
 
+// blockIdx.y 1: x's checkpoint, split for the products that follow.
 template <int ACT, int VEC>
 __global__ void __launch_bounds__(kBlock, 4) k_act_back(const __grid_constant__ ActBackArgs a,
-                                                     const __grid_constant__ ChunkRange r) {
+                                                        const __grid_constant__ ChunkRange r,
+                                                        const __grid_constant__ SplitArgs x,
+                                                        const __grid_constant__ ChunkRange xr) {
   pdl_enter();
+  if (blockIdx.y) return x.vec ? split_chunks<1>(x, xr) : split_chunks<0>(x, xr);
   const int lane = threadIdx.x & 31;
   Raw<CR_BF16, VEC> in[1];
   RawQ8<VEC> gate[1], up[1];
@@ -185,7 +188,7 @@ cudaError_t launch_q8_store(cr_dtype d, const Mat& x, const Q8& q, uint64_t rows
   const ChunkRange r = chunk_range(rows, cols, vec);
   return with_vec(vec, [&](auto v) {
     return launch_pdl(d == CR_BF16 ? k_q8_store<CR_BF16, v()> : k_q8_store<CR_F32, v()>,
-                      chunk_grid(r, kAhead), kBlock, s, x, q, cols, r);
+                      chunk_grid(r, ahead(v())), kBlock, s, x, q, cols, r);
   });
 }
 
@@ -194,15 +197,7 @@ cudaError_t launch_q8_load(cr_dtype d, const Q8& q, const Mat& x, uint64_t rows,
   const ChunkRange r = chunk_range(rows, cols, vec);
   return with_vec(vec, [&](auto v) {
     return launch_pdl(d == CR_BF16 ? k_q8_load<CR_BF16, v()> : k_q8_load<CR_F32, v()>,
-                      chunk_grid(r, kAhead), kBlock, s, q, x, cols, r);
-  });
-}
-
-cudaError_t launch_q8_split(const Q8& q, const Mat& hi, const Mat& lo, uint64_t rows, uint32_t cols,
-                            int vec, cudaStream_t s) {
-  const ChunkRange r = chunk_range(rows, cols, vec);
-  return with_vec(vec, [&](auto v) {
-    return launch_pdl(k_q8_split<v()>, chunk_grid(r, kAhead), kBlock, s, q, hi, lo, cols, r);
+                      chunk_grid(r, ahead(v())), kBlock, s, q, x, cols, r);
   });
 }
 
@@ -215,16 +210,20 @@ cudaError_t launch_copy_bf16(const CopyBf16& c, cudaStream_t s) {
   if (c.n == 0) return cudaSuccess;
   uint64_t most = 0;
   for (int k = 0; k < c.n; ++k) most = c.one[k].chunks > most ? c.one[k].chunks : most;
-  dim3 grid = chunk_grid(ChunkRange{most, FastDiv{}}, kAhead);
+  dim3 grid = chunk_grid(ChunkRange{most, FastDiv{}}, ahead(0));
   grid.y = c.n;
   return launch_pdl(k_copy_bf16, grid, kBlock, s, c);
 }
 
-cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, int vec, cudaStream_t s) {
+cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, const SplitArgs* x, int vec,
+                            cudaStream_t s) {
   const ChunkRange r = chunk_range(a.rows, a.cols, vec);
+  const ChunkRange xr = x ? chunk_range(x->rows, x->cols, x->vec) : ChunkRange{};
+  dim3 grid = chunk_grid(ChunkRange{std::max(r.chunks, xr.chunks), FastDiv{}}, 1);
+  grid.y = x ? 2 : 1;
   return with_vec(vec, [&](auto v) {
     return launch_pdl(act == CR_ACT_SILU ? k_act_back<CR_ACT_SILU, v()> : k_act_back<CR_ACT_GELU, v()>,
-                      chunk_grid(r, 1), kBlock, s, a, r);
+                      grid, kBlock, s, a, r, x ? *x : SplitArgs{}, xr);
   });
 }
 

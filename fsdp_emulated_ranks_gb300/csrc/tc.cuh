@@ -39,36 +39,17 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return done;
 }
 
-// The same, for arrivals from the other block of a pair.
-__device__ __forceinline__ bool bar_try_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;"
-      " selp.u32 %0, 1, 0, p; }"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done;
-}
-
-// Arrives on a barrier of any block of the cluster (cluster_addr).
-__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Clock cycles (about two seconds) after which a wait gives up.
-constexpr long long kWaitCycles = 4ll << 30;
+// Clock cycles (about half a second) after which a wait gives up.
+constexpr long long kWaitCycles = 1ll << 30;
 
 // Waits for the phase of `parity` to complete.  False if it did not in
 // kWaitCycles, or if another role of the block gave up (*gave_up set): the
 // caller then leaves its loop.
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity,
                                          volatile uint32_t* gave_up) {
-  const auto done = [&] { return CLUSTER ? bar_try_cluster(bar, parity) : bar_try(bar, parity); };
-  if (done()) return true;
+  if (bar_try(bar, parity)) return true;
   const long long start = clock64();
-  while (!done()) {
+  while (!bar_try(bar, parity)) {
     if (*gave_up) return false;
     if (clock64() - start > kWaitCycles) {
       *gave_up = 1;
@@ -135,41 +116,18 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// The same with bytes counted on a barrier of either block of the pair
-// (cluster_addr).
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                              uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
 // ---- tensor memory and products -----------------------------------------------------
 
-// Whole warp (GROUP 2: one in each block of the pair).  Writes the address of
-// `cols` columns to shared memory.
-template <int GROUP>
+// Whole warp.  Writes the address of `cols` columns to shared memory.
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_out, uint32_t cols) {
-  if constexpr (GROUP == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_out),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_out),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_out),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
 
-template <int GROUP>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-  if constexpr (GROUP == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-  else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
 
 __device__ __forceinline__ void fence_before() {
@@ -198,39 +156,20 @@ constexpr uint32_t product_desc(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
          (n >> 3) << 17 | (m >> 4) << 24;
 }
 
-// One thread: D (tensor memory) = A B + (accumulate ? D : 0), K = 16.  GROUP 2:
-// one thread of the pair's first block; each block holds half the rows of A
-// and of D and half the columns of B.
-template <int GROUP>
+// One thread: D (tensor memory) = A B + (accumulate ? D : 0), K = 16.
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                     bool accumulate) {
-  if constexpr (GROUP == 1)
-    asm volatile(
-        "{ .reg .pred p; setp.ne.u32 p, %4, 0;"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{ .reg .pred p; setp.ne.u32 p, %4, 0;"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
-        : "memory");
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+      : "memory");
 }
 
 // Arrives on bar when this thread's products so far are done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
-// The same for a pair's products: on bar in both blocks.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
       : "memory");
 }
 

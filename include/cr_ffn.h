@@ -173,7 +173,7 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8,
                           cr_stream_t stream);
 
 /* The block's products wait on barriers inside the kernel, each wait for about
- * two seconds at most.  A wait that runs out (it never should) ends the
+ * half a second at most.  A wait that runs out (it never should) ends the
  * kernel, leaves its results undefined and sets this word, which stays set
  * until it is cleared.  Returns the word (0: no wait ever ran out), or -2 if
  * reading it failed; waits for the device. */
