@@ -99,7 +99,8 @@ class Q8(C.Structure):
                 ("scales", C.c_void_p), ("lds", C.c_size_t)]
 
     def __init__(self, codes, scales, ld=None, lds=None):
-        super().__init__(_ptr(codes), _ld(codes, ld), _ptr(scales), _ld(scales, lds))
+        self.codes, self.ld = _mat(codes, ld)
+        self.scales, self.lds = _mat(scales, lds)
         self._keep = (codes, scales)
 
 
@@ -225,19 +226,22 @@ def _ptr(x) -> int:
     return x.data_ptr()
 
 
-def _ld(x, ld=None) -> int:
-    """Row stride in elements: the one given, else the 2-D tensor's own (0
-    for an absent matrix, and for a pointer or a vector)."""
-    if ld is not None:
-        return ld
-    if x is None or type(x) is int:
-        return 0
-    st = x.stride()
-    if len(st) < 2:
-        return 0
-    if st[1] != 1 and x.shape[1] > 1:
-        raise ValueError("the columns of a matrix must be contiguous")
-    return st[0]
+def _mat(x, ld):
+    """Address and row stride in elements of a matrix: the stride given, else
+    the 2-D tensor's own (0 for an absent matrix, a pointer or a vector)."""
+    if x is None:
+        return 0, 0
+    if type(x) is int:
+        return x, ld or 0
+    if ld is None:
+        st = x.stride()
+        if len(st) < 2:
+            ld = 0
+        else:
+            if st[1] != 1 and x.shape[1] > 1:
+                raise ValueError("the columns of a matrix must be contiguous")
+            ld = st[0]
+    return x.data_ptr(), ld
 
 
 _PACK = {}  # length -> struct packer of that many native 64-bit pointers
@@ -717,21 +721,29 @@ def _q8(q):
 
 
 def cr_q8_store(x, rows, cols, dtype, q: Q8, stream=None, ldx=None) -> None:
-    _check(lib().cr_q8_store(_ptr(x), _ld(x, ldx), rows, cols, _dtype(dtype), _q8(q),
-                             _stream(stream)), "cr_q8_store")
+    x, ldx = _mat(x, ldx)
+    status = lib().cr_q8_store(x, ldx, rows, cols, _dtype(dtype), _q8(q), _stream(stream))
+    if status:
+        _check(status, "cr_q8_store")
 
 
 def cr_q8_load(q: Q8, rows, cols, x, dtype, stream=None, ldx=None) -> None:
-    _check(lib().cr_q8_load(_q8(q), rows, cols, _ptr(x), _ld(x, ldx), _dtype(dtype),
-                            _stream(stream)), "cr_q8_load")
+    x, ldx = _mat(x, ldx)
+    status = lib().cr_q8_load(_q8(q), rows, cols, x, ldx, _dtype(dtype), _stream(stream))
+    if status:
+        _check(status, "cr_q8_load")
 
 
 def cr_rms_norm(x, residual, weight, rows, cols, dtype, eps, sum, y, y8: Q8 = None, rstd=None,
                 stream=None, ldx=None, ldr=None, ldsum=None, ldy=None) -> None:
-    _check(lib().cr_rms_norm(_ptr(x), _ld(x, ldx), _ptr(residual), _ld(residual, ldr),
-                             _ptr(weight), rows, cols, _dtype(dtype), eps, _ptr(sum),
-                             _ld(sum, ldsum), _ptr(y), _ld(y, ldy), _q8(y8), _ptr(rstd),
-                             _stream(stream)), "cr_rms_norm")
+    x, ldx = _mat(x, ldx)
+    residual, ldr = _mat(residual, ldr)
+    sum, ldsum = _mat(sum, ldsum)
+    y, ldy = _mat(y, ldy)
+    status = lib().cr_rms_norm(x, ldx, residual, ldr, _ptr(weight), rows, cols, _dtype(dtype), eps,
+                               sum, ldsum, y, ldy, _q8(y8), _ptr(rstd), _stream(stream))
+    if status:
+        _check(status, "cr_rms_norm")
 
 
 def cr_rms_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
@@ -741,11 +753,16 @@ def cr_rms_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
 def cr_rms_norm_backward(dy, h, h8: Q8, weight, rstd, dres, rows, cols, dtype, dx, dweight,
                          dw_dtype="bf16", workspace=None, workspace_bytes=0, stream=None,
                          lddy=None, ldh=None, lddres=None, lddx=None) -> None:
-    _check(lib().cr_rms_norm_backward(_ptr(dy), _ld(dy, lddy), _ptr(h), _ld(h, ldh), _q8(h8),
-                                      _ptr(weight), _ptr(rstd), _ptr(dres), _ld(dres, lddres),
-                                      rows, cols, _dtype(dtype), _ptr(dx), _ld(dx, lddx),
-                                      _ptr(dweight), _dtype(dw_dtype), _ptr(workspace),
-                                      workspace_bytes, _stream(stream)), "cr_rms_norm_backward")
+    dy, lddy = _mat(dy, lddy)
+    h, ldh = _mat(h, ldh)
+    dres, lddres = _mat(dres, lddres)
+    dx, lddx = _mat(dx, lddx)
+    status = lib().cr_rms_norm_backward(dy, lddy, h, ldh, _q8(h8), _ptr(weight), _ptr(rstd), dres,
+                                        lddres, rows, cols, _dtype(dtype), dx, lddx, _ptr(dweight),
+                                        _dtype(dw_dtype), _ptr(workspace), workspace_bytes,
+                                        _stream(stream))
+    if status:
+        _check(status, "cr_rms_norm_backward")
 
 
 def cr_glu_workspace_bytes(tokens: int, dim: int, ffn: int) -> int:
@@ -755,18 +772,27 @@ def cr_glu_workspace_bytes(tokens: int, dim: int, ffn: int) -> int:
 def cr_glu(x, wg, wu, tokens, dim, ffn, dtype, act, a, g8: Q8 = None, u8: Q8 = None,
            workspace=None, workspace_bytes=0, stream=None, ldx=None, ldwg=None, ldwu=None,
            lda=None) -> None:
-    _check(lib().cr_glu(_ptr(x), _ld(x, ldx), _ptr(wg), _ld(wg, ldwg), _ptr(wu), _ld(wu, ldwu),
-                        tokens, dim, ffn, _dtype(dtype), _act(act), _ptr(a), _ld(a, lda),
-                        _q8(g8), _q8(u8), _ptr(workspace), workspace_bytes, _stream(stream)),
-           "cr_glu")
+    x, ldx = _mat(x, ldx)
+    wg, ldwg = _mat(wg, ldwg)
+    wu, ldwu = _mat(wu, ldwu)
+    a, lda = _mat(a, lda)
+    status = lib().cr_glu(x, ldx, wg, ldwg, wu, ldwu, tokens, dim, ffn, _dtype(dtype), _act(act),
+                          a, lda, _q8(g8), _q8(u8), _ptr(workspace), workspace_bytes,
+                          _stream(stream))
+    if status:
+        _check(status, "cr_glu")
 
 
 def cr_glu_act_backward(da, g8: Q8, u8: Q8, tokens, ffn, dtype, act, dg, du, a=None, stream=None,
                         ldda=None, lddg=None, lddu=None, lda=None) -> None:
-    _check(lib().cr_glu_act_backward(_ptr(da), _ld(da, ldda), _q8(g8), _q8(u8), tokens, ffn,
-                                     _dtype(dtype), _act(act), _ptr(dg), _ld(dg, lddg), _ptr(du),
-                                     _ld(du, lddu), _ptr(a), _ld(a, lda), _stream(stream)),
-           "cr_glu_act_backward")
+    da, ldda = _mat(da, ldda)
+    dg, lddg = _mat(dg, lddg)
+    du, lddu = _mat(du, lddu)
+    a, lda = _mat(a, lda)
+    status = lib().cr_glu_act_backward(da, ldda, _q8(g8), _q8(u8), tokens, ffn, _dtype(dtype),
+                                       _act(act), dg, lddg, du, lddu, a, lda, _stream(stream))
+    if status:
+        _check(status, "cr_glu_act_backward")
 
 
 def cr_glu_backward_workspace_bytes(tokens: int, dim: int, ffn: int) -> int:
@@ -776,12 +802,18 @@ def cr_glu_backward_workspace_bytes(tokens: int, dim: int, ffn: int) -> int:
 def cr_glu_backward(da, g8: Q8, u8: Q8, x, x8: Q8, wg, wu, tokens, dim, ffn, dtype, act, dx, dwg,
                     dwu, dw_dtype="bf16", a=None, workspace=None, workspace_bytes=0, stream=None,
                     ldda=None, ldx=None, ldwg=None, ldwu=None, lddx=None, lda=None) -> None:
-    _check(lib().cr_glu_backward(_ptr(da), _ld(da, ldda), _q8(g8), _q8(u8), _ptr(x), _ld(x, ldx),
-                                 _q8(x8), _ptr(wg), _ld(wg, ldwg), _ptr(wu), _ld(wu, ldwu),
-                                 tokens, dim, ffn, _dtype(dtype), _act(act), _ptr(dx),
-                                 _ld(dx, lddx), _ptr(dwg), _ptr(dwu), _dtype(dw_dtype), _ptr(a),
-                                 _ld(a, lda), _ptr(workspace), workspace_bytes, _stream(stream)),
-           "cr_glu_backward")
+    da, ldda = _mat(da, ldda)
+    x, ldx = _mat(x, ldx)
+    wg, ldwg = _mat(wg, ldwg)
+    wu, ldwu = _mat(wu, ldwu)
+    dx, lddx = _mat(dx, lddx)
+    a, lda = _mat(a, lda)
+    status = lib().cr_glu_backward(da, ldda, _q8(g8), _q8(u8), x, ldx, _q8(x8), wg, ldwg, wu, ldwu,
+                                   tokens, dim, ffn, _dtype(dtype), _act(act), dx, lddx, _ptr(dwg),
+                                   _ptr(dwu), _dtype(dw_dtype), a, lda, _ptr(workspace),
+                                   workspace_bytes, _stream(stream))
+    if status:
+        _check(status, "cr_glu_backward")
 
 
 def cr_glu_wait_word(clear: bool = False) -> int:

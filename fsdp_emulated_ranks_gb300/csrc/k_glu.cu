@@ -24,8 +24,8 @@
 // reading the partials of all in rank order.  k_split_back runs the tiles of dx
 // and of dW in one launch.
 //
-// Both let the next kernel's blocks onto their SMs only as they end: a waiting
-// block beside them would have nothing to do for most of their time.
+// Both let the next kernel's blocks onto their SMs only when their last products
+// are loaded: a waiting block beside them would have nothing to do before.
 //
 // Every wait is bounded (tc.cuh); a block that gives up sets g_wait_word and
 // leaves.
@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant
         load_block<MODE>(a, which, row, tn, k, smem + s * kStageBytes, full + 8 * s);
       }
     }
+    pdl_launch_dependents();
     if (!live) {
       // leave no copy in flight behind: the last kStages blocks issued
       const uint32_t first = it > kStages ? it - kStages : 0;
@@ -538,6 +539,7 @@ __device__ __forceinline__ void split_tile(const TileArgs& a, SplitShared* sh, u
       if (!(live = tc::bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, gave_up))) break;
       load_block<MODE>(a, which, row0, tn, k, smem + s * kStageBytes, full + 8 * s);
     }
+    pdl_launch_dependents();
     if (!live) {
       // leave no copy in flight behind: the last kStages blocks issued
       const uint32_t first = it > kStages ? it - kStages : 0;
@@ -737,8 +739,9 @@ struct Launch {
 
 // Blocks of these kernels the device holds at once (an SM holds one), by log2
 // of the cluster, whose SMs lie in one part of the chip.
+constexpr int kClusterLogs = 3;
 struct Capacity {
-  uint32_t blocks[4];
+  uint32_t blocks[kClusterLogs];
 };
 
 // Cached per device.  Every kernel is allowed its shared memory here.
@@ -766,7 +769,7 @@ cudaError_t capacity(Capacity* out) {
     if (e != cudaSuccess) return e;
   }
   Capacity c;
-  for (int log = 0; log < 4; ++log) {
+  for (int log = 0; log < kClusterLogs; ++log) {
     Launch split(1u << log, kTileThreads, kTileSmem, 1u << log, nullptr);
     split.cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(&n, k_split<kGlu, CR_ACT_SILU>, &split.cfg);
@@ -777,11 +780,16 @@ cudaError_t capacity(Capacity* out) {
   return cudaSuccess;
 }
 
+// Blocks to share a tile, at most.  Clusters of 8 wait long for 8 free SMs in
+// one part of the chip: 6 tiles of dx and 64 of dW (257 x 512 x 2048) took 31.1
+// us in clusters of 8, 19.6 in clusters of 4, 19.3 of 2 and 26.6 unsplit.
+constexpr int kMaxSplitLog = kClusterLogs - 1;
+
 // Blocks to share a tile: as many as find an SM each, all units at once, and
-// have at least `least` K blocks; at most 8 (a portable cluster).
+// have at least `least` K blocks.
 uint32_t splits_of(uint32_t units, uint32_t blocks, const Capacity& c, uint32_t least) {
   int log = 0;
-  while (log < 3 && (uint64_t)units << (log + 1) <= c.blocks[log + 1] && blocks >= (least << (log + 1)))
+  while (log < kMaxSplitLog && (uint64_t)units << (log + 1) <= c.blocks[log + 1] && blocks >= (least << (log + 1)))
     ++log;
   return 1u << log;
 }
@@ -839,13 +847,13 @@ cudaError_t run_split_back(BackArgs& b, uint32_t outputs, bool* done, cudaStream
     return ceil_div((uint32_t)units[k] * both[k]->splits, cluster) * cluster;
   };
   uint32_t cluster = 1;
-  const auto log2 = [](uint32_t c) { return c == 8 ? 3 : c == 4 ? 2 : c == 2 ? 1 : 0; };
+  const auto log2 = [](uint32_t c) { return c == 4 ? 2 : c == 2 ? 1 : 0; };
   for (;;) {
     int k = both[0]->blocks / both[0]->splits >= both[1]->blocks / both[1]->splits ? 0 : 1;
     bool grown = false;
     for (int look = 0; look < 2 && !grown; ++look, k ^= 1) {
       TileArgs& a = *both[k];
-      if (a.splits == 8 || a.blocks < a.splits * 2 * kMinBlocks) continue;
+      if (a.splits == 1u << kMaxSplitLog || a.blocks < a.splits * 2 * kMinBlocks) continue;
       a.splits *= 2;
       const uint32_t c = std::max(cluster, a.splits);
       if (blocks(0, c) + blocks(1, c) <= cap.blocks[log2(c)]) {

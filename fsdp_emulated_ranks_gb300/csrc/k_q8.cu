@@ -56,8 +56,7 @@ __device__ __forceinline__ char* row_at(const Mat& m, uint64_t row) {
   return static_cast<char*>(m.p) + row * m.ld * (DT == CR_BF16 ? 2 : 4);
 }
 
-// Chunks of a warp in flight, where a chunk is few bytes.
-constexpr int ahead(int vec) { return vec ? 2 : 4; }
+constexpr int kAhead = 2;  // chunks of a warp in flight, where a chunk is few bytes
 
 template <int DT, int VEC>
 __global__ void __launch_bounds__(kBlock) k_q8_store(const __grid_constant__ Mat x,
@@ -65,8 +64,8 @@ __global__ void __launch_bounds__(kBlock) k_q8_store(const __grid_constant__ Mat
                                                      const __grid_constant__ ChunkRange r) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  Raw<DT, VEC> in[ahead(VEC)];
-  for_chunks<VEC, ahead(VEC)>(
+  Raw<DT, VEC> in[kAhead];
+  for_chunks<VEC, kAhead>(
       r,
       [&](int j, uint64_t row, uint32_t base) { in[j].load(row_at<DT>(x, row), base, cols, lane); },
       [&](int j, uint64_t row, uint32_t base) {
@@ -83,8 +82,8 @@ __global__ void __launch_bounds__(kBlock) k_q8_load(const __grid_constant__ Q8 q
                                                     const __grid_constant__ ChunkRange r) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  RawQ8<VEC> in[ahead(VEC)];
-  for_chunks<VEC, ahead(VEC)>(
+  RawQ8<VEC> in[kAhead];
+  for_chunks<VEC, kAhead>(
       r, [&](int j, uint64_t row, uint32_t base) { in[j].load(q, row, base, cols, lane); },
       [&](int j, uint64_t row, uint32_t base) {
         float v[lane_vals(VEC)];
@@ -116,8 +115,8 @@ __global__ void __launch_bounds__(kBlock) k_copy_bf16(const __grid_constant__ Co
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const CopyBf16::One& m = c.one[blockIdx.y];
-  Raw<CR_BF16, 0> in[ahead(0)];
-  for_chunks<0, ahead(0)>(
+  Raw<CR_BF16, 0> in[2];
+  for_chunks<0, 2>(
       ChunkRange{m.chunks, m.per_row},
       [&](int j, uint64_t row, uint32_t base) {
         in[j].load(row_at<CR_BF16>(m.src, row), base, m.cols, lane);
@@ -188,7 +187,7 @@ cudaError_t launch_q8_store(cr_dtype d, const Mat& x, const Q8& q, uint64_t rows
   const ChunkRange r = chunk_range(rows, cols, vec);
   return with_vec(vec, [&](auto v) {
     return launch_pdl(d == CR_BF16 ? k_q8_store<CR_BF16, v()> : k_q8_store<CR_F32, v()>,
-                      chunk_grid(r, ahead(v())), kBlock, s, x, q, cols, r);
+                      chunk_grid(r, kAhead), kBlock, s, x, q, cols, r);
   });
 }
 
@@ -197,7 +196,7 @@ cudaError_t launch_q8_load(cr_dtype d, const Q8& q, const Mat& x, uint64_t rows,
   const ChunkRange r = chunk_range(rows, cols, vec);
   return with_vec(vec, [&](auto v) {
     return launch_pdl(d == CR_BF16 ? k_q8_load<CR_BF16, v()> : k_q8_load<CR_F32, v()>,
-                      chunk_grid(r, ahead(v())), kBlock, s, q, x, cols, r);
+                      chunk_grid(r, kAhead), kBlock, s, q, x, cols, r);
   });
 }
 
@@ -210,7 +209,7 @@ cudaError_t launch_copy_bf16(const CopyBf16& c, cudaStream_t s) {
   if (c.n == 0) return cudaSuccess;
   uint64_t most = 0;
   for (int k = 0; k < c.n; ++k) most = c.one[k].chunks > most ? c.one[k].chunks : most;
-  dim3 grid = chunk_grid(ChunkRange{most, FastDiv{}}, ahead(0));
+  dim3 grid = chunk_grid(ChunkRange{most, FastDiv{}}, 2);
   grid.y = c.n;
   return launch_pdl(k_copy_bf16, grid, kBlock, s, c);
 }
