@@ -797,7 +797,7 @@ uint32_t splits_of(uint32_t units, uint32_t blocks, const Capacity& c, uint32_t 
 constexpr uint32_t kMinBlocks = 4;    // K blocks worth a block of a cluster
 constexpr uint32_t kTailBlocks = 32;  // K blocks for which splitting the last turn is worth a launch
 
-// Clusters for a tile each as long as every tile finds an SM of its own; else
+// Clusters for a tile each if several blocks find SMs for every tile; else
 // persistent blocks, the last turn's tiles split where they would leave most
 // SMs idle.
 template <int MODE, int EPI>
@@ -813,6 +813,7 @@ cudaError_t run_tiles(TileArgs& a, uint32_t outputs, cudaStream_t s) {
   if (n <= sms) {
     units = (uint32_t)n;
     a.splits = splits_of(units, a.blocks, cap, kMinBlocks);
+    if (a.splits == 1) units = 0;  // k_tiles ends sooner after its products: 11.5 against 13.7 us
   } else if (rest) {
     a.splits = splits_of(rest, a.blocks, cap, kTailBlocks);
     if (a.splits > 1) units = rest;

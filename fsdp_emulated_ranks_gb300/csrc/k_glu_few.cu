@@ -14,6 +14,7 @@ namespace cr {
 
 namespace {
 
+constexpr int kMaxThreads = 320;  // of a block; two blocks an SM
 constexpr int kDeep = 4;  // chunks of each weight row loaded before the first is used
 
 template <int T, int VEC>
@@ -43,13 +44,13 @@ __device__ __forceinline__ void add_chunk(const Raw<CR_BF16, VEC>& g, const Raw<
 
 // x in shared memory is zero past dim, up to `pitch`, a multiple of any chunk.
 template <int ACT, int T, int VEC>
-__global__ void __launch_bounds__(kBlock) k_glu_few(const __grid_constant__ GluArgs a,
+__global__ void __launch_bounds__(kMaxThreads, 2) k_glu_few(const __grid_constant__ GluArgs a,
                                                     uint32_t pitch) {
   extern __shared__ __align__(16) uint16_t x[];
   pdl_enter();
   // a warp a chunk, all of them loaded before the first is stored
   const uint32_t per = pitch / chunk_cols(0);
-  for (uint32_t k = threadIdx.x >> 5; k < T * per; k += kBlock / 32) {
+  for (uint32_t k = threadIdx.x >> 5; k < T * per; k += blockDim.x / 32) {
     const uint32_t t = k / per, base = (k - t * per) * chunk_cols(0);
     Raw<CR_BF16, 0> r;
     r.clear();
@@ -61,8 +62,8 @@ __global__ void __launch_bounds__(kBlock) k_glu_few(const __grid_constant__ GluA
   }
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  const uint32_t warps = gridDim.x * (kBlock / 32);
-  for (uint32_t f = blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); f < a.ffn; f += warps) {
+  const uint32_t warps = gridDim.x * (blockDim.x / 32);
+  for (uint32_t f = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); f < a.ffn; f += warps) {
     const uint16_t* wg = static_cast<const uint16_t*>(a.wg.p) + f * a.wg.ld;
     const uint16_t* wu = static_cast<const uint16_t*>(a.wu.p) + f * a.wu.ld;
     float g[T], u[T];
@@ -96,13 +97,19 @@ __global__ void __launch_bounds__(kBlock) k_glu_few(const __grid_constant__ GluA
 
 template <int ACT, int T, int VEC>
 cudaError_t run(const GluArgs& a, uint32_t pitch, cudaStream_t s) {
-  int full = 0;
-  cudaError_t e = persistent_grid(reinterpret_cast<const void*>(k_glu_few<ACT, T, VEC>), ~0ull >> 8, &full);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const uint32_t blocks = (a.ffn + kBlock / 32 - 1) / (kBlock / 32);
+  // Two blocks an SM, of as many warps (5 to 10) as leave the fewest idle in
+  // the last turn, the larger block where that is even.
+  uint32_t best = 0, least = ~0u;
+  for (uint32_t w = 5; w <= kMaxThreads / 32; ++w) {
+    const uint32_t all = 2 * (uint32_t)sms * w, slots = (a.ffn + all - 1) / all * all;
+    if (slots <= least) least = slots, best = w;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(blocks, (uint32_t)full));
-  cfg.blockDim = dim3(kBlock);
+  cfg.gridDim = dim3(std::min((a.ffn + best - 1) / best, 2 * (uint32_t)sms));
+  cfg.blockDim = dim3(best * 32);
   cfg.dynamicSmemBytes = (size_t)T * pitch * 2;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -115,12 +122,13 @@ cudaError_t run(const GluArgs& a, uint32_t pitch, cudaStream_t s) {
 
 template <int ACT, int VEC>
 cudaError_t by_tokens(const GluArgs& a, uint32_t pitch, cudaStream_t s) {
-  if (a.tokens == 1) return run<ACT, 1, VEC>(a, pitch, s);
-  if (a.tokens == 2) return run<ACT, 2, VEC>(a, pitch, s);
-  return run<ACT, 4, VEC>(a, pitch, s);
+  return a.tokens == 1 ? run<ACT, 1, VEC>(a, pitch, s) : run<ACT, 2, VEC>(a, pitch, s);
 }
 
-constexpr uint32_t kFewTokens = 4;
+// 2048 x 8192, a call: 1 token 13.2 us and 2 tokens 17.1 here, 3 tokens 22.7
+// (a third row of sums leaves too few registers for loads); in tiles any
+// number up to 128 takes about 20.
+constexpr uint32_t kFewTokens = 2;
 constexpr uint32_t kFewSmem = 48 << 10;  // what a block gets without asking
 
 uint32_t pitch_of(uint32_t dim) { return (dim + 511) / 512 * 512; }
@@ -129,8 +137,7 @@ uint32_t pitch_of(uint32_t dim) { return (dim + 511) / 512 * 512; }
 
 bool glu_few(uint64_t tokens, uint64_t dim, bool keeps) {
   if (keeps || tokens > kFewTokens || dim > kFewSmem / 2) return false;
-  const uint64_t rows = tokens > 2 ? 4 : tokens;
-  return rows * pitch_of((uint32_t)dim) * 2 <= kFewSmem;
+  return tokens * pitch_of((uint32_t)dim) * 2 <= kFewSmem;
 }
 
 template <int ACT>

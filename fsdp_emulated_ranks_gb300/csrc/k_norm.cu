@@ -209,8 +209,8 @@ __device__ __forceinline__ void back_st(const NormBackArgs& a, uint64_t row, uin
 }
 
 // Rows a block of 16 warps can hold: block (32 * warps per row, rows per
-// block), persistent; partial row blockIdx.x * blockDim.y + threadIdx.y of
-// dweight, whose sums stay in registers.  With vectors, everything the next
+// block), persistent; partial row blockIdx.x of dweight, whose sums stay in
+// registers.  With vectors, everything the next
 // row needs is loaded while this one is reduced and written; the scalar
 // kernel, whose loads take twice the registers, relies on more warps instead.
 template <int DT, int VEC, bool HELD8>
@@ -270,13 +270,27 @@ __global__ void __launch_bounds__(kBackThreads)
     const float c = row_sum(s, part, buf) * a.inv_cols;
     if (row < a.rows) back_st<DT, VEC>(a, row, base, lane, t, n, r, rstd, c);
   }
-  if (a.partial) {
-    float* p = a.partial + ((uint64_t)blockIdx.x * blockDim.y + threadIdx.y) * a.cols;
+  if (!a.partial) return;
+  // the sums of the block's other rows join the first's, in order
+  extern __shared__ float sums[];  // lane_vals x threads of a row
+  for (unsigned y = 1; y < blockDim.y; ++y) {
+    __syncthreads();
+    if (threadIdx.y == y) {
 #pragma unroll
-    for (int i = 0; i < vals; ++i) {
-      const uint32_t c = chunk_col<VEC>(base, lane, i);
-      if (c < a.cols) p[c] = dw[i];
+      for (int i = 0; i < vals; ++i) sums[i * blockDim.x + threadIdx.x] = dw[i];
     }
+    __syncthreads();
+    if (threadIdx.y == 0) {
+#pragma unroll
+      for (int i = 0; i < vals; ++i) dw[i] += sums[i * blockDim.x + threadIdx.x];
+    }
+  }
+  if (threadIdx.y) return;
+  float* p = a.partial + (uint64_t)blockIdx.x * a.cols;
+#pragma unroll
+  for (int i = 0; i < vals; ++i) {
+    const uint32_t c = chunk_col<VEC>(base, lane, i);
+    if (c < a.cols) p[c] = dw[i];
   }
 }
 
@@ -393,10 +407,10 @@ struct RowShape {
   unsigned rows;   // per block, at most the matrix's
 };
 
-// Short rows share a block of about 256 threads.
+// Short rows share a block of 8 to 12 warps.
 RowShape row_shape(uint64_t rows, uint32_t cols, int vec) {
   const unsigned warps = (unsigned)(((uint64_t)cols + chunk_cols(vec) - 1) / chunk_cols(vec));
-  const unsigned fit = std::max(8 / warps, 1u);
+  const unsigned fit = warps <= 8 ? std::max(warps > 4 && warps <= 6 ? 12 / warps : 8 / warps, 1u) : 1u;
   return {warps, (unsigned)std::min<uint64_t>(fit, std::max<uint64_t>(rows, 1))};
 }
 
@@ -408,11 +422,12 @@ uint32_t wide_parts(uint64_t rows) {
 uint32_t back_wide_from(int vec) { return kBackThreads / 32 * chunk_cols(vec); }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch2(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s,
-                    Args... args) {
+cudaError_t launch2_smem(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -420,6 +435,12 @@ cudaError_t launch2(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch2(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s,
+                    Args... args) {
+  return launch2_smem(kernel, grid, block, 0, s, args...);
 }
 
 // Blocks of `threads` that all SMs hold at once (cached: the query costs
@@ -479,9 +500,10 @@ cudaError_t back_run(NormBackArgs& a, const RowShape& r, cudaStream_t s) {
   unsigned grid = 0;
   const cudaError_t e = row_grid(kernel, r, a.rows, &grid);
   if (e != cudaSuccess) return e;
-  grid = std::min(std::max(grid, 1u), kBackParts / r.rows);  // no rows: one block writes zeros
-  a.parts = grid * r.rows;
-  return launch2(kernel, dim3(grid), dim3(r.warps * 32, r.rows), s, a);
+  grid = std::min(std::max(grid, 1u), kBackParts);  // no rows: one block writes zeros
+  a.parts = grid;
+  const size_t smem = r.rows > 1 ? (size_t)lane_vals(VEC) * r.warps * 32 * sizeof(float) : 0;
+  return launch2_smem(kernel, dim3(grid), dim3(r.warps * 32, r.rows), smem, s, a);
 }
 
 template <int DT, int VEC>
@@ -517,14 +539,8 @@ cudaError_t launch_rms_norm(cr_dtype d, const NormArgs& a, int vec, cudaStream_t
 }
 
 uint32_t norm_back_parts(uint64_t rows, uint32_t cols) {
-  uint32_t most = cols > back_wide_from(0) ? wide_parts(rows) : 1;
-  for (int vec : {0, 1}) {
-    if (cols > back_wide_from(vec)) continue;
-    const RowShape r = row_shape(rows, cols, vec);
-    const uint64_t blocks = std::max<uint64_t>((rows + r.rows - 1) / r.rows, 1);
-    most = std::max(most, (uint32_t)std::min<uint64_t>(blocks, kBackParts / r.rows) * r.rows);
-  }
-  return most;
+  const uint32_t narrow = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(rows, 1), kBackParts);
+  return cols > back_wide_from(1) ? wide_parts(rows) : narrow;  // no less than wide_parts
 }
 
 cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, NormBackArgs a, int vec, cudaStream_t s) {
