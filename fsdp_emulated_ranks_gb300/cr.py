@@ -56,7 +56,8 @@ EXPORTS = ["cr_status_string", "cr_last_error", "cr_version", "cr_chunk_len",
 FFN_EXPORTS = ["cr_q8_store", "cr_q8_load", "cr_rms_norm",
                "cr_rms_norm_backward_workspace_bytes", "cr_rms_norm_backward",
                "cr_glu_workspace_bytes", "cr_glu", "cr_glu_act_backward",
-               "cr_glu_backward_workspace_bytes", "cr_glu_backward", "cr_glu_wait_word"]
+               "cr_glu_backward_workspace_bytes", "cr_glu_backward", "cr_ffn_call",
+               "cr_glu_wait_word"]
 
 ACT_SILU, ACT_GELU = 0, 1
 _ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
@@ -189,16 +190,7 @@ def lib() -> C.CDLL:
     L.cr_adamw_step.argtypes = [sz, vp, vp, vp, vp, C.POINTER(AdamWCfg), vp, vp]
     L.cr_comm_elems.argtypes = [i, i, i, sz, i, C.POINTER(C.c_uint64),
                                 C.POINTER(C.c_uint64), C.POINTER(i)]
-    q8 = C.POINTER(Q8)
-    L.cr_q8_store.argtypes = [vp, sz, sz, sz, i, q8, vp]
-    L.cr_q8_load.argtypes = [q8, sz, sz, vp, sz, i, vp]
-    L.cr_rms_norm.argtypes = [vp, sz, vp, sz, vp, sz, sz, i, C.c_double, vp, sz, vp, sz, q8, vp, vp]
-    L.cr_rms_norm_backward.argtypes = [vp, sz, vp, sz, q8, vp, vp, vp, sz, sz, sz, i, vp, sz, vp, i,
-                                       vp, sz, vp]
-    L.cr_glu.argtypes = [vp, sz, vp, sz, vp, sz, sz, sz, sz, i, i, vp, sz, q8, q8, vp, sz, vp]
-    L.cr_glu_act_backward.argtypes = [vp, sz, q8, q8, sz, sz, i, i, vp, sz, vp, sz, vp, sz, vp]
-    L.cr_glu_backward.argtypes = [vp, sz, q8, q8, vp, sz, q8, vp, sz, vp, sz, sz, sz, sz, i, i,
-                                  vp, sz, vp, vp, i, vp, sz, vp, sz, vp]
+    L.cr_ffn_call.argtypes = [i, vp]
     L.cr_glu_wait_word.restype, L.cr_glu_wait_word.argtypes = C.c_longlong, [i]
     for name, n in (("cr_rms_norm_backward", 2), ("cr_glu", 3), ("cr_glu_backward", 3)):
         fn = getattr(L, name + "_workspace_bytes")
@@ -716,22 +708,34 @@ def _act(a) -> int:
     return a if isinstance(a, int) else _ACTS[a]
 
 
-def _q8(q):
-    return None if q is None else C.byref(q)
+# cr_ffn_call: each call's number, and its arguments as 64-bit words.  Packing
+# them and passing one pointer costs ctypes less than up to 26 arguments do.
+_FFN_CALLS = {"cr_q8_store": 0, "cr_q8_load": 1, "cr_rms_norm": 2, "cr_rms_norm_backward": 3,
+              "cr_glu": 4, "cr_glu_act_backward": 5, "cr_glu_backward": 6}
+_FFN_NAMES = list(_FFN_CALLS)
+_STORE, _LOAD, _NORM, _NORM_BACK, _GLU, _GLU_ACT, _GLU_BACK = (
+    struct.Struct("=" + words).pack for words in
+    ("4Qq2Q", "5QqQ", "7Qqd7Q", "11Qq3Qq3Q", "9Q2q7Q", "6Q2q7Q", "14Q2q4Qq5Q"))
+
+
+def _q8(q) -> int:
+    return 0 if q is None else C.addressof(q)
+
+
+def _call(op: int, words: bytes) -> None:
+    status = lib().cr_ffn_call(op, words)
+    if status:
+        _check(status, _FFN_NAMES[op])
 
 
 def cr_q8_store(x, rows, cols, dtype, q: Q8, stream=None, ldx=None) -> None:
     x, ldx = _mat(x, ldx)
-    status = lib().cr_q8_store(x, ldx, rows, cols, _dtype(dtype), _q8(q), _stream(stream))
-    if status:
-        _check(status, "cr_q8_store")
+    _call(0, _STORE(x, ldx, rows, cols, _dtype(dtype), _q8(q), _stream(stream)))
 
 
 def cr_q8_load(q: Q8, rows, cols, x, dtype, stream=None, ldx=None) -> None:
     x, ldx = _mat(x, ldx)
-    status = lib().cr_q8_load(_q8(q), rows, cols, x, ldx, _dtype(dtype), _stream(stream))
-    if status:
-        _check(status, "cr_q8_load")
+    _call(1, _LOAD(_q8(q), rows, cols, x, ldx, _dtype(dtype), _stream(stream)))
 
 
 def cr_rms_norm(x, residual, weight, rows, cols, dtype, eps, sum, y, y8: Q8 = None, rstd=None,
@@ -740,10 +744,8 @@ def cr_rms_norm(x, residual, weight, rows, cols, dtype, eps, sum, y, y8: Q8 = No
     residual, ldr = _mat(residual, ldr)
     sum, ldsum = _mat(sum, ldsum)
     y, ldy = _mat(y, ldy)
-    status = lib().cr_rms_norm(x, ldx, residual, ldr, _ptr(weight), rows, cols, _dtype(dtype), eps,
-                               sum, ldsum, y, ldy, _q8(y8), _ptr(rstd), _stream(stream))
-    if status:
-        _check(status, "cr_rms_norm")
+    _call(2, _NORM(x, ldx, residual, ldr, _ptr(weight), rows, cols, _dtype(dtype), eps, sum,
+              ldsum, y, ldy, _q8(y8), _ptr(rstd), _stream(stream)))
 
 
 def cr_rms_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
@@ -757,12 +759,9 @@ def cr_rms_norm_backward(dy, h, h8: Q8, weight, rstd, dres, rows, cols, dtype, d
     h, ldh = _mat(h, ldh)
     dres, lddres = _mat(dres, lddres)
     dx, lddx = _mat(dx, lddx)
-    status = lib().cr_rms_norm_backward(dy, lddy, h, ldh, _q8(h8), _ptr(weight), _ptr(rstd), dres,
-                                        lddres, rows, cols, _dtype(dtype), dx, lddx, _ptr(dweight),
-                                        _dtype(dw_dtype), _ptr(workspace), workspace_bytes,
-                                        _stream(stream))
-    if status:
-        _check(status, "cr_rms_norm_backward")
+    _call(3, _NORM_BACK(dy, lddy, h, ldh, _q8(h8), _ptr(weight), _ptr(rstd), dres, lddres, rows,
+              cols, _dtype(dtype), dx, lddx, _ptr(dweight), _dtype(dw_dtype), _ptr(workspace),
+              workspace_bytes, _stream(stream)))
 
 
 def cr_glu_workspace_bytes(tokens: int, dim: int, ffn: int) -> int:
@@ -776,11 +775,8 @@ def cr_glu(x, wg, wu, tokens, dim, ffn, dtype, act, a, g8: Q8 = None, u8: Q8 = N
     wg, ldwg = _mat(wg, ldwg)
     wu, ldwu = _mat(wu, ldwu)
     a, lda = _mat(a, lda)
-    status = lib().cr_glu(x, ldx, wg, ldwg, wu, ldwu, tokens, dim, ffn, _dtype(dtype), _act(act),
-                          a, lda, _q8(g8), _q8(u8), _ptr(workspace), workspace_bytes,
-                          _stream(stream))
-    if status:
-        _check(status, "cr_glu")
+    _call(4, _GLU(x, ldx, wg, ldwg, wu, ldwu, tokens, dim, ffn, _dtype(dtype), _act(act), a,
+              lda, _q8(g8), _q8(u8), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def cr_glu_act_backward(da, g8: Q8, u8: Q8, tokens, ffn, dtype, act, dg, du, a=None, stream=None,
@@ -789,10 +785,8 @@ def cr_glu_act_backward(da, g8: Q8, u8: Q8, tokens, ffn, dtype, act, dg, du, a=N
     dg, lddg = _mat(dg, lddg)
     du, lddu = _mat(du, lddu)
     a, lda = _mat(a, lda)
-    status = lib().cr_glu_act_backward(da, ldda, _q8(g8), _q8(u8), tokens, ffn, _dtype(dtype),
-                                       _act(act), dg, lddg, du, lddu, a, lda, _stream(stream))
-    if status:
-        _check(status, "cr_glu_act_backward")
+    _call(5, _GLU_ACT(da, ldda, _q8(g8), _q8(u8), tokens, ffn, _dtype(dtype), _act(act), dg,
+              lddg, du, lddu, a, lda, _stream(stream)))
 
 
 def cr_glu_backward_workspace_bytes(tokens: int, dim: int, ffn: int) -> int:
@@ -808,12 +802,9 @@ def cr_glu_backward(da, g8: Q8, u8: Q8, x, x8: Q8, wg, wu, tokens, dim, ffn, dty
     wu, ldwu = _mat(wu, ldwu)
     dx, lddx = _mat(dx, lddx)
     a, lda = _mat(a, lda)
-    status = lib().cr_glu_backward(da, ldda, _q8(g8), _q8(u8), x, ldx, _q8(x8), wg, ldwg, wu, ldwu,
-                                   tokens, dim, ffn, _dtype(dtype), _act(act), dx, lddx, _ptr(dwg),
-                                   _ptr(dwu), _dtype(dw_dtype), a, lda, _ptr(workspace),
-                                   workspace_bytes, _stream(stream))
-    if status:
-        _check(status, "cr_glu_backward")
+    _call(6, _GLU_BACK(da, ldda, _q8(g8), _q8(u8), x, ldx, _q8(x8), wg, ldwg, wu, ldwu, tokens,
+              dim, ffn, _dtype(dtype), _act(act), dx, lddx, _ptr(dwg), _ptr(dwu), _dtype(dw_dtype), a,
+              lda, _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def cr_glu_wait_word(clear: bool = False) -> int:
@@ -834,7 +825,7 @@ _PREPARABLE = frozenset([
     "cr_fsdp2_step_planned", "cr_all_reduce_range", "cr_reduce_scatter_range",
     "cr_fsdp_step_range", "cr_accumulate", "cr_all_reduce_accumulate", "cr_adamw_step",
     "cr_q8_store", "cr_q8_load", "cr_rms_norm", "cr_rms_norm_backward", "cr_glu",
-    "cr_glu_act_backward", "cr_glu_backward"])
+    "cr_glu_act_backward", "cr_glu_backward", "cr_ffn_call"])
 # Functions without side effects that a wrapper may call while it marshals.
 _PURE = frozenset(["cr_last_error", "cr_status_string", "cr_chunk_len", "cr_version",
                    "cr_fsdp_clip_workspace_bytes", "cr_shard_range", "cr_slab_range",
@@ -861,7 +852,8 @@ class _Recorder:
             raise TypeError(f"prepare() records launching entry points only, not {name}")
 
         def record(*args):
-            self.calls.append((name, fn, args))
+            called = _FFN_NAMES[args[0]] if name == "cr_ffn_call" else name
+            self.calls.append((called, fn, args))
             return 0
         return record
 
@@ -872,8 +864,9 @@ class Prepared:
     __slots__ = ("name", "_calls", "_keep")
 
     def __init__(self, name, calls, keep):
-        # keep: the wrapper's arguments, so that the tensors and the bucket
-        # plan whose addresses were recorded outlive the prepared call
+        # keep: the wrapper and its arguments, so that the tensors, the bucket
+        # plan and the 8-bit matrices whose addresses were recorded outlive the
+        # prepared call
         self.name, self._calls, self._keep = name, calls, keep
 
     def __call__(self) -> None:
@@ -913,4 +906,4 @@ def prepare(wrapper, *args, **kwargs) -> Prepared:
     name = getattr(wrapper, "__name__", "call")
     if not rec.calls:
         raise ValueError(f"{name} launches nothing that prepare() could record")
-    return Prepared(name, rec.calls, (args, kwargs))
+    return Prepared(name, rec.calls, (wrapper, args, kwargs))

@@ -452,6 +452,43 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr
   return launched(launch_glu_back(dw_dtype, k, s), "cr_glu_backward");
 }
 
+cr_status cr_ffn_call(cr_ffn_op op, const void* words) {
+  if (!words) return fail(CR_ERR_INVALID_ARG, "words is NULL");
+  const uint64_t* w = static_cast<const uint64_t*>(words);
+  const auto in = [&](int i) { return reinterpret_cast<const void*>(w[i]); };
+  const auto out = [&](int i) { return reinterpret_cast<void*>(w[i]); };
+  const auto q = [&](int i) { return reinterpret_cast<const cr_q8*>(w[i]); };
+  const auto type = [&](int i) { return (cr_dtype)w[i]; };
+  const auto act = [&](int i) { return (cr_act)w[i]; };
+  const auto stream = [&](int i) { return reinterpret_cast<cr_stream_t>(w[i]); };
+  switch (op) {
+    case CR_CALL_Q8_STORE: return cr_q8_store(in(0), w[1], w[2], w[3], type(4), q(5), stream(6));
+    case CR_CALL_Q8_LOAD: return cr_q8_load(q(0), w[1], w[2], out(3), w[4], type(5), stream(6));
+    case CR_CALL_RMS_NORM: {
+      double eps;
+      memcpy(&eps, &w[8], sizeof(eps));
+      return cr_rms_norm(in(0), w[1], in(2), w[3], in(4), w[5], w[6], type(7), eps, out(9), w[10],
+                         out(11), w[12], q(13), static_cast<float*>(out(14)), stream(15));
+    }
+    case CR_CALL_RMS_NORM_BACKWARD:
+      return cr_rms_norm_backward(in(0), w[1], in(2), w[3], q(4), in(5),
+                                  static_cast<const float*>(in(6)), in(7), w[8], w[9], w[10],
+                                  type(11), out(12), w[13], out(14), type(15), out(16), w[17],
+                                  stream(18));
+    case CR_CALL_GLU:
+      return cr_glu(in(0), w[1], in(2), w[3], in(4), w[5], w[6], w[7], w[8], type(9), act(10),
+                    out(11), w[12], q(13), q(14), out(15), w[16], stream(17));
+    case CR_CALL_GLU_ACT_BACKWARD:
+      return cr_glu_act_backward(in(0), w[1], q(2), q(3), w[4], w[5], type(6), act(7), out(8), w[9],
+                                 out(10), w[11], out(12), w[13], stream(14));
+    case CR_CALL_GLU_BACKWARD:
+      return cr_glu_backward(in(0), w[1], q(2), q(3), in(4), w[5], q(6), in(7), w[8], in(9), w[10],
+                             w[11], w[12], w[13], type(14), act(15), out(16), w[17], out(18),
+                             out(19), type(20), out(21), w[22], out(23), w[24], stream(25));
+  }
+  return fail(CR_ERR_INVALID_ARG, "unknown call %d", (int)op);
+}
+
 long long cr_glu_wait_word(int clear) {
   unsigned int word = 0;
   const cudaError_t e = glu_wait_word(clear != 0, &word);

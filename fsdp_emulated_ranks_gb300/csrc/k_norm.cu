@@ -99,14 +99,13 @@ __device__ __forceinline__ void norm_st(const NormArgs& a, uint64_t row, uint32_
 // to kWideFrom columns.
 constexpr int row_threads(int vec) { return (int)(kWideFrom / chunk_cols(vec)) * 32; }
 
-// Block (32 * warps per row, rows per block), persistent.  With vectors the
-// next row is loaded while this one is reduced and written; the scalar kernel
-// has fewer registers for it and relies on several blocks an SM instead.
+// Block (32 * warps per row, rows per block), persistent.  The next row is
+// loaded while this one is reduced and written.  The scalar kernel reads the
+// weights again for each row, so that two blocks of 17 warps fit an SM.
 template <int DT, int VEC>
-__global__ void __launch_bounds__(row_threads(VEC)) __maxnreg__(VEC ? 128 : 40) k_rms_norm(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(row_threads(VEC)) __maxnreg__(VEC ? 128 : 48) k_rms_norm(const __grid_constant__ NormArgs a) {
   pdl_enter();
   __shared__ float part[2][kMaxWarps];
-  constexpr bool kLoadAhead = VEC != 0;
   const int lane = threadIdx.x & 31;
   const uint32_t base = (threadIdx.x >> 5) * chunk_cols(VEC);
   const uint64_t step = (uint64_t)gridDim.x * blockDim.y;
@@ -118,23 +117,18 @@ __global__ void __launch_bounds__(row_threads(VEC)) __maxnreg__(VEC ? 128 : 40) 
     else
       in.clear();
   };
-  if (kLoadAhead) {
-    load((uint64_t)blockIdx.x * blockDim.y + threadIdx.y);
-    w.load(a.weight, base, a.cols, lane);
-  }
+  load((uint64_t)blockIdx.x * blockDim.y + threadIdx.y);
+  if (VEC) w.load(a.weight, base, a.cols, lane);
   int buf = 0;
   // every row of a block's turn takes part in the barriers
   for (uint64_t first = (uint64_t)blockIdx.x * blockDim.y; first < a.rows; first += step, buf ^= 1) {
     const uint64_t row = first + threadIdx.y;
-    if (!kLoadAhead) {
-      load(row);
-      w.load(a.weight, base, a.cols, lane);
-    }
     float h[lane_vals(VEC)], s = 0.0f;
     in.values(h);
 #pragma unroll
     for (int i = 0; i < lane_vals(VEC); ++i) s = fmaf(h[i], h[i], s);
-    if (kLoadAhead) load(row + step);
+    load(row + step);
+    if (!VEC) w.load(a.weight, base, a.cols, lane);
     const float rstd = rsqrtf(fmaf(row_sum(s, part, buf), a.inv_cols, a.eps));
     if (row >= a.rows) continue;
     norm_st<DT, VEC>(a, row, base, lane, h, w, rstd);

@@ -172,6 +172,21 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8,
                           void* workspace, size_t workspace_bytes,
                           cr_stream_t stream);
 
+/* The calls above from one array of 64-bit words, for bindings whose cost grows
+ * with the number of arguments: words[] holds the call's arguments in order
+ * (pointers, sizes, enum values and the stream as unsigned integers, a double
+ * as its bits). */
+typedef enum {
+  CR_CALL_Q8_STORE = 0,
+  CR_CALL_Q8_LOAD = 1,
+  CR_CALL_RMS_NORM = 2,
+  CR_CALL_RMS_NORM_BACKWARD = 3,
+  CR_CALL_GLU = 4,
+  CR_CALL_GLU_ACT_BACKWARD = 5,
+  CR_CALL_GLU_BACKWARD = 6
+} cr_ffn_op;
+cr_status cr_ffn_call(cr_ffn_op op, const void* words);
+
 /* The block's products wait on barriers inside the kernel, each wait for about
  * half a second at most.  A wait that runs out (it never should) ends the
  * kernel, leaves its results undefined and sets this word, which stays set
