@@ -168,6 +168,11 @@ uint64_t padded(uint64_t rows, uint64_t cols) { return rows * padded_ld(cols); }
 // workspace itself is 16-byte aligned).
 int vec_with(int vec, const void* p) { return vec == 2 && !aligned(p, 32) ? 1 : vec; }
 
+// Tokens up to which dW's products take dg and du in two bf16 parts.  Over more
+// tokens their rounding errors average out against the result's own; over a
+// few they would not, and there one more K block costs next to nothing.
+constexpr uint64_t kExactTokens = 64;
+
 // TMA reads operands whose rows start on 16-byte boundaries; any other is
 // copied to `ws` first.
 void operand(CopyBf16* copies, Mat* m, uint64_t rows, uint64_t cols, uint16_t* ws) {
@@ -313,7 +318,7 @@ cr_status cr_glu_act_backward(const void* da, size_t ldda, const cr_q8* g8, cons
   if (st != CR_OK) return st;
   if (tokens == 0 || ffn == 0 || (!dg && !du && !a_out)) return ok();
   ActBackArgs k = {mat(da, ldda), mat(dg, lddg), mat(du, lddu), mat(a_out, lda),
-                   q8_of(g8),     q8_of(u8),     tokens,        (uint32_t)ffn};
+                   q8_of(g8),     q8_of(u8),     tokens,        (uint32_t)ffn, {}, {}};
   return launched(launch_act_back(act, k, nullptr, a.vec(), stream_of(stream)),
                   "cr_glu_act_backward");
 }
@@ -367,8 +372,9 @@ cr_status cr_glu(const void* x, size_t ldx, const void* wg, size_t ldwg, const v
 size_t cr_glu_backward_workspace_bytes(size_t tokens, size_t dim, size_t ffn) {
   if (tokens >= (1ull << 31) || dim >= (1ull << 31) || ffn >= (1ull << 31)) return 0;
   // dg and du; x restored from its checkpoint, in two parts; copies of
-  // weights that are not aligned
-  return 2 * (2 * padded(tokens, ffn) + 2 * padded(tokens, dim) + 2 * padded(ffn, dim));
+  // weights that are not aligned; what dg and du were rounded by
+  const size_t rest = tokens <= kExactTokens ? 2 * padded(tokens, ffn) : 0;
+  return 2 * (2 * padded(tokens, ffn) + 2 * padded(tokens, dim) + 2 * padded(ffn, dim) + rest);
 }
 
 cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr_q8* u8,
@@ -415,13 +421,19 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr
   const Mat dg = {ws, padded_ld(ffn)};
   const Mat du = {ws + padded(tokens, ffn), padded_ld(ffn)};
   uint16_t* const xs = ws + 2 * padded(tokens, ffn);
+  Mat dg_lo = {}, du_lo = {};
+  if (dw && tokens <= kExactTokens) {
+    dg_lo = Mat{xs + 2 * padded(tokens, dim) + 2 * padded(ffn, dim), padded_ld(ffn)};
+    du_lo = Mat{static_cast<uint16_t*>(dg_lo.p) + padded(tokens, ffn), padded_ld(ffn)};
+  }
   cudaError_t e = cudaSuccess;
   const SplitArgs split = {q8_of(x8), Mat{xs, padded_ld(dim)},
                            Mat{xs + padded(tokens, dim), padded_ld(dim)}, tokens, (uint32_t)dim,
                            xa.vec()};
   const bool splits = dw && x8 && tokens && dim;
   if (tokens && ffn) {
-    ActBackArgs k = {mat(da, ldda), dg, du, mat(a_out, lda), q8_of(g8), q8_of(u8), tokens, (uint32_t)ffn};
+    ActBackArgs k = {mat(da, ldda), dg,     du, mat(a_out, lda), q8_of(g8), q8_of(u8),
+                     tokens,        (uint32_t)ffn, dg_lo, du_lo};
     if (!dx && !dw) k.dg = k.du = Mat{nullptr, 0};
     if (k.dg.p || k.a.p)
       e = launch_act_back(act, k, splits ? &split : nullptr, vec_with(act_vec, ws), s);
@@ -430,6 +442,7 @@ cr_status cr_glu_backward(const void* da, size_t ldda, const cr_q8* g8, const cr
   if (dim == 0 || (!dw && !(dx && tokens))) return ok();
   GluBackArgs k = {};
   k.dg = dg, k.du = du;
+  k.dg_lo = dg_lo, k.du_lo = du_lo;
   k.x = mat(x, ldx);
   k.wg = mat(wg, ldwg), k.wu = mat(wu, ldwu);
   ws = xs;

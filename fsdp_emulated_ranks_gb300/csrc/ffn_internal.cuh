@@ -69,6 +69,7 @@ struct ActBackArgs {
   Q8 g8, u8;
   uint64_t rows;
   uint32_t cols;
+  Mat dg_lo, du_lo;  // what dg and du were rounded by (optional)
 };
 
 // The values q stands for as bf16 hi + lo (lo: what the rounding of hi left).
@@ -88,7 +89,8 @@ struct GluArgs {
 };
 
 struct GluBackArgs {
-  Mat dg, du, x, x_lo, wg, wu, dx;  // x_lo: what x lacks to a checkpoint's value, or absent
+  Mat dg, du, x, wg, wu, dx;
+  Mat dg_lo, du_lo, x_lo;  // what dg, du and x were rounded by, or absent
   void *dwg, *dwu;  // [ffn][dim]
   uint32_t tokens, dim, ffn;
 };

@@ -56,12 +56,13 @@ constexpr uint32_t kTileSmem = kStages * kStageBytes + 1024;  // + room to align
 constexpr int kTileThreads = 320;
 
 struct TileArgs {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a[4], b[2];     // kDw: a[2], a[3] are what a[0], a[1] were rounded by
   Mat out[2];
   Q8 g8, u8;
   uint32_t rows, cols;        // of an output
   uint32_t seg_blocks;        // K blocks of one product
-  uint32_t blocks;            // K blocks of a tile: one or two products
+  uint32_t blocks;            // K blocks of a tile: one to three products
+  uint32_t a_lo;              // kDw: the second product takes a[2 + output]
   uint32_t tiles_m, tiles_n;  // of an output
   uint32_t tiles;             // k_tiles: tiles 0 .. tiles - 1 of all outputs
   uint32_t first;             // k_split: its first tile
@@ -303,7 +304,7 @@ __device__ __forceinline__ void multiply_block(uint32_t acc, uint32_t sa, uint32
 template <int MODE>
 __device__ __forceinline__ void load_block(const TileArgs& a, uint32_t which, uint32_t row,
                                            uint32_t tn, uint32_t k, uint32_t sa, uint32_t bar) {
-  const uint32_t seg = k >= a.seg_blocks, sb = sa + kABytes;
+  const uint32_t seg = (k >= a.seg_blocks) + (k >= 2 * a.seg_blocks), sb = sa + kABytes;
   const int k0 = (int)((k - seg * a.seg_blocks) * kK), m0 = (int)row;
   tc::bar_expect(bar, kStageBytes);
   if constexpr (MODE == kGlu) {
@@ -314,12 +315,15 @@ __device__ __forceinline__ void load_block(const TileArgs& a, uint32_t which, ui
     if constexpr (MODE == kDx) {
       tc::tma_load(sa, &a.a[seg], k0, m0, bar);
     } else {
-      tc::tma_load(sa, &a.a[which], m0, k0, bar);
-      tc::tma_load(sa + 8192, &a.a[which], m0 + 64, k0, bar);
+      // (dg, x), then (rest of dg, x), then (dg, rest of x): those there are
+      const CUtensorMap* left = &a.a[which + (a.a_lo && seg == 1 ? 2 : 0)];
+      tc::tma_load(sa, left, m0, k0, bar);
+      tc::tma_load(sa + 8192, left, m0 + 64, k0, bar);
     }
+    const CUtensorMap* right = &a.b[MODE == kDx ? seg : seg == a.a_lo + 1];
 #pragma unroll
     for (int j = 0; j < kN / 64; ++j)
-      tc::tma_load(sb + j * 8192, &a.b[seg], (int)(tn * kN) + j * 64, k0, bar);
+      tc::tma_load(sb + j * 8192, right, (int)(tn * kN) + j * 64, k0, bar);
   }
 }
 
@@ -922,7 +926,8 @@ cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& g, cudaStream_t s) {
   const uint32_t outputs = (g.dwg ? 1 : 0) + (g.dwu ? 1 : 0);
   if (outputs) {
     TileArgs& a = b.dw;
-    e = shape(a, g.ffn, g.dim, kN, g.tokens, g.x_lo.p ? 2 : 1);
+    a.a_lo = g.dg_lo.p != nullptr;
+    e = shape(a, g.ffn, g.dim, kN, g.tokens, 1 + a.a_lo + (g.x_lo.p != nullptr));
     a.width = 32;
     uint32_t n = 0;
     for (int k = 0; k < 2 && e == cudaSuccess; ++k) {
@@ -930,7 +935,9 @@ cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& g, cudaStream_t s) {
       if (!out) continue;
       a.out[n] = Mat{out, g.dim};
       a.width = std::min(a.width, out_width(a.out[n], g.ffn, dw == CR_BF16 ? 2 : 4));
-      e = encode(&a.a[n++], k ? g.du : g.dg, g.tokens, g.ffn, kK);
+      e = encode(&a.a[n], k ? g.du : g.dg, g.tokens, g.ffn, kK);
+      if (e == cudaSuccess) e = encode(&a.a[2 + n], k ? g.du_lo : g.dg_lo, g.tokens, g.ffn, kK);
+      ++n;
     }
     if (e == cudaSuccess) e = encode(&a.b[0], g.x, g.tokens, g.dim, kK);
     if (e == cudaSuccess) e = encode(&a.b[1], g.x_lo, g.tokens, g.dim, kK);

@@ -92,6 +92,12 @@ __global__ void __launch_bounds__(kBlock) k_q8_load(const __grid_constant__ Q8 q
       });
 }
 
+// What rounding v to bf16 leaves; nothing where the rounded value is not finite.
+__device__ __forceinline__ float bf16_rest(float v) {
+  const float hi = ffn_bf16((uint16_t)ffn_bf16x2(v, 0.0f));
+  return fabsf(hi) <= kFloatMax ? v - hi : 0.0f;
+}
+
 // The values of q's chunks as hi + lo.
 template <int VEC>
 __device__ __forceinline__ void split_chunks(const SplitArgs& a, const ChunkRange& r) {
@@ -103,8 +109,7 @@ __device__ __forceinline__ void split_chunks(const SplitArgs& a, const ChunkRang
         float v[lane_vals(VEC)], rest[lane_vals(VEC)];
         in[j].values(v);
 #pragma unroll
-        for (int i = 0; i < lane_vals(VEC); ++i)
-          rest[i] = v[i] - ffn_bf16((uint16_t)ffn_bf16x2(v[i], 0.0f));
+        for (int i = 0; i < lane_vals(VEC); ++i) rest[i] = bf16_rest(v[i]);
         st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(a.hi, row), base, a.cols, lane, v);
         st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(a.lo, row), base, a.cols, lane, rest);
       });
@@ -156,8 +161,9 @@ __global__ void __launch_bounds__(kBlock) k_copy_bf16(const __grid_constant__ Co
       });
 }
 
-// blockIdx.y 1: x's checkpoint, split for the products that follow.
-template <int ACT, int VEC>
+// blockIdx.y 1: x's checkpoint, split for the products that follow.  REST: dg_lo
+// and du_lo are wanted too.
+template <int ACT, int VEC, bool REST>
 __global__ void __launch_bounds__(kBlock, 4) k_act_back(const __grid_constant__ ActBackArgs a,
                                                         const __grid_constant__ ChunkRange r,
                                                         const __grid_constant__ SplitArgs x,
@@ -189,6 +195,12 @@ __global__ void __launch_bounds__(kBlock, 4) k_act_back(const __grid_constant__ 
         if (a.dg.p) st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(a.dg, row), base, a.cols, lane, dg);
         if (a.du.p) st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(a.du, row), base, a.cols, lane, du);
         if (a.a.p) st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(a.a, row), base, a.cols, lane, u);
+        if constexpr (REST) {
+#pragma unroll
+          for (int i = 0; i < lane_vals(VEC); ++i) dg[i] = bf16_rest(dg[i]), du[i] = bf16_rest(du[i]);
+          st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(a.dg_lo, row), base, a.cols, lane, dg);
+          st_chunk<CR_BF16, VEC>(row_at<CR_BF16>(a.du_lo, row), base, a.cols, lane, du);
+        }
       });
 }
 
@@ -248,8 +260,10 @@ cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, const SplitArgs* x
   dim3 grid = chunk_grid(ChunkRange{std::max(r.chunks, xr.chunks), FastDiv{}}, 1);
   grid.y = x ? 2 : 1;
   return with_vec(vec, [&](auto v) {
-    return launch_pdl(act == CR_ACT_SILU ? k_act_back<CR_ACT_SILU, v()> : k_act_back<CR_ACT_GELU, v()>,
-                      grid, kBlock, s, a, r, x ? *x : SplitArgs{}, xr);
+    const bool silu = act == CR_ACT_SILU;
+    const auto kernel = a.dg_lo.p ? silu ? k_act_back<CR_ACT_SILU, v(), true> : k_act_back<CR_ACT_GELU, v(), true>
+                                  : silu ? k_act_back<CR_ACT_SILU, v(), false> : k_act_back<CR_ACT_GELU, v(), false>;
+    return launch_pdl(kernel, grid, kBlock, s, a, r, x ? *x : SplitArgs{}, xr);
   });
 }
 

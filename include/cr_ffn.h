@@ -151,7 +151,8 @@ cr_status cr_glu_act_backward(const void* da, size_t ldda, const cr_q8* g8,
 
 /* The whole backward pass of cr_glu:
  *     dx = dg wg + du wu,  dwg = dg^T x,  dwu = du^T x,  a = act(g) * u
- * with dg and du as above, rounded to bf16 as operands of the products.
+ * with dg and du as above, rounded to bf16 as operands of the products (for
+ * dwg and dwu of at most 64 tokens: as sums of two bf16 numbers).
  *   x or x8    the block's input, tokens x dim, as bf16 or as its 8-bit
  *              checkpoint (whose values enter the products as a sum of two
  *              bf16 numbers, exact to 2^-16): exactly one

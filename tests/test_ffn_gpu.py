@@ -460,7 +460,7 @@ def check_glu_backward(tokens, dim, ffn, held, dw_dt, kind, left, right):
     edg = 2.0 ** -18 * da.double().abs() * uv.abs() * (1 + gv.abs())
     edu = 2.0 ** -18 * da.double().abs() * gv.abs()
 
-    def check(got, pairs, terms, u_out, what):
+    def check(got, pairs, terms, u_out, what, exact=False):
         want = sum(l @ r for l, r, _ in pairs)
         mag = sum((l.abs() + e) @ r.abs() for l, r, e in pairs)
         err = sum(e @ r.abs() for _, r, e in pairs)
@@ -468,13 +468,14 @@ def check_glu_backward(tokens, dim, ffn, held, dw_dt, kind, left, right):
         assert torch.all((got.double() - want).abs() <= tol), what
         # the operands' rounding taken into account, what is left is the result's own
         # rounding and, where fp32 and 64 bits round an operand apart, a rare U16
-        near = sum(R.bf16(l) @ r for l, r, _ in pairs)
+        near = sum((l if exact else R.bf16(l)) @ r for l, r, _ in pairs)
         if got.numel() > 500:
             assert R.rel_norm(got, near) <= max(u_out, 2.0 ** -12), what
 
     check(dx, [(dg, wg.double(), edg), (du, wu.double(), edu)], 2 * ffn, R.U16, "dx")
-    check(dwg, [(dg.T, xv, edg.T)], tokens, R.U_OUT[dw_dt], "dwg")
-    check(dwu, [(du.T, xv, edu.T)], tokens, R.U_OUT[dw_dt], "dwu")
+    # up to 64 tokens dW takes dg and du in two parts
+    check(dwg, [(dg.T, xv, edg.T)], tokens, R.U_OUT[dw_dt], "dwg", tokens <= 64)
+    check(dwu, [(du.T, xv, edu.T)], tokens, R.U_OUT[dw_dt], "dwu", tokens <= 64)
 
 
 def test_glu_backward_outputs_alone():
