@@ -4,6 +4,7 @@ no kernel is launched), workspace sizes, and the reference formulas' own
 gradients against differences."""
 import os
 import re
+import struct
 
 import pytest
 import torch
@@ -168,6 +169,17 @@ def test_glu_backward_refusals():
         expect(3, glu_back, **bad)
     for bad in ({"dt": "f32"}, {"dw_dt": "i32"}, {"t": 1 << 31}):
         expect(2, glu_back, **bad)
+
+
+def test_packed_call_refusals(L):
+    words = struct.pack("=4Qq2Q", at(0), 64, 4, 64, 1, 0, 0)
+    assert L.cr_ffn_call(0, words) == 1 and b"q is NULL" in L.cr_last_error()
+    assert L.cr_ffn_call(99, words) == 1 and b"unknown call" in L.cr_last_error()
+    assert L.cr_ffn_call(0, None) == 1
+    p = cr.prepare(norm, x=None)
+    assert p._calls[0][0] == "cr_rms_norm"
+    with pytest.raises(cr.CRError, match="cr_rms_norm: .*x is NULL"):
+        p()
 
 
 def test_columns_of_one_buffer_do_not_overlap():
