@@ -115,49 +115,215 @@ __device__ __forceinline__ void split_chunks(const SplitArgs& a, const ChunkRang
       });
 }
 
-// 8 bf16 at p, which is 2-byte aligned, the first `n` of them in bounds: the
-// one or two 16-byte granules that hold them, shifted.  A granule is read only
-// if it holds an element that is in bounds.
-__device__ __forceinline__ void ld_shifted(const uint16_t* p, int n, uint4* lo, uint4* hi) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  const uint4* g = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
-  *lo = n > 0 ? g[0] : make_uint4(0, 0, 0, 0);
-  *hi = (int)(at & 15) + 2 * n > 16 ? g[1] : make_uint4(0, 0, 0, 0);
+// ---- rows off the vector grid ---------------------------------------------------------
+//
+// Where a row's start is not aligned, a lane's 8 columns are moved instead:
+// they start `lead` columns earlier, so that what is written is whole 16-byte
+// granules in spite of the row, and what is read is taken from the granules
+// that hold it, shifted.  Only the granules at a row's two ends are written by
+// elements.  (With a column a lane and 2-byte accesses the gate's backward
+// pass of 1777 x 4099 ran at 2.9 TB/s.)
+
+// A lane's columns first .. first + 7, of which lo .. hi - 1 (counted from
+// first) are in the row.
+struct Span8 {
+  int64_t first;
+  int lo, hi;
+};
+
+__device__ __forceinline__ Span8 span8(int64_t first, uint32_t cols) {
+  return {first, (int)max((int64_t)0, -first), (int)min((int64_t)8, (int64_t)cols - first)};
 }
 
-__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, uint32_t bytes) {
-  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = bytes & 8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = bytes & 4 ? w[i + 1] : w[i];
-  const uint32_t bits = (bytes & 2) * 8;
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+// Columns by which lanes start early, so that `p` + first * ES is a multiple of 16.
+template <int ES>
+__device__ __forceinline__ uint32_t lead_of(const void* p) {
+  return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15) / ES;
 }
 
-// blockIdx.y: which copy.  Rows of dst start on 16-byte boundaries, so a lane
-// writes 8 columns at once and reads them as shifted granules: with 2-byte
-// loads and stores the three operands of 1531 x 1001 x 2731 took 11 us.
+// The two granules that hold a span of bf16 (SIZE 16) or of codes (SIZE 8); one
+// is read only if it holds an element of the span.
+template <int SIZE>
+struct Granules {
+  static constexpr int kWords = SIZE / 4, es = SIZE / 8;
+  uint32_t w[2 * kWords];
+  uint32_t shift;  // bytes
+
+  __device__ __forceinline__ void load(const void* row, const Span8& s) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (uintptr_t)(s.first * es);
+    shift = (uint32_t)(at & (SIZE - 1));
+    const uintptr_t g = at - shift;
+    const int split = (int)(SIZE - shift) / es;  // elements of the first granule
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bool any = s.hi > s.lo && (k ? s.hi > split : s.lo < split);
+      if constexpr (SIZE == 16) {
+        const uint4 v = any ? reinterpret_cast<const uint4*>(g)[k] : make_uint4(0, 0, 0, 0);
+        w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+      } else {
+        const uint2 v = any ? reinterpret_cast<const uint2*>(g)[k] : make_uint2(0, 0);
+        w[2 * k] = v.x, w[2 * k + 1] = v.y;
+      }
+    }
+  }
+
+  // The span's SIZE bytes in w[0 .. kWords - 1].
+  __device__ __forceinline__ void align() {
+    if (SIZE == 16) {
+#pragma unroll
+      for (int i = 0; i < kWords + 2; ++i)
+        if (i + 2 < 2 * kWords) w[i] = shift & 8 ? w[i + 2] : w[i];
+    }
+#pragma unroll
+    for (int i = 0; i <= kWords; ++i)
+      if (i + 1 < 2 * kWords) w[i] = shift & 4 ? w[i + 1] : w[i];
+    const uint32_t bits = (shift & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+  }
+};
+
+// A span of an 8-bit matrix: its codes, and the scales of the one or two groups
+// it reaches into.
+struct SpanQ8 {
+  Granules<8> codes;
+  float s[2];
+  int next;  // first column (counted from the span's) of the second group
+
+  __device__ __forceinline__ void load(const Q8& q, uint64_t row, const Span8& sp) {
+    codes.load(q.codes + row * q.ld, sp);
+    const float* scales = q.scales + row * q.lds;
+    const int64_t group = (sp.first + sp.lo) / CR_Q8_GROUP;
+    next = (int)((group + 1) * CR_Q8_GROUP - sp.first);
+    s[0] = sp.hi > sp.lo ? scales[group] : 0.0f;
+    s[1] = sp.hi > next ? scales[group + 1] : 0.0f;
+  }
+
+  __device__ __forceinline__ void values(float* v) {
+    codes.align();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = from_e4m3x2(codes.w[i >> 1] >> (16 * (i & 1)));
+      v[2 * i] = f.x * (2 * i < next ? s[0] : s[1]);
+      v[2 * i + 1] = f.y * (2 * i + 1 < next ? s[0] : s[1]);
+    }
+  }
+};
+
+// A span's results: whole granules, or element by element at a row's ends.
+template <int DT>
+__device__ __forceinline__ void st_span(void* row, const Span8& s, const float* v) {
+  if constexpr (DT == CR_BF16) {
+    uint16_t* p = static_cast<uint16_t*>(row) + s.first;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = ffn_bf16x2(v[2 * i], v[2 * i + 1]);
+    if (s.lo == 0 && s.hi == 8) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= s.lo && i < s.hi) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
+  } else {
+    float* p = static_cast<float*>(row) + s.first;
+    if (s.lo == 0 && s.hi == 8) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= s.lo && i < s.hi) p[i] = v[i];
+    }
+  }
+}
+
+// bf16 results of a whole warp's spans where another matrix set the lead, so
+// that a granule begins `d` columns into a span: it is made of this lane's last
+// 8 - d results and the next lane's first d.  Lane 0's first and lane 31's last
+// go out by elements, as a row's ends do.
+__device__ __forceinline__ void st_spans(void* row, const Span8& s, uint32_t cols, int lane,
+                                         const float* v) {
+  uint16_t* p = static_cast<uint16_t*>(row) + s.first;
+  const int d = (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / 2;
+  if (d == 0) {  // the same in every lane
+    if (s.hi > s.lo) st_span<CR_BF16>(row, s, v);
+    return;
+  }
+  Granules<16> g;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    g.w[i] = ffn_bf16x2(v[2 * i], v[2 * i + 1]);
+    g.w[4 + i] = __shfl_down_sync(~0u, g.w[i], 1);
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < d && i >= s.lo && i < s.hi) p[i] = (uint16_t)(g.w[i / 2] >> (16 * (i & 1)));
+  }
+  g.shift = 2 * d;
+  g.align();
+  const Span8 own = span8(s.first + d, cols);
+  const int end = lane == 31 ? min(own.hi, 8 - d) : own.hi;
+  if (own.lo == 0 && end == 8) {
+    *reinterpret_cast<uint4*>(p + d) = make_uint4(g.w[0], g.w[1], g.w[2], g.w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= own.lo && i < end) p[d + i] = (uint16_t)(g.w[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+// Chunks of a matrix whose rows are walked in spans: one more column chunk
+// where a lead of up to 7 columns can push the last ones out.
+ChunkRange span_range(uint64_t rows, uint32_t cols) {
+  const uint64_t per_row = ((uint64_t)cols + 7 + 255) / 256;
+  return {rows * per_row, fastdiv_make(per_row, rows * per_row)};
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kBlock) k_q8_load_span(const __grid_constant__ Q8 q,
+                                                         const __grid_constant__ Mat x,
+                                                         uint32_t cols,
+                                                         const __grid_constant__ ChunkRange r) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  SpanQ8 in[kAhead];
+  Span8 span[kAhead];
+  for_chunks<0, kAhead>(
+      r,
+      [&](int j, uint64_t row, uint32_t base) {
+        const uint32_t lead = lead_of<DT == CR_BF16 ? 2 : 4>(row_at<DT>(x, row));
+        span[j] = span8((int64_t)base + 8 * lane - lead, cols);
+        in[j].load(q, row, span[j]);
+      },
+      [&](int j, uint64_t row, uint32_t) {
+        float v[8];
+        in[j].values(v);
+        if (span[j].hi > span[j].lo) st_span<DT>(row_at<DT>(x, row), span[j], v);
+      });
+}
+
+// blockIdx.y: which copy.  Rows of dst start on 16-byte boundaries.  (With
+// 2-byte loads and stores the three operands of 1531 x 1001 x 2731 took 11 us
+// instead of 6.)
 __global__ void __launch_bounds__(kBlock) k_copy_bf16(const __grid_constant__ CopyBf16 c) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const CopyBf16::One& m = c.one[blockIdx.y];
-  uint4 lo[kAhead], hi[kAhead];
+  Granules<16> in[kAhead];
   for_chunks<0, kAhead>(
       ChunkRange{m.chunks, m.per_row},
       [&](int j, uint64_t row, uint32_t base) {
-        const uint32_t col = base + 8 * lane;
-        const int n = col < m.cols ? (int)min(m.cols - col, 8u) : 0;
-        ld_shifted(reinterpret_cast<const uint16_t*>(row_at<CR_BF16>(m.src, row)) + col, n, &lo[j], &hi[j]);
+        in[j].load(row_at<CR_BF16>(m.src, row), span8((int64_t)base + 8 * lane, m.cols));
       },
       [&](int j, uint64_t row, uint32_t base) {
         const uint32_t col = base + 8 * lane;
         if (col >= m.cols) return;
-        const uintptr_t src = reinterpret_cast<uintptr_t>(row_at<CR_BF16>(m.src, row));
-        const uint4 v = shifted(lo[j], hi[j], (uint32_t)((src + 2 * col) & 15));
+        in[j].align();
         // columns past the row's end are the row's padding
-        *reinterpret_cast<uint4*>(row_at<CR_BF16>(m.dst, row) + 2 * col) = v;
+        *reinterpret_cast<uint4*>(row_at<CR_BF16>(m.dst, row) + 2 * (uint64_t)col) =
+            make_uint4(in[j].w[0], in[j].w[1], in[j].w[2], in[j].w[3]);
       });
 }
 
@@ -204,6 +370,54 @@ __global__ void __launch_bounds__(kBlock, 4) k_act_back(const __grid_constant__ 
       });
 }
 
+// The same on spans, led by the first output there is.
+template <int ACT, bool REST>
+__global__ void __launch_bounds__(kBlock, 4) k_act_back_span(const __grid_constant__ ActBackArgs a,
+                                                             const __grid_constant__ ChunkRange r,
+                                                             const __grid_constant__ SplitArgs x,
+                                                             const __grid_constant__ ChunkRange xr) {
+  pdl_enter();
+  if (blockIdx.y) return x.vec ? split_chunks<1>(x, xr) : split_chunks<0>(x, xr);
+  const int lane = threadIdx.x & 31;
+  const Mat& lead_mat = a.dg.p ? a.dg : a.du.p ? a.du : a.a;
+  Granules<16> in[1];
+  SpanQ8 gate[1], up[1];
+  Span8 span[1];
+  for_chunks<0, 1>(
+      r,
+      [&](int j, uint64_t row, uint32_t base) {
+        const uint32_t lead = lead_of<2>(row_at<CR_BF16>(lead_mat, row));
+        span[j] = span8((int64_t)base + 8 * lane - lead, a.cols);
+        in[j].load(row_at<CR_BF16>(a.da, row), span[j]);
+        gate[j].load(a.g8, row, span[j]);
+        up[j].load(a.u8, row, span[j]);
+      },
+      [&](int j, uint64_t row, uint32_t) {
+        float g[8], u[8], dg[8], du[8];
+        in[j].align();
+        gate[j].values(g);
+        up[j].values(u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t w = in[j].w[i / 2];
+          const float da = __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+          const float2 v = act_gate_slope<ACT>(g[i]);
+          dg[i] = da * u[i] * v.y;
+          du[i] = da * v.x;
+          u[i] *= v.x;
+        }
+        if (a.dg.p) st_spans(row_at<CR_BF16>(a.dg, row), span[j], a.cols, lane, dg);
+        if (a.du.p) st_spans(row_at<CR_BF16>(a.du, row), span[j], a.cols, lane, du);
+        if (a.a.p) st_spans(row_at<CR_BF16>(a.a, row), span[j], a.cols, lane, u);
+        if constexpr (REST) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dg[i] = bf16_rest(dg[i]), du[i] = bf16_rest(du[i]);
+          st_spans(row_at<CR_BF16>(a.dg_lo, row), span[j], a.cols, lane, dg);
+          st_spans(row_at<CR_BF16>(a.du_lo, row), span[j], a.cols, lane, du);
+        }
+      });
+}
+
 // A warp for every `ahead` chunks.
 dim3 chunk_grid(const ChunkRange& r, int ahead) {
   return dim3(flat_grid((r.chunks + ahead - 1) / ahead * 32));
@@ -211,32 +425,30 @@ dim3 chunk_grid(const ChunkRange& r, int ahead) {
 
 }  // namespace
 
-// f(integral constant) for the access width.
-template <typename F>
-cudaError_t with_vec(int vec, F f) {
-  switch (vec) {
-    case 2: return f(std::integral_constant<int, 2>());
-    case 1: return f(std::integral_constant<int, 1>());
-    default: return f(std::integral_constant<int, 0>());
-  }
-}
-
 cudaError_t launch_q8_store(cr_dtype d, const Mat& x, const Q8& q, uint64_t rows, uint32_t cols,
                             int vec, cudaStream_t s) {
   const ChunkRange r = chunk_range(rows, cols, vec);
-  return with_vec(vec, [&](auto v) {
+  const auto run = [&](auto v) {
     return launch_pdl(d == CR_BF16 ? k_q8_store<CR_BF16, v()> : k_q8_store<CR_F32, v()>,
                       chunk_grid(r, kAhead), kBlock, s, x, q, cols, r);
-  });
+  };
+  return vec == 2 ? run(std::integral_constant<int, 2>())
+                  : vec == 1 ? run(std::integral_constant<int, 1>()) : run(std::integral_constant<int, 0>());
 }
 
 cudaError_t launch_q8_load(cr_dtype d, const Q8& q, const Mat& x, uint64_t rows, uint32_t cols,
                            int vec, cudaStream_t s) {
+  if (vec == 0) {
+    const ChunkRange r = span_range(rows, cols);
+    return launch_pdl(d == CR_BF16 ? k_q8_load_span<CR_BF16> : k_q8_load_span<CR_F32>,
+                      chunk_grid(r, kAhead), kBlock, s, q, x, cols, r);
+  }
   const ChunkRange r = chunk_range(rows, cols, vec);
-  return with_vec(vec, [&](auto v) {
+  const auto run = [&](auto v) {
     return launch_pdl(d == CR_BF16 ? k_q8_load<CR_BF16, v()> : k_q8_load<CR_F32, v()>,
                       chunk_grid(r, kAhead), kBlock, s, q, x, cols, r);
-  });
+  };
+  return vec == 2 ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 1>());
 }
 
 void add_copy(CopyBf16* c, const Mat& src, const Mat& dst, uint64_t rows, uint32_t cols) {
@@ -255,16 +467,25 @@ cudaError_t launch_copy_bf16(const CopyBf16& c, cudaStream_t s) {
 
 cudaError_t launch_act_back(cr_act act, const ActBackArgs& a, const SplitArgs* x, int vec,
                             cudaStream_t s) {
-  const ChunkRange r = chunk_range(a.rows, a.cols, vec);
   const ChunkRange xr = x ? chunk_range(x->rows, x->cols, x->vec) : ChunkRange{};
+  const bool silu = act == CR_ACT_SILU;
+  if (vec == 0) {
+    const ChunkRange sr = span_range(a.rows, a.cols);
+    dim3 grid = chunk_grid(ChunkRange{std::max(sr.chunks, xr.chunks), FastDiv{}}, 1);
+    grid.y = x ? 2 : 1;
+    const auto kernel = a.dg_lo.p ? silu ? k_act_back_span<CR_ACT_SILU, true> : k_act_back_span<CR_ACT_GELU, true>
+                                  : silu ? k_act_back_span<CR_ACT_SILU, false> : k_act_back_span<CR_ACT_GELU, false>;
+    return launch_pdl(kernel, grid, kBlock, s, a, sr, x ? *x : SplitArgs{}, xr);
+  }
+  const ChunkRange r = chunk_range(a.rows, a.cols, vec);
   dim3 grid = chunk_grid(ChunkRange{std::max(r.chunks, xr.chunks), FastDiv{}}, 1);
   grid.y = x ? 2 : 1;
-  return with_vec(vec, [&](auto v) {
-    const bool silu = act == CR_ACT_SILU;
+  const auto run = [&](auto v) {
     const auto kernel = a.dg_lo.p ? silu ? k_act_back<CR_ACT_SILU, v(), true> : k_act_back<CR_ACT_GELU, v(), true>
                                   : silu ? k_act_back<CR_ACT_SILU, v(), false> : k_act_back<CR_ACT_GELU, v(), false>;
     return launch_pdl(kernel, grid, kBlock, s, a, r, x ? *x : SplitArgs{}, xr);
-  });
+  };
+  return vec == 2 ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 1>());
 }
 
 }  // namespace cr

@@ -308,6 +308,35 @@ def test_act_backward(rows, cols, kind, left, right):
         assert torch.equal(t, outs[k][0])
 
 
+@pytest.mark.parametrize("rows,cols", [(7, 1), (9, 100), (5, 255), (12, 257), (33, 513), (40, 1111)])
+@pytest.mark.parametrize("offs", [(0, 1, 2), (5, 0, 3), (4, 4, 7)])
+@pytest.mark.parametrize("over", [None, 0, 1, 2])
+def test_act_backward_rows_that_start_apart(rows, cols, offs, over):
+    """Inputs and outputs each at an alignment of their own, one of them over da: the bits of
+    the aligned call."""
+    g = gen(rows + cols)
+    q, codes, scales, _ = new_q8(rows, cols)
+    p, codes2, scales2, _ = new_q8(rows, cols)
+    cr.cr_q8_store(rand(g, rows, cols, "f32", 2.0), rows, cols, "f32", q)
+    cr.cr_q8_store(rand(g, rows, cols, "f32"), rows, cols, "f32", p)
+    da = rand(g, rows, cols, "bf16")
+    pad = (-cols) % 16 + 16
+    want = [empty(rows, cols, "bf16", 0, pad)[0] for _ in range(3)]
+    q2 = cr.Q8(strided(codes, 0, pad, 0), scales)
+    p2 = cr.Q8(strided(codes2, 0, pad, 0), scales2)
+    cr.cr_glu_act_backward(strided(da, 0, pad), q2, p2, rows, cols, "bf16", "gelu", *want)
+    outs = [empty(rows, cols, "bf16", off, 3 + k) for k, off in enumerate(offs)]
+    src = strided(da, 3, 2)
+    if over is not None:
+        outs[over][0].copy_(da)
+        src = outs[over][0]
+    cr.cr_glu_act_backward(src, cr.Q8(strided(codes, 1, 4, 0), scales), p, rows, cols, "bf16", "gelu",
+                           *[o[0] for o in outs])
+    for (out, wide), ref, off in zip(outs, want, offs):
+        assert torch.equal(out, ref)
+        untouched(wide, off, cols)
+
+
 # ---- the gated block --------------------------------------------------------------------------
 
 GLU_SHAPES = [(1, 1, 1), (1, 2048, 512), (2, 64, 128), (7, 63, 127), (16, 128, 256), (17, 65, 129),
