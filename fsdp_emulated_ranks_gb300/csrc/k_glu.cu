@@ -32,6 +32,7 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "ffn_internal.cuh"
@@ -138,21 +139,22 @@ __device__ __forceinline__ void st_values(const Mat& m, uint64_t row0, uint32_t 
   }
 }
 
-// Infinities have been made NaN where there are any (`inf`, the same for the
-// whole warp); otherwise none is left to look at.
-__device__ __forceinline__ float code_value(float v, float inv, bool inf) {
-  if (inf && fabsf(v) > kFloatMax) return __int_as_float(0x7fc00000);
+// INF: the warp's rows hold infinities, which the codes make NaN.
+template <bool INF>
+__device__ __forceinline__ float code_value(float v, float inv) {
+  if (INF && fabsf(v) > kFloatMax) return __int_as_float(0x7fc00000);
   return v * inv;
 }
 
+template <bool INF>
 __device__ __forceinline__ void st_codes(const Q8& q, uint64_t row0, uint32_t c, uint32_t rows,
                                          uint32_t cols, int width, int lane, const float* v,
-                                         float inv, bool inf, uint32_t* slab) {
+                                         float inv, uint32_t* slab) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    w[i] = e4m3x2(code_value(v[4 * i], inv, inf), code_value(v[4 * i + 1], inv, inf)) |
-           e4m3x2(code_value(v[4 * i + 2], inv, inf), code_value(v[4 * i + 3], inv, inf)) << 16;
+    w[i] = e4m3x2(code_value<INF>(v[4 * i], inv), code_value<INF>(v[4 * i + 1], inv)) |
+           e4m3x2(code_value<INF>(v[4 * i + 2], inv), code_value<INF>(v[4 * i + 3], inv)) << 16;
   st_square(q.codes, q.ld, row0, c, rows, cols, width, lane, w, slab);
 }
 
@@ -195,44 +197,54 @@ struct Maxima {
   uint64_t bar[4];        // one for each 32 rows, an arrival of each warp
 };
 
-// Largest finite magnitudes of a row's 128 columns of g and of u.  fmaxf
-// passes NaN over; only where some row of the warp holds an infinity
-// (returned) are the columns looked at again.  Columns past the matrix hold
-// zeros, which no magnitude is below.
+// Largest magnitudes of a row's 128 columns of g and of u, NaN passed over; with
+// FINITE, infinities too.  Columns past the matrix hold zeros, which no
+// magnitude is below.
+template <bool FINITE>
+__device__ __forceinline__ void row_maxima(uint32_t acc, bool any, Maxima* m, uint32_t* turn,
+                                           volatile uint32_t* gave_up, int quarter, int half,
+                                           int lane, float* mg, float* mu) {
+  const int row = quarter * 32 + lane;
+  const uint32_t bar = tc::smem_addr(&m->bar[quarter]);
+  *mg = *mu = 0.0f;
+#pragma unroll 1
+  for (int c = half * 64; c < half * 64 + 64; c += 32) {
+    float g[32], u[32];
+    ld_acc2(acc + c, acc + kN / 2 + c, any, g, u);
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // short chains
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float a = fabsf(g[i + j]), b = fabsf(u[i + j]);
+        x[j] = fmaxf(x[j], FINITE && a > kFloatMax ? 0.0f : a);
+        x[2 + j] = fmaxf(x[2 + j], FINITE && b > kFloatMax ? 0.0f : b);
+      }
+    }
+    *mg = fmaxf(*mg, fmaxf(x[0], x[1])), *mu = fmaxf(*mu, fmaxf(x[2], x[3]));
+  }
+  const uint32_t at = *turn & 1;
+  m->seen[at][half][row] = make_float2(*mg, *mu);
+  __syncwarp();
+  if (lane == 0) {
+    tc::bar_arrive(bar);
+    tc::bar_wait(bar, at, gave_up);  // if it gives up, the next tile's wait ends the warp
+  }
+  __syncwarp();
+  ++*turn;
+  const float2 other = m->seen[at][half ^ 1][row];
+  *mg = fmaxf(*mg, other.x), *mu = fmaxf(*mu, other.y);
+}
+
+// The same among finite values; only where some row of the warp holds an
+// infinity (returned) are the columns looked at again.  Both warps of a row
+// hold the same maxima, and so decide alike.
 __device__ __forceinline__ bool row_magnitudes(uint32_t acc, bool any, Maxima* m, uint32_t* turn,
                                                volatile uint32_t* gave_up, int quarter, int half,
                                                int lane, float* mg, float* mu) {
-  const int row = quarter * 32 + lane;
-  const uint32_t bar = tc::smem_addr(&m->bar[quarter]);
-  bool inf = false;
-  for (int look = 0; look < 2; ++look) {
-    *mg = *mu = 0.0f;
-#pragma unroll 1
-    for (int c = half * 64; c < half * 64 + 64; c += 32) {
-      float g[32], u[32];
-      ld_acc2(acc + c, acc + kN / 2 + c, any, g, u);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float x = fabsf(g[i]), y = fabsf(u[i]);
-        *mg = fmaxf(*mg, inf && x > kFloatMax ? 0.0f : x);
-        *mu = fmaxf(*mu, inf && y > kFloatMax ? 0.0f : y);
-      }
-    }
-    const uint32_t at = *turn & 1;
-    m->seen[at][half][row] = make_float2(*mg, *mu);
-    __syncwarp();
-    if (lane == 0) {
-      tc::bar_arrive(bar);
-      tc::bar_wait(bar, at, gave_up);  // if it gives up, the next tile's wait ends the warp
-    }
-    __syncwarp();
-    ++*turn;
-    const float2 other = m->seen[at][half ^ 1][row];
-    *mg = fmaxf(*mg, other.x), *mu = fmaxf(*mu, other.y);
-    // both warps hold the same maxima, and so decide alike
-    if (inf || !__any_sync(~0u, *mg > kFloatMax || *mu > kFloatMax)) break;
-    inf = true;
-  }
+  row_maxima<false>(acc, any, m, turn, gave_up, quarter, half, lane, mg, mu);
+  const bool inf = __any_sync(~0u, *mg > kFloatMax || *mu > kFloatMax);
+  if (inf) row_maxima<true>(acc, any, m, turn, gave_up, quarter, half, lane, mg, mu);
   return inf;
 }
 
@@ -267,10 +279,17 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32
       float g[32], u[32];
       __syncwarp();  // the last square's stores leave rows past the matrix out
       ld_acc2(acc + c, acc + kN / 2 + c, any, g, u);
-      if (a.g8.codes)
-        st_codes(a.g8, row0, c0 + c, a.rows, a.cols, a.width8, lane, g, inv_g, inf, slab);
-      if (a.u8.codes)
-        st_codes(a.u8, row0, c0 + c, a.rows, a.cols, a.width8, lane, u, inv_u, inf, slab);
+      const auto codes = [&](auto infinite) {
+        constexpr bool kInf = decltype(infinite)::value;
+        if (a.g8.codes)
+          st_codes<kInf>(a.g8, row0, c0 + c, a.rows, a.cols, a.width8, lane, g, inv_g, slab);
+        if (a.u8.codes)
+          st_codes<kInf>(a.u8, row0, c0 + c, a.rows, a.cols, a.width8, lane, u, inv_u, slab);
+      };
+      if (inf)
+        codes(std::true_type());
+      else
+        codes(std::false_type());
 #pragma unroll
       for (int i = 0; i < 32; ++i) g[i] = act_gate<EPI>(g[i]) * u[i];
       st_values<CR_BF16>(a.out[0], row0, c0 + c, a.rows, a.cols, a.width, lane, g, slab);
@@ -787,16 +806,16 @@ cudaError_t capacity(Capacity* out) {
   return cudaSuccess;
 }
 
-// Blocks to share a tile, at most.  Clusters of 8 wait long for 8 free SMs in
-// one part of the chip: 6 tiles of dx and 64 of dW (257 x 512 x 2048) took 31.1
-// us in clusters of 8, 19.6 in clusters of 4, 19.3 of 2 and 26.6 unsplit.
-constexpr int kMaxSplitLog = kClusterLogs - 1;
-
 // Blocks to share a tile: as many as find an SM each, all units at once, and
-// have at least `least` K blocks.
+// have at least `least` K blocks; 4 at most.  Clusters of 8 wait long for 8
+// free SMs in one part of the chip: 6 tiles of dx and 64 of dW (257 x 512 x
+// 2048) took 31.1 us in clusters of 8, 19.6 of 4, 19.3 of 2 and 26.6 unsplit; 8
+// tiles of dx alone (64 x 2048 x 8192 backward) 66 us in all in clusters of 8,
+// 61 of 4.
 uint32_t splits_of(uint32_t units, uint32_t blocks, const Capacity& c, uint32_t least) {
   int log = 0;
-  while (log < kMaxSplitLog && (uint64_t)units << (log + 1) <= c.blocks[log + 1] && blocks >= (least << (log + 1)))
+  while (log + 1 < kClusterLogs && (uint64_t)units << (log + 1) <= c.blocks[log + 1] &&
+         blocks >= (least << (log + 1)))
     ++log;
   return 1u << log;
 }
@@ -861,7 +880,7 @@ cudaError_t run_split_back(BackArgs& b, uint32_t outputs, bool* done, cudaStream
     bool grown = false;
     for (int look = 0; look < 2 && !grown; ++look, k ^= 1) {
       TileArgs& a = *both[k];
-      if (a.splits == 1u << kMaxSplitLog || a.blocks < a.splits * 2 * kMinBlocks) continue;
+      if (a.splits == 1u << (kClusterLogs - 1) || a.blocks < a.splits * 2 * kMinBlocks) continue;
       a.splits *= 2;
       const uint32_t c = std::max(cluster, a.splits);
       if (blocks(0, c) + blocks(1, c) <= cap.blocks[log2(c)]) {

@@ -25,9 +25,8 @@ namespace cr {
 
 namespace {
 
-constexpr int kBackThreads = 512;       // threads of the backward pass's blocks, at most
 constexpr int kWideThreads = 1024;      // threads of a block on a wide row
-constexpr uint32_t kWideFrom = 8192;    // columns above which a row of the forward pass is wide
+constexpr uint32_t kWideFrom = 8192;    // columns above which a row is wide
 constexpr uint32_t kBackParts = 912;    // partial rows of dweight, at most
 constexpr uint32_t kWideParts = 64;
 constexpr int kMaxWarps = kWideThreads / 32;
@@ -209,13 +208,13 @@ __device__ __forceinline__ void back_st(const NormBackArgs& a, uint64_t row, uin
   st_chunk<DT, VEC>(row_of_out<DT>(a.dx, row), base, a.cols, lane, dx);
 }
 
-// Rows a block of 16 warps can hold: block (32 * warps per row, rows per
+// Rows of at most kWideFrom columns: block (32 * warps per row, rows per
 // block), persistent; partial row blockIdx.x of dweight, whose sums stay in
 // registers.  With vectors, everything the next
 // row needs is loaded while this one is reduced and written; the scalar
 // kernel, whose loads take twice the registers, relies on more warps instead.
 template <int DT, int VEC, bool HELD8>
-__global__ void __launch_bounds__(kBackThreads)
+__global__ void __launch_bounds__(row_threads(VEC))
     k_rms_norm_back(const __grid_constant__ NormBackArgs a) {
   pdl_enter();
   __shared__ float part[2][kMaxWarps];
@@ -418,9 +417,6 @@ uint32_t wide_parts(uint64_t rows) {
   return (uint32_t)std::min<uint64_t>(std::max<uint64_t>(rows, 1), kWideParts);
 }
 
-// Columns above which a row of the backward pass is wide.
-uint32_t back_wide_from(int vec) { return kBackThreads / 32 * chunk_cols(vec); }
-
 template <typename... KArgs, typename... Args>
 cudaError_t launch2_smem(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                          cudaStream_t s, Args... args) {
@@ -508,7 +504,7 @@ cudaError_t back_run(NormBackArgs& a, const RowShape& r, cudaStream_t s) {
 
 template <int DT, int VEC>
 cudaError_t back_dispatch(NormBackArgs& a, cudaStream_t s) {
-  if (a.cols <= back_wide_from(VEC)) return back_run<DT, VEC>(a, row_shape(a.rows, a.cols, VEC), s);
+  if (a.cols <= kWideFrom) return back_run<DT, VEC>(a, row_shape(a.rows, a.cols, VEC), s);
   a.parts = wide_parts(a.rows);
   // dweight first: dx may be written over dy or h
   if (a.partial) {
@@ -540,7 +536,7 @@ cudaError_t launch_rms_norm(cr_dtype d, const NormArgs& a, int vec, cudaStream_t
 
 uint32_t norm_back_parts(uint64_t rows, uint32_t cols) {
   const uint32_t narrow = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(rows, 1), kBackParts);
-  return cols > back_wide_from(1) ? wide_parts(rows) : narrow;  // no less than wide_parts
+  return cols > kWideFrom ? wide_parts(rows) : narrow;
 }
 
 cudaError_t launch_rms_norm_back(cr_dtype d, cr_dtype dw, NormBackArgs a, int vec, cudaStream_t s) {
