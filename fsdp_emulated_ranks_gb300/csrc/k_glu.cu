@@ -27,6 +27,13 @@
 // Both let the next kernel's blocks onto their SMs only when their last products
 // are loaded: a waiting block beside them would have nothing to do before.
 //
+// Measured, 8192 tokens, 2048 x 8192, one call after another: forward 350 us
+// (1.57 PFLOP/s), dx 321 and dW 324 (1.7) alone, 355 each (1.55) in a loop under
+// the power cap; cuBLAS holds 1.70 there.  The tensor pipe is 66 % busy in
+// kGlu and 75 to 80 % in the others, which share operands better: kGlu moves 19
+// TB/s from L2.  A K block takes 0.27 to 0.34 us, of which the products are
+// 0.25.
+//
 // Every wait is bounded (tc.cuh); a block that gives up sets g_wait_word and
 // leaves.
 #include <algorithm>

