@@ -317,14 +317,55 @@ __device__ __forceinline__ void st_chunk(void* row, uint32_t base, uint32_t cols
   }
 }
 
+// 8-bit form of GROUPS groups from column `base` on: v[i] is column base + lane
+// + 32 i's value, and is changed.  Every lane of the warp calls it.  A group's
+// magnitude is one integer maximum over the lanes (bits of floats from 0 up
+// order as the floats do), and lane g makes group g's scale for all.
+template <int GROUPS, bool FULL>
+__device__ __forceinline__ void st_groups_q8(const Q8& q, uint64_t row, uint32_t base,
+                                             uint32_t cols, int lane, float* v) {
+  uint8_t* codes = q.codes + row * q.ld + base + lane;
+  float m[GROUPS];
+  bool inf = false;
+  for (int look = 0; look < 2; ++look) {
+    float most = 0.0f;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      m[g] = 0.0f;
+#pragma unroll
+      for (int i = 4 * g; i < 4 * g + 4; ++i) {
+        if (inf && fabsf(v[i]) > kFloatMax) v[i] = __int_as_float(0x7fc00000);
+        m[g] = fmaxf(m[g], fabsf(v[i]));
+      }
+      m[g] = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(m[g])));
+      most = fmaxf(most, m[g]);
+    }
+    inf = most > kFloatMax;  // the same in every lane
+    if (!inf) break;
+  }
+  float mine = m[0];
+#pragma unroll
+  for (int g = 1; g < GROUPS; ++g) mine = lane == g ? m[g] : mine;
+  const float s = q8_scale(mine), inv = 1.0f / s;
+  if (lane < GROUPS && (FULL || base + lane * CR_Q8_GROUP < cols))
+    q.scales[row * q.lds + base / CR_Q8_GROUP + lane] = s;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    const float by = __shfl_sync(~0u, inv, g);
+#pragma unroll
+    for (int i = 4 * g; i < 4 * g + 4; ++i)
+      if (FULL || base + lane + 32 * i < cols) codes[32 * i] = (uint8_t)e4m3x2(v[i] * by, 0.0f);
+  }
+}
+
 // 8-bit form of a chunk: every lane of the warp calls it.  v may be changed.
 template <int VEC>
 __device__ __forceinline__ void st_chunk_q8(const Q8& q, uint64_t row, uint32_t base,
                                             uint32_t cols, int lane, float* v) {
-  const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
-  uint8_t* codes = q.codes + row * q.ld + c0;
-  float* scales = q.scales + row * q.lds + base / CR_Q8_GROUP;
   if constexpr (VEC) {  // 8 lanes hold a group
+    const uint32_t c0 = chunk_col<VEC>(base, lane, 0);
+    uint8_t* codes = q.codes + row * q.ld + c0;
+    float* scales = q.scales + row * q.lds + base / CR_Q8_GROUP;
     const float m = q8_magnitude<16>(v, [](float x) {
 #pragma unroll
       for (int o = 4; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
@@ -345,35 +386,8 @@ __device__ __forceinline__ void st_chunk_q8(const Q8& q, uint64_t row, uint32_t 
       for (int i = 0; i < 16; ++i)
         if (c0 + i < cols) codes[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
     }
-  } else {  // values 0-3 of every lane are one group, 4-7 the next
-    float m[2];
-    bool inf = false;
-    for (int look = 0; look < 2; ++look) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        m[h] = 0.0f;
-#pragma unroll
-        for (int i = 4 * h; i < 4 * h + 4; ++i) {
-          if (inf && fabsf(v[i]) > kFloatMax) v[i] = __int_as_float(0x7fc00000);
-          m[h] = fmaxf(m[h], fabsf(v[i]));
-        }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        m[0] = fmaxf(m[0], __shfl_xor_sync(~0u, m[0], o));
-        m[1] = fmaxf(m[1], __shfl_xor_sync(~0u, m[1], o));
-      }
-      inf = fmaxf(m[0], m[1]) > kFloatMax;  // the same in every lane
-      if (!inf) break;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float s = q8_scale(m[h]), inv = 1.0f / s;
-      if (lane == 0 && base + h * CR_Q8_GROUP < cols) scales[h] = s;
-#pragma unroll
-      for (int i = 4 * h; i < 4 * h + 4; ++i)
-        if (c0 + 32 * i < cols) codes[32 * i] = (uint8_t)e4m3x2(v[i] * inv, 0.0f);
-    }
+  } else {
+    st_groups_q8<2, false>(q, row, base, cols, lane, v);
   }
 }
 

@@ -208,6 +208,34 @@ def test_rms_norm_special_rows():
     assert torch.isnan(y[1]).all() and torch.isfinite(y[0]).all()
 
 
+# rows off the vector grid: both sides of each width at which the kernels change, and more
+# rows than the blocks that run at once
+APART = [(3, 256), (2500, 257), (700, 511), (650, 512), (640, 513), (1300, 1025), (700, 4099),
+         (330, 8191), (320, 8192)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,cols", APART)
+def test_rms_norm_rows_that_start_apart(rows, cols, residual, dt):
+    """Every matrix at an alignment of its own, NaN beside the inputs."""
+    g = gen(rows + cols)
+    x = rand(g, rows, cols, dt, 3.0)
+    res = rand(g, rows, cols, dt) if residual else None
+    w = (1 + rand(g, 1, cols, "f32", 0.2)).to(R.TORCH[dt])
+    s, wide_s = empty(rows, cols, dt, 2, 3)
+    y, wide_y = empty(rows, cols, dt, 5, 1)
+    rstd = torch.empty(rows, device="cuda")
+    q, codes, scales, around = new_q8(rows, cols, 7, 2)
+    cr.cr_rms_norm(strided(x, 1, 4), strided(res, 3, 3) if residual else None, strided(w, 1, 1)[0],
+                   rows, cols, dt, EPS, s if residual else None, y, q, rstd)
+    check_norm(x, res, w[0], dt, EPS, {"y": y, "y8": (codes, scales), "rstd": rstd,
+                                       **({"sum": s} if residual else {})})
+    untouched(wide_s, 2, cols)
+    untouched(wide_y, 5, cols)
+    untouched(around, 7, cols)
+
+
 @pytest.mark.parametrize("dt,dw_dt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
 @pytest.mark.parametrize("held", ["full", "q8"])
 @pytest.mark.parametrize("rows,cols", NORM_SHAPES)
@@ -232,6 +260,40 @@ def test_rms_norm_backward(rows, cols, held, dt, dw_dt):
         rel_dw = (rows + 8) * R.U32
         assert torch.all((dw.double() - want_dw).abs()
                          <= R.U_OUT[dw_dt] * want_dw.abs() * (1 + rel_dw) + rel_dw * mag_dw)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("held", ["full", "q8"])
+@pytest.mark.parametrize("rows,cols", APART)
+def test_rms_norm_backward_rows_that_start_apart(rows, cols, held, dt):
+    g = gen(rows * 3 + cols)
+    h = rand(g, rows, cols, dt, 2.0)
+    dy, dres = rand(g, rows, cols, dt, 1e-2), rand(g, rows, cols, dt, 1e-2)
+    w = (1 + rand(g, 1, cols, "f32", 0.2)).to(R.TORCH[dt])
+    rstd = R.norm(h, None, w[0], EPS)[1].float()
+    q, hv = None, h
+    if held == "q8":
+        _, codes, scales, _ = new_q8(rows, cols)
+        cr.cr_q8_store(h, rows, cols, dt, cr.Q8(codes, scales))
+        hv = R.decode(codes, scales)
+        q = cr.Q8(strided(codes, 3, 6, 0), strided(scales, 1, 1))
+    need = cr.cr_rms_norm_backward_workspace_bytes(rows, cols)
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    dx, wide = empty(rows, cols, dt, 2, 5)
+    dw = torch.empty(cols, device="cuda")
+    for res in (strided(dres, 7, 2), None):
+        cr.cr_rms_norm_backward(strided(dy, 1, 2), strided(h, 5, 4) if held == "full" else None, q,
+                                strided(w, 1, 1)[0], rstd, res, rows, cols, dt, dx, dw, "f32", work,
+                                need)
+        want_dx, want_dw, mag, mag_dw = R.norm_backward(dy, hv, w[0], rstd,
+                                                        None if res is None else dres)
+        rel = (R.norm_depth(cols) + 8) * R.U32
+        assert torch.all((dx.double() - want_dx).abs()
+                         <= R.U_OUT[dt] * want_dx.abs() * (1 + rel) + rel * (mag + want_dx.abs()))
+        rel_dw = (rows + 8) * R.U32
+        assert torch.all((dw.double() - want_dw).abs()
+                         <= R.U32 * want_dw.abs() * (1 + rel_dw) + rel_dw * mag_dw)
+        untouched(wide, 2, cols)
 
 
 @pytest.mark.parametrize("cols", [77, 2048, 9001])
