@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(row_threads(VEC)) __maxnreg__(VEC ? 128 : 64) 
 //
 // Staged, the loads need neither registers nor a check a value, and a lane has
 // 16 values, over which the sums' shuffles and the codes' scales spread (40
-// instructions a value forward; 60 with 8 values from global memory, whose loads
+// instructions a value forward; 57 with 8 values from global memory, whose loads
 // ahead filled the registers).  Bound by instructions: 53 % of the issue slots,
 // at 24 to 36 warps an SM.  Measured against loads of single values:
 // bf16 2700 x 6001 with residual, sum, y and 8-bit y 49 us (80), backward 36
