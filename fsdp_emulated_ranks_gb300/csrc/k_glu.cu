@@ -15,7 +15,9 @@
 // TMA into a ring of kStages buffers, warp 1 issues the products into one of
 // two accumulators in tensor memory, warps 2-9 read the other one out and write
 // the results.  TMA fills rows and columns outside a matrix with zeros, so
-// ragged sizes need no masks before the epilogue.
+// ragged sizes need no masks before the epilogue.  Where K is long and the tiles
+// are many, two tiles one below the other share their B as one tall tile, which
+// loads 64 KB in place of 96 and fills tensor memory: its epilogue runs alone.
 //
 // k_split, where the tiles are too few for the SMs, and for the tiles that
 // would leave most SMs idle in the last turn of k_tiles: the blocks of a
@@ -27,12 +29,13 @@
 // Both let the next kernel's blocks onto their SMs only when their last products
 // are loaded: a waiting block beside them would have nothing to do before.
 //
-// Measured, 8192 tokens, 2048 x 8192, one call after another: forward 350 us
-// (1.57 PFLOP/s), dx 321 and dW 324 (1.7) alone, 355 each (1.55) in a loop under
-// the power cap; cuBLAS holds 1.70 there.  The tensor pipe is 66 % busy in
-// kGlu and 75 to 80 % in the others, which share operands better: kGlu moves 19
-// TB/s from L2.  A K block takes 0.27 to 0.34 us, of which the products are
-// 0.25.
+// Measured, 8192 tokens, 2048 x 8192, in a loop under the power cap: forward 348
+// us (1.58 PFLOP/s), with codes 430; the backward pass 765, of which the
+// products 658 (1.67; cuBLAS holds 1.70 there).  A tile's K block takes 0.27 to
+// 0.34 us, of which the products are 0.25: an SM takes 48 KB of it at 62 bytes a
+// cycle from L2.  Tall tiles take 32 KB a tile: the backward pass was 825 us
+// without them, forward over 4096 x 4096 342 against 357, 8192 x 2048 337
+// against 372.
 //
 // Every wait is bounded (tc.cuh); a block that gives up sets g_wait_word and
 // leaves.
@@ -63,6 +66,11 @@ constexpr uint32_t kStageBytes = kABytes + kBBytes;
 constexpr uint32_t kTileSmem = kStages * kStageBytes + 1024;  // + room to align to 1024
 constexpr int kTileThreads = 320;
 
+// A tall tile is two tiles, one below the other, that share their B.
+constexpr int stages_of(bool tall) { return tall ? 3 : kStages; }
+constexpr uint32_t stage_bytes(bool tall) { return (tall ? 2 : 1) * kABytes + kBBytes; }
+constexpr uint32_t kTallSmem = stages_of(true) * stage_bytes(true) + 1024;
+
 struct TileArgs {
   CUtensorMap a[4], b[2];     // kDw: a[2], a[3] are what a[0], a[1] were rounded by
   Mat out[2];
@@ -74,6 +82,8 @@ struct TileArgs {
   uint32_t tiles_m, tiles_n;  // of an output
   uint32_t tiles;             // k_tiles: tiles 0 .. tiles - 1 of all outputs
   uint32_t first;             // k_split: its first tile
+  uint32_t pairs;             // tall tiles of an output's column of tiles; 0: none are used
+  uint32_t skip;              // tall tiles of all outputs that come before tile 0
   uint32_t splits;            // k_split: blocks that share a tile, a power of two
   int width;                  // bytes of the output stores all rows allow: 32, 16 or 0
   int width8;                 // the same for the codes
@@ -169,17 +179,22 @@ __device__ __forceinline__ void st_codes(const Q8& q, uint64_t row0, uint32_t c,
 // time, so that their operands stay in L2; 16 in kGlu, whose short K changes
 // tiles often (8192 x 2048 x 8192 in turn on one card: 398 us at 8, 377 at 16,
 // 372 at 32; the backward pass 877, 880 and 895).
-template <int MODE>
+// Where some tiles are tall, the others are the halves of the tall tiles that
+// come after them.
+template <int MODE, bool TALL>
 __device__ __forceinline__ void tile_at(const TileArgs& a, uint32_t t, uint32_t* which,
                                         uint32_t* row, uint32_t* tn) {
-  constexpr uint32_t walk = MODE == kGlu ? 16 : 8;
-  const uint32_t per_out = a.tiles_m * a.tiles_n;
+  const bool pairs = TALL || a.pairs;
+  const uint32_t walk = (MODE == kGlu ? 16 : 8) / (pairs ? 2 : 1), lower = TALL || !pairs ? 0 : t & 1;
+  const uint32_t high = pairs ? a.pairs : a.tiles_m;
+  if (!TALL && pairs) t = a.skip + (t >> 1);
+  const uint32_t per_out = high * a.tiles_n;
   *which = t / per_out;
   t -= *which * per_out;
   const uint32_t group = t / (walk * a.tiles_n), first = group * walk;
-  const uint32_t height = min(walk, a.tiles_m - first);
+  const uint32_t height = min(walk, high - first);
   t -= group * walk * a.tiles_n;
-  *row = (first + t % height) * kM;
+  *row = ((first + t % height) * (pairs ? 2 : 1) + lower) * kM;
   *tn = t / height;
 }
 
@@ -330,24 +345,29 @@ __device__ __forceinline__ void multiply_block(uint32_t acc, uint32_t sa, uint32
 
 // One K block of the tile at `row` into buffer `sa`, arriving on `bar`: one
 // thread.
-template <int MODE>
+template <int MODE, bool TALL>
 __device__ __forceinline__ void load_block(const TileArgs& a, uint32_t which, uint32_t row,
                                            uint32_t tn, uint32_t k, uint32_t sa, uint32_t bar) {
-  const uint32_t seg = (k >= a.seg_blocks) + (k >= 2 * a.seg_blocks), sb = sa + kABytes;
+  constexpr int kHalves = TALL ? 2 : 1;
+  const uint32_t seg = (k >= a.seg_blocks) + (k >= 2 * a.seg_blocks), sb = sa + kHalves * kABytes;
   const int k0 = (int)((k - seg * a.seg_blocks) * kK), m0 = (int)row;
-  tc::bar_expect(bar, kStageBytes);
+  tc::bar_expect(bar, stage_bytes(TALL));
   if constexpr (MODE == kGlu) {
-    tc::tma_load(sa, &a.a[0], k0, m0, bar);
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+      tc::tma_load(sa + h * kABytes, &a.a[0], k0, m0 + h * kM, bar);
     tc::tma_load(sb, &a.b[0], k0, (int)(tn * (kN / 2)), bar);
     tc::tma_load(sb + kBBytes / 2, &a.b[1], k0, (int)(tn * (kN / 2)), bar);
   } else {
     if constexpr (MODE == kDx) {
-      tc::tma_load(sa, &a.a[seg], k0, m0, bar);
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        tc::tma_load(sa + h * kABytes, &a.a[seg], k0, m0 + h * kM, bar);
     } else {
       // (dg, x), then (rest of dg, x), then (dg, rest of x): those there are
       const CUtensorMap* left = &a.a[which + (a.a_lo && seg == 1 ? 2 : 0)];
-      tc::tma_load(sa, left, m0, k0, bar);
-      tc::tma_load(sa + 8192, left, m0 + 64, k0, bar);
+#pragma unroll
+      for (int j = 0; j < 2 * kHalves; ++j) tc::tma_load(sa + j * 8192, left, m0 + j * 64, k0, bar);
     }
     const CUtensorMap* right = &a.b[MODE == kDx ? seg : seg == a.a_lo + 1];
 #pragma unroll
@@ -358,22 +378,25 @@ __device__ __forceinline__ void load_block(const TileArgs& a, uint32_t which, ui
 
 // ---- many tiles: persistent blocks ------------------------------------------------------
 
-template <int MODE, int EPI>
+template <int MODE, int EPI, bool TALL>
 __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant__ TileArgs a) {
+  constexpr int kRing = stages_of(TALL);
+  constexpr uint32_t kBytes = stage_bytes(TALL);
+  constexpr int kHalves = TALL ? 2 : 1, kAccs = TALL ? 1 : 2;  // of an accumulator; accumulators
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+  __shared__ __align__(8) uint64_t bars[2 * kRing + 5];
   __shared__ Maxima maxima;
   __shared__ uint32_t tmem_base, slab[8 * kSlab];
   __shared__ uint32_t gave_up_word;
   volatile uint32_t* gave_up = &gave_up_word;
   const uint32_t smem = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
-  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
-  const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16;
+  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kRing;
+  const uint32_t acc_full = empty + 8 * kRing, acc_empty = acc_full + 16;
   const uint32_t drained = acc_empty + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kRing; ++s) {
       tc::bar_init(full + 8 * s, 1);
       tc::bar_init(empty + 8 * s, 1);
     }
@@ -398,32 +421,34 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant
     bool live = true;
     for (uint32_t t = blockIdx.x; t < a.tiles && live; t += gridDim.x) {
       uint32_t which, row, tn;
-      tile_at<MODE>(a, t, &which, &row, &tn);
+      tile_at<MODE, TALL>(a, t, &which, &row, &tn);
       for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
-        const uint32_t s = it % kStages;
-        if (!(live = tc::bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, gave_up))) break;
-        load_block<MODE>(a, which, row, tn, k, smem + s * kStageBytes, full + 8 * s);
+        const uint32_t s = it % kRing;
+        if (!(live = tc::bar_wait(empty + 8 * s, (it / kRing & 1) ^ 1, gave_up))) break;
+        load_block<MODE, TALL>(a, which, row, tn, k, smem + s * kBytes, full + 8 * s);
       }
     }
     pdl_launch_dependents();
     if (!live) {
-      // leave no copy in flight behind: the last kStages blocks issued
-      const uint32_t first = it > kStages ? it - kStages : 0;
-      for (uint32_t i = first; i < it; ++i) tc::bar_poll(full + 8 * (i % kStages), i / kStages & 1);
+      // leave no copy in flight behind: the last kRing blocks issued
+      const uint32_t first = it > kRing ? it - kRing : 0;
+      for (uint32_t i = first; i < it; ++i) tc::bar_poll(full + 8 * (i % kRing), i / kRing & 1);
     }
   } else if (warp == 1 && lane == 0) {
     uint32_t it = 0, n = 0;
     bool live = true;
     for (uint32_t t = blockIdx.x; t < a.tiles && live; t += gridDim.x, ++n) {
-      const uint32_t buf = n & 1, acc = tmem + buf * kN;
-      if (!(live = tc::bar_wait(acc_empty + 8 * buf, (n >> 1 & 1) ^ 1, gave_up))) break;
+      const uint32_t buf = n % kAccs, acc = tmem + buf * kN;
+      if (!(live = tc::bar_wait(acc_empty + 8 * buf, (n / kAccs & 1) ^ 1, gave_up))) break;
       tc::fence_after();
       for (uint32_t k = 0; k < a.blocks; ++k, ++it) {
-        const uint32_t s = it % kStages;
-        if (!(live = tc::bar_wait(full + 8 * s, it / kStages & 1, gave_up))) break;
+        const uint32_t s = it % kRing;
+        if (!(live = tc::bar_wait(full + 8 * s, it / kRing & 1, gave_up))) break;
         tc::fence_after();
-        const uint32_t sa = smem + s * kStageBytes;
-        multiply_block<MODE>(acc, sa, sa + kABytes, k == 0);
+        const uint32_t sa = smem + s * kBytes;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          multiply_block<MODE>(acc + h * kN, sa + h * kABytes, sa + kHalves * kABytes, k == 0);
         tc::mma_commit(empty + 8 * s);
       }
       if (live) tc::mma_commit(acc_full + 8 * buf);
@@ -436,16 +461,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     uint32_t n = 0, turn = 0;
     for (uint32_t t = blockIdx.x; t < a.tiles; t += gridDim.x, ++n) {
-      const uint32_t buf = n & 1;
+      const uint32_t buf = n % kAccs;
       uint32_t which, row, tn;
-      tile_at<MODE>(a, t, &which, &row, &tn);
+      tile_at<MODE, TALL>(a, t, &which, &row, &tn);
       // one lane polls, so that the warp stays whole for the tensor memory loads
       bool got = true;
-      if (lane == 0) got = tc::bar_wait(acc_full + 8 * buf, n >> 1 & 1, gave_up);
+      if (lane == 0) got = tc::bar_wait(acc_full + 8 * buf, n / kAccs & 1, gave_up);
       if (!__shfl_sync(~0u, got, 0)) break;
       tc::fence_after();
-      epilogue<MODE, EPI>(a, tmem + buf * kN, which, (uint64_t)row + quarter * 32, tn, quarter,
-                          half, lane, slab + (warp - 2) * kSlab, &maxima, &turn, gave_up);
+#pragma unroll 1
+      for (int h = 0; h < kHalves; ++h)
+        epilogue<MODE, EPI>(a, tmem + (buf + h) * kN, which, (uint64_t)row + h * kM + quarter * 32,
+                            tn, quarter, half, lane, slab + (warp - 2) * kSlab, &maxima, &turn,
+                            gave_up);
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
@@ -559,7 +587,7 @@ __device__ __forceinline__ void split_tile(const TileArgs& a, SplitShared* sh, u
   const bool mine = unit < units;
   uint32_t which = 0, row0 = 0, tn = 0, k0 = 0, k1 = 0;
   if (mine) {
-    tile_at<MODE>(a, a.first + unit, &which, &row0, &tn);
+    tile_at<MODE, false>(a, a.first + unit, &which, &row0, &tn);
     k0 = (uint32_t)((uint64_t)a.blocks * rank / a.splits);
     k1 = (uint32_t)((uint64_t)a.blocks * (rank + 1) / a.splits);
   }
@@ -570,7 +598,7 @@ __device__ __forceinline__ void split_tile(const TileArgs& a, SplitShared* sh, u
     for (uint32_t k = k0; k < k1; ++k, ++it) {
       const uint32_t s = it % kStages;
       if (!(live = tc::bar_wait(empty + 8 * s, (it / kStages & 1) ^ 1, gave_up))) break;
-      load_block<MODE>(a, which, row0, tn, k, smem + s * kStageBytes, full + 8 * s);
+      load_block<MODE, false>(a, which, row0, tn, k, smem + s * kStageBytes, full + 8 * s);
     }
     pdl_launch_dependents();
     if (!live) {
@@ -790,11 +818,15 @@ cudaError_t capacity(Capacity* out) {
     *out = it->second;
     return cudaSuccess;
   }
-  for (Kernel k : {k_tiles<kGlu, CR_ACT_SILU>, k_tiles<kGlu, CR_ACT_GELU>, k_tiles<kDx, CR_BF16>,
-                   k_tiles<kDw, CR_BF16>, k_tiles<kDw, CR_F32>, k_split<kGlu, CR_ACT_SILU>,
+  for (Kernel k : {k_tiles<kGlu, CR_ACT_SILU, false>, k_tiles<kGlu, CR_ACT_GELU, false>, k_tiles<kDx, CR_BF16, false>,
+                   k_tiles<kDw, CR_BF16, false>, k_tiles<kDw, CR_F32, false>, k_split<kGlu, CR_ACT_SILU>,
                    k_split<kGlu, CR_ACT_GELU>, k_split<kDx, CR_BF16>, k_split<kDw, CR_BF16>,
                    k_split<kDw, CR_F32>}) {
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+    if (e != cudaSuccess) return e;
+  }
+  for (Kernel k : {k_tiles<kGlu, CR_ACT_SILU, true>, k_tiles<kGlu, CR_ACT_GELU, true>, k_tiles<kDx, CR_BF16, true>, k_tiles<kDw, CR_BF16, true>, k_tiles<kDw, CR_F32, true>}) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTallSmem);
     if (e != cudaSuccess) return e;
   }
   for (auto k : {k_split_back<CR_BF16>, k_split_back<CR_F32>}) {
@@ -828,19 +860,40 @@ uint32_t splits_of(uint32_t units, uint32_t blocks, const Capacity& c, uint32_t 
 }
 
 constexpr uint32_t kMinBlocks = 4;    // K blocks worth a block of a cluster
+// K blocks from which tall tiles are the faster: dW of 2048 x 8192 over 2048
+// tokens (32) 216 us against 216 with the rest of its backward pass, over 1024
+// 130 against 125; kGlu over 8192 tokens and 8192 columns, no codes, 2048 (32)
+// 349 against 353, 1024 187 against 176.  With codes the epilogue, which a tall
+// tile does not overlap with products, is longer: 2048 443 against 430, 2560 504
+// against 503, 2816 558 against 553, 4096 x 4096 392 against 405.  Rows that do
+// not start on 128 bytes cost more L2 traffic, which tall tiles save: 2040 with
+// codes 497 against 587.
+constexpr uint32_t kTallBlocks = 32, kTallBlocksCodes = 48;
 constexpr uint32_t kTailBlocks = 32;  // K blocks for which splitting the last turn is worth a launch
 
 // Clusters for a tile each if several blocks find SMs for every tile; else
 // persistent blocks, the last turn's tiles split where they would leave most
 // SMs idle.
 template <int MODE, int EPI>
-cudaError_t run_tiles(TileArgs& a, uint32_t outputs, cudaStream_t s) {
+cudaError_t run_tiles(TileArgs& a, uint32_t outputs, cudaStream_t s, uint32_t least = kTallBlocks) {
   Capacity cap;
   cudaError_t e = capacity(&cap);
   if (e != cudaSuccess) return e;
-  const uint64_t n = (uint64_t)a.tiles_m * a.tiles_n * outputs;
+  uint64_t n = (uint64_t)a.tiles_m * a.tiles_n * outputs;
   if (n >= 1ull << 31) return cudaErrorInvalidValue;
-  const uint32_t sms = cap.blocks[0], rest = (uint32_t)(n % sms);
+  const uint32_t sms = cap.blocks[0];
+  if (n > sms && a.blocks >= least) {
+    // as many tall tiles as make whole turns, or fill more than half the SMs in
+    // the last: two tiles on an SM in turn take longer than the tall one
+    a.pairs = ceil_div(a.tiles_m, 2);
+    const uint32_t all = a.pairs * a.tiles_n * outputs, rest = all % sms;
+    a.tiles = a.skip = 2 * rest > sms ? all : all - rest;
+    const Launch l(std::min(a.tiles, sms), kTileThreads, kTallSmem, 1, s);
+    if ((e = cudaLaunchKernelEx(&l.cfg, k_tiles<MODE, EPI, true>, a)) != cudaSuccess) return e;
+    n = 2 * (all - a.skip);
+    if (!n) return cudaSuccess;
+  }
+  const uint32_t rest = (uint32_t)(n % sms);
   uint32_t units = 0;
   a.tiles = (uint32_t)n;
   if (n <= sms) {
@@ -854,7 +907,7 @@ cudaError_t run_tiles(TileArgs& a, uint32_t outputs, cudaStream_t s) {
   a.tiles -= units;
   if (a.tiles) {
     const Launch l(std::min(a.tiles, sms), kTileThreads, kTileSmem, 1, s);
-    if ((e = cudaLaunchKernelEx(&l.cfg, k_tiles<MODE, EPI>, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&l.cfg, k_tiles<MODE, EPI, false>, a)) != cudaSuccess) return e;
   }
   if (!units) return cudaSuccess;
   a.first = a.tiles;
@@ -933,8 +986,12 @@ cudaError_t launch_glu(cr_act act, const GluArgs& g, cudaStream_t s) {
   a.width8 = 32;
   for (const Q8* q : {&g.g8, &g.u8})
     if (q->codes) a.width8 = std::min(a.width8, store_width(q->codes, g.tokens > 1 ? q->ld : 0));
-  return act == CR_ACT_SILU ? run_tiles<kGlu, CR_ACT_SILU>(a, 1, s)
-                            : run_tiles<kGlu, CR_ACT_GELU>(a, 1, s);
+  bool apart = false;  // rows of 128 bytes start in the middle of one
+  for (const Mat* m : {&g.x, &g.wg, &g.wu})
+    apart = apart || (reinterpret_cast<uintptr_t>(m->p) | m->ld * 2) % 128;
+  const uint32_t least = (g.g8.codes || g.u8.codes) && !apart ? kTallBlocksCodes : kTallBlocks;
+  return act == CR_ACT_SILU ? run_tiles<kGlu, CR_ACT_SILU>(a, 1, s, least)
+                            : run_tiles<kGlu, CR_ACT_GELU>(a, 1, s, least);
 }
 
 cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& g, cudaStream_t s) {

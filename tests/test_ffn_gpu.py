@@ -483,6 +483,18 @@ def test_glu_backward_many_tiles(tokens, dim, ffn, held, dw_dt):
     check_glu_backward(tokens, dim, ffn, held, dw_dt, "gelu", 0, 0)
 
 
+# Tall tiles and, after them, halves of tall tiles; then operands whose rows are 128 bytes off.
+@pytest.mark.parametrize("tokens,dim,ffn,side", [(2000, 3100, 2600, 0), (1900, 2056, 2600, 8)])
+def test_glu_tall_tiles(tokens, dim, ffn, side):
+    check_glu(tokens, dim, ffn, "silu", side, side)
+
+
+@pytest.mark.parametrize("dw_dt", ["f32", "bf16"])
+def test_glu_backward_tall_tiles(dw_dt):
+    """dx: 168 tall tiles, 152 in a turn and 16 in halves on 152 SMs; dW: 252."""
+    check_glu_backward(2900, 3330, 2270, "full", dw_dt, "silu", 0, 0)
+
+
 def test_glu_integers_are_exact_with_many_tiles():
     test_glu_integers_are_exact(3000, 256, 1500)
 
