@@ -30,7 +30,7 @@
 // are loaded: a waiting block beside them would have nothing to do before.
 //
 // Measured, 8192 tokens, 2048 x 8192, in a loop under the power cap: forward 348
-// us (1.58 PFLOP/s), with codes 430; the backward pass 765, of which the
+// us (1.58 PFLOP/s), with codes, read back after it, 430; the backward pass 765, of which the
 // products 658 (1.67; cuBLAS holds 1.70 there).  A tile's K block takes 0.27 to
 // 0.34 us, of which the products are 0.25: an SM takes 48 KB of it at 62 bytes a
 // cycle from L2.  Tall tiles take 32 KB a tile: the backward pass was 825 us
@@ -863,8 +863,8 @@ constexpr uint32_t kMinBlocks = 4;    // K blocks worth a block of a cluster
 // K blocks from which tall tiles are the faster: dW of 2048 x 8192 over 2048
 // tokens (32) 216 us against 216 with the rest of its backward pass, over 1024
 // 130 against 125; kGlu over 8192 tokens and 8192 columns, no codes, 2048 (32)
-// 349 against 353, 1024 187 against 176.  With codes the epilogue, which a tall
-// tile does not overlap with products, is longer: 2048 443 against 430, 2560 504
+// 349 against 353, 1024 187 against 176.  With codes (read back after it) the
+// epilogue, which a tall tile does not overlap with products, is longer: 2048 443 against 430, 2560 504
 // against 503, 2816 558 against 553, 4096 x 4096 392 against 405.  Rows that do
 // not start on 128 bytes cost more L2 traffic, which tall tiles save: 2040 with
 // codes 497 against 587.

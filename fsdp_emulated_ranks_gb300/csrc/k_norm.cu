@@ -159,8 +159,9 @@ __global__ void __launch_bounds__(row_threads(VEC)) __maxnreg__(VEC ? 128 : 64) 
 // instructions a value forward; 57 with 8 values from global memory, whose loads
 // ahead filled the registers).  Bound by instructions: 53 % of the issue slots,
 // at 24 to 36 warps an SM.  Measured against loads of single values:
-// bf16 2700 x 6001 with residual, sum, y and 8-bit y 49 us (80), backward 36
-// (55); 4000 x 4097 50 (66), backward 33 (46); fp32 1777 x 4099 21.9 (24.5).  At
+// bf16 2700 x 6001 with residual, sum, y and 8-bit y, which is read back after
+// it, 49 us (80; 37 of the 49 in the norm), backward 36 (55); 4000 x 4097 50
+// (66), backward 33 (46); fp32 1777 x 4099 21.9 (24.5).  At
 // up to kSpanFrom columns, where a warp holds a row, single values are as fast:
 // 20000 x 129 17.0 us against 18.1, 77 columns 14.8 against 16.5.
 
