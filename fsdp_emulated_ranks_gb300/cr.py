@@ -227,13 +227,23 @@ def _mat(x, ld):
         return x, ld or 0
     if ld is None:
         st = x.stride()
-        if len(st) < 2:
-            ld = 0
-        else:
-            if st[1] != 1 and x.shape[1] > 1:
-                raise ValueError("the columns of a matrix must be contiguous")
-            ld = st[0]
+        if st and st[-1] != 1 and x.shape[-1] > 1:
+            raise ValueError("the columns of a matrix must be contiguous")
+        if len(st) > 2 and any(n != 1 for n in x.shape[1:-1]):
+            raise ValueError("a matrix has two dimensions")
+        ld = st[0] if len(st) > 1 else 0
     return x.data_ptr(), ld
+
+
+def _dense(x) -> int:
+    """Address of a buffer that the call reads or writes as packed."""
+    if x is None:
+        return 0
+    if isinstance(x, int):
+        return x
+    if not x.is_contiguous():
+        raise ValueError("a vector, dwg, dwu and a workspace must be contiguous")
+    return x.data_ptr()
 
 
 _PACK = {}  # length -> struct packer of that many native 64-bit pointers
@@ -703,6 +713,8 @@ def cr_comm_elems(coll: int, sched: int, nranks: int, count: int,
 #
 # Matrices are 2-D tensors, whose row strides are taken from the tensors, or
 # device pointers, whose row strides are given (ldx, ...); None where optional.
+# What has no row stride in the call (vectors, dwg, dwu, the workspace) is
+# packed: a tensor that is not contiguous is refused.
 
 def _act(a) -> int:
     return a if isinstance(a, int) else _ACTS[a]
@@ -744,8 +756,8 @@ def cr_rms_norm(x, residual, weight, rows, cols, dtype, eps, sum, y, y8: Q8 = No
     residual, ldr = _mat(residual, ldr)
     sum, ldsum = _mat(sum, ldsum)
     y, ldy = _mat(y, ldy)
-    _call(2, _NORM(x, ldx, residual, ldr, _ptr(weight), rows, cols, _dtype(dtype), eps, sum,
-              ldsum, y, ldy, _q8(y8), _ptr(rstd), _stream(stream)))
+    _call(2, _NORM(x, ldx, residual, ldr, _dense(weight), rows, cols, _dtype(dtype), eps, sum,
+              ldsum, y, ldy, _q8(y8), _dense(rstd), _stream(stream)))
 
 
 def cr_rms_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
@@ -759,8 +771,8 @@ def cr_rms_norm_backward(dy, h, h8: Q8, weight, rstd, dres, rows, cols, dtype, d
     h, ldh = _mat(h, ldh)
     dres, lddres = _mat(dres, lddres)
     dx, lddx = _mat(dx, lddx)
-    _call(3, _NORM_BACK(dy, lddy, h, ldh, _q8(h8), _ptr(weight), _ptr(rstd), dres, lddres, rows,
-              cols, _dtype(dtype), dx, lddx, _ptr(dweight), _dtype(dw_dtype), _ptr(workspace),
+    _call(3, _NORM_BACK(dy, lddy, h, ldh, _q8(h8), _dense(weight), _dense(rstd), dres, lddres, rows,
+              cols, _dtype(dtype), dx, lddx, _dense(dweight), _dtype(dw_dtype), _dense(workspace),
               workspace_bytes, _stream(stream)))
 
 
@@ -776,7 +788,7 @@ def cr_glu(x, wg, wu, tokens, dim, ffn, dtype, act, a, g8: Q8 = None, u8: Q8 = N
     wu, ldwu = _mat(wu, ldwu)
     a, lda = _mat(a, lda)
     _call(4, _GLU(x, ldx, wg, ldwg, wu, ldwu, tokens, dim, ffn, _dtype(dtype), _act(act), a,
-              lda, _q8(g8), _q8(u8), _ptr(workspace), workspace_bytes, _stream(stream)))
+              lda, _q8(g8), _q8(u8), _dense(workspace), workspace_bytes, _stream(stream)))
 
 
 def cr_glu_act_backward(da, g8: Q8, u8: Q8, tokens, ffn, dtype, act, dg, du, a=None, stream=None,
@@ -803,8 +815,8 @@ def cr_glu_backward(da, g8: Q8, u8: Q8, x, x8: Q8, wg, wu, tokens, dim, ffn, dty
     dx, lddx = _mat(dx, lddx)
     a, lda = _mat(a, lda)
     _call(6, _GLU_BACK(da, ldda, _q8(g8), _q8(u8), x, ldx, _q8(x8), wg, ldwg, wu, ldwu, tokens,
-              dim, ffn, _dtype(dtype), _act(act), dx, lddx, _ptr(dwg), _ptr(dwu), _dtype(dw_dtype), a,
-              lda, _ptr(workspace), workspace_bytes, _stream(stream)))
+              dim, ffn, _dtype(dtype), _act(act), dx, lddx, _dense(dwg), _dense(dwu), _dtype(dw_dtype), a,
+              lda, _dense(workspace), workspace_bytes, _stream(stream)))
 
 
 def cr_glu_wait_word(clear: bool = False) -> int:
