@@ -471,7 +471,7 @@ template <int ACT>
 __device__ __forceinline__ float2 act_gate_slope(float g) {
   float z = g, dz = 1.0f;
   if constexpr (ACT == CR_ACT_GELU) {
-    const float sq = g * g;
+    const float sq = fminf(g * g, 1e4f);  // finite: past |g| = 100 p is 0 or 1, and 0 * dz has to be 0
     z = g * fmaf(0.0713548163f, sq, 1.5957691216f);
     dz = fmaf(0.2140644488f, sq, 1.5957691216f);
   }
