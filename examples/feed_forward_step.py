@@ -116,6 +116,8 @@ def train(ranks: int = 4, tokens: int = 512, dim: int = 256, ffn: int = 1024, st
                         cr.adamw_cfg(lr=lr, weight_decay=0.0, step=step),
                         [k.params for k in members])
         losses.append(float(total) / ranks)
+        if cr.cr_glu_wait_word():
+            raise RuntimeError(f"step {step}: a wait of the gated block ran out, its gradients are undefined")
     return losses, members
 
 

@@ -38,7 +38,7 @@
 // against 372.
 //
 // Every wait is bounded (tc.cuh); a block that gives up sets g_wait_word and
-// leaves.
+// leaves.  A wait for a tile's sums may last longer the longer K is.
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -329,6 +329,16 @@ __device__ __forceinline__ void epilogue(const TileArgs& a, uint32_t acc, uint32
   __syncwarp();
 }
 
+// Turns (tc.cuh) that the wait for the sums over so many K blocks may take
+// beyond those of any wait: 16384 cycles a block, of which the products are 512
+// and the loads at most some 2000 where all SMs wait for memory.  If the products
+// stop, the warps that issue them and load for them give up first.  (Blocks
+// counted as they go would make it exact, but a store each in the loop that
+// issues the products made 8192 x 2048 x 8192 with codes 14 us longer.)
+constexpr uint32_t kTurnBlocks = tc::kTurnCycles / 16384;
+
+__device__ __forceinline__ int sum_turns(uint32_t blocks) { return (int)(blocks / kTurnBlocks); }
+
 // The products of one K block, A at sa and B at sb: one thread.
 template <int MODE>
 __device__ __forceinline__ void multiply_block(uint32_t acc, uint32_t sa, uint32_t sb, bool first) {
@@ -466,7 +476,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_tiles(const __grid_constant
       tile_at<MODE, TALL>(a, t, &which, &row, &tn);
       // one lane polls, so that the warp stays whole for the tensor memory loads
       bool got = true;
-      if (lane == 0) got = tc::bar_wait(acc_full + 8 * buf, n / kAccs & 1, gave_up);
+      if (lane == 0) got = tc::bar_wait(acc_full + 8 * buf, n / kAccs & 1, gave_up, sum_turns(a.blocks));
       if (!__shfl_sync(~0u, got, 0)) break;
       tc::fence_after();
 #pragma unroll 1
@@ -622,7 +632,7 @@ __device__ __forceinline__ void split_tile(const TileArgs& a, SplitShared* sh, u
   }
   __syncwarp();
   if (warp >= 2 && mine) {
-    if (lane == 0) tc::bar_wait(acc_full, 0, gave_up);
+    if (lane == 0) tc::bar_wait(acc_full, 0, gave_up, sum_turns(k1 - k0));
     __syncwarp();
     tc::fence_after();
     const int quarter = warp & 3, half = (warp - 2) >> 2;

@@ -39,21 +39,28 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return done;
 }
 
-// Clock cycles (about half a second) after which a wait gives up.
-constexpr long long kWaitCycles = 1ll << 30;
+// What a wait may last: kWaitTurns turns of kTurnCycles clock cycles, about half a
+// second.  Time that the block is held off its SM ends one turn at most,
+// however long it is, and so does going on on another SM, whose clock differs.
+constexpr int kWaitTurns = 16;
+constexpr unsigned long long kTurnCycles = 1ull << 26;
 
-// Waits for the phase of `parity` to complete.  False if it did not in
-// kWaitCycles, or if another role of the block gave up (*gave_up set): the
-// caller then leaves its loop.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity,
-                                         volatile uint32_t* gave_up) {
+// Waits for the phase of `parity` to complete.  False if that took too long, or
+// if another role of the block gave up (*gave_up set): the caller then leaves
+// its loop.  A wait for many steps may take `more` turns.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up,
+                                         int more = 0) {
   if (bar_try(bar, parity)) return true;
-  const long long start = clock64();
+  long long start = clock64();
+  int left = kWaitTurns + more;
   while (!bar_try(bar, parity)) {
     if (*gave_up) return false;
-    if (clock64() - start > kWaitCycles) {
-      *gave_up = 1;
-      return false;
+    if ((unsigned long long)(clock64() - start) > kTurnCycles) {
+      if (--left < 0) {
+        *gave_up = 1;
+        return false;
+      }
+      start = clock64();
     }
   }
   return true;
@@ -61,8 +68,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity,
 
 // Polls for the phase, as long as a wait may last, whoever gave up.
 __device__ __forceinline__ void bar_poll(uint32_t bar, uint32_t parity) {
-  const long long start = clock64();
-  while (!bar_try(bar, parity) && clock64() - start < kWaitCycles) {
+  long long start = clock64();
+  for (int left = kWaitTurns; !bar_try(bar, parity) && left >= 0;) {
+    if ((unsigned long long)(clock64() - start) > kTurnCycles) --left, start = clock64();
   }
 }
 

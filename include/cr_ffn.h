@@ -189,9 +189,11 @@ typedef enum {
 cr_status cr_ffn_call(cr_ffn_op op, const void* words);
 
 /* The block's products wait on barriers inside the kernel, each wait for about
- * half a second at most.  A wait that runs out (it never should) ends the
- * kernel, leaves its results undefined and sets this word, which stays set
- * until it is cleared.  Returns the word (0: no wait ever ran out), or -2 if
+ * half a second at most; the wait for a sum, 8 ms more for every 65536 of its K.
+ * A wait that runs out (it never should) ends the kernel, leaves its results
+ * undefined and sets this word, which stays set until it is cleared.  The call
+ * has returned CR_OK by then, so a training loop reads the word where it waits
+ * for the device anyway.  Returns the word (0: no wait ever ran out), or -2 if
  * reading it failed; waits for the device. */
 long long cr_glu_wait_word(int clear);
 
