@@ -1052,9 +1052,12 @@ cudaError_t launch_glu_back(cr_dtype dw, const GluBackArgs& g, cudaStream_t s) {
 }
 
 cudaError_t glu_wait_word(bool clear, unsigned int* word) {
-  cudaError_t e = cudaMemcpyFromSymbol(word, g_wait_word, sizeof(*word));
+  // the default stream, which the copies go by, does not wait for every stream
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(word, g_wait_word, sizeof(*word));
   const unsigned int zero = 0;
-  if (e == cudaSuccess && clear) e = cudaMemcpyToSymbol(g_wait_word, &zero, sizeof(zero));
+  // a word that was 0 is left alone: it may have been set since
+  if (e == cudaSuccess && clear && *word) e = cudaMemcpyToSymbol(g_wait_word, &zero, sizeof(zero));
   return e;
 }
 

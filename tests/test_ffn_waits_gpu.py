@@ -43,3 +43,24 @@ def test_example_stops_when_a_wait_ran_out(monkeypatch):
     monkeypatch.setattr(example.cr, "cr_glu_wait_word", lambda clear=False: 1)
     with pytest.raises(RuntimeError, match="wait"):
         example.train(2, 40, 64, 72, steps=2)
+
+
+def test_wait_word_waits_for_every_stream():
+    """The word is read after what is still queued on a stream of the caller's own (which
+    the default stream does not wait for): here some 0.2 s of work and an event behind it."""
+    stream, done = torch.cuda.Stream(), torch.cuda.Event()
+    assert cr.cr_glu_wait_word() == 0  # the library is loaded, its module too
+    torch.cuda._sleep(1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(400_000_000)
+        done.record()
+    assert cr.cr_glu_wait_word() == 0
+    assert done.query()
+
+
+def test_no_wait_ran_out_on_streams_or_in_graphs():
+    """Read behind concurrent, prepared and captured calls."""
+    T.test_streams()
+    T.test_prepared_and_captured()
+    assert cr.cr_glu_wait_word() == 0
