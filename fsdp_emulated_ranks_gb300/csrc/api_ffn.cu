@@ -224,7 +224,8 @@ cr_status cr_rms_norm(const void* x, size_t ldx, const void* residual, size_t ld
                       cr_stream_t stream) {
   cr_status st = check_float(dtype, "dtype");
   if (st != CR_OK) return st;
-  if (!(eps >= 0.0) || !isfinite(eps)) return fail(CR_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", eps);
+  if (!(eps >= 0.0) || !isfinite((float)eps))
+    return fail(CR_ERR_INVALID_ARG, "eps=%g must be >= 0 and finite in fp32", eps);
   if ((st = check_size(rows, "rows")) != CR_OK || (st = check_size(cols, "cols")) != CR_OK) return st;
   const size_t es = esize_of(dtype);
   Args a;

@@ -84,9 +84,10 @@ cr_status cr_q8_load(const cr_q8* q, size_t rows, size_t cols, void* x,
  *   y            v rounded to dtype (optional)
  *   y8           8-bit form of v, quantised from fp32 (optional)
  *   rstd         rows floats (optional; cr_rms_norm_backward reads it)
- * sum or y may be x or residual itself (same pointer and ld).  eps >= 0 and
- * finite (CR_ERR_INVALID_ARG).  A row of zeros with eps 0 gives NaN, as the
- * formula does. */
+ * sum or y may be x or residual itself (same pointer and ld).  eps is rounded
+ * to fp32: >= 0 and finite there (CR_ERR_INVALID_ARG).  A row of zeros with eps
+ * 0 gives NaN, as the formula does.  h^2 and its sum are fp32: a row whose sum
+ * of squares passes fp32's range (values from about 1e19) has rstd 0. */
 cr_status cr_rms_norm(const void* x, size_t ldx, const void* residual,
                       size_t ldr, const void* weight, size_t rows, size_t cols,
                       cr_dtype dtype, double eps, void* sum, size_t ldsum,
