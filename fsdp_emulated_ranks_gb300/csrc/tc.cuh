@@ -111,10 +111,6 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
 
 // ---- TMA ----------------------------------------------------------------------------
 
-__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
 // Loads the map's box at column x, row y to dst; bytes count on bar.
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
                                          uint32_t bar) {
