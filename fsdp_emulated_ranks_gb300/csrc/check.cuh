@@ -1,8 +1,9 @@
 // check.cuh -- device-side index checks of the checked build.
 //
 // The library is also built as a checked variant (CR_DEVICE_CHECKS, into
-// a separate directory) for tests: every kernel then verifies, before it
-// touches memory, the index arithmetic its accesses rest on -- the chunk a
+// a separate directory) for tests: every kernel of the collectives, buckets and
+// steps (not those of the feed-forward operators, cr_ffn.h) then verifies, before
+// it touches memory, the index arithmetic its accesses rest on -- the chunk a
 // vector falls in is a rank, its offset lies inside that rank's shard, a
 // tile belongs to its tensor, and so on.  A violated check sets one bit of
 // a device error word (one bit per kind of check) and skips the rest of the

@@ -29,13 +29,15 @@
 // Both let the next kernel's blocks onto their SMs only when their last products
 // are loaded: a waiting block beside them would have nothing to do before.
 //
-// Measured, 8192 tokens, 2048 x 8192, in a loop under the power cap: forward 348
-// us (1.58 PFLOP/s), with codes, read back after it, 430; the backward pass 765, of which the
-// products 658 (1.67; cuBLAS holds 1.70 there).  A tile's K block takes 0.27 to
-// 0.34 us, of which the products are 0.25: an SM takes 48 KB of it at 62 bytes a
-// cycle from L2.  Tall tiles take 32 KB a tile: the backward pass was 825 us
-// without them, forward over 4096 x 4096 342 against 357, 8192 x 2048 337
-// against 372.
+// Measured, 8192 tokens, 2048 x 8192, three seconds on end under the power cap:
+// forward 361 us (1.52 PFLOP/s), with codes 393; the backward pass 794, of which
+// the products 688 (1.60 PFLOP/s; cuBLAS's four products of these sizes 707 on
+// the same card), and 1105 from an 8-bit x, whose second part makes dW's
+// products twice as many.  In short bursts forward 329 and 371, backward 734.
+// A tile's K block takes 0.27 to 0.34 us, of which the products are 0.25: an SM
+// takes 48 KB of it at 62 bytes a cycle from L2.  Tall tiles take 32 KB a tile:
+// on one card the backward pass took 765 us with them and 825 without,
+// forward over 4096 x 4096 342 and 357, 8192 x 2048 337 and 372.
 //
 // Every wait is bounded (tc.cuh); a block that gives up sets g_wait_word and
 // leaves.  A wait for a tile's sums may last longer the longer K is.
@@ -177,8 +179,12 @@ __device__ __forceinline__ void st_codes(const Q8& q, uint64_t row0, uint32_t c,
 
 // Tile `t`: its output, first row and tile column.  Tile rows are walked 8 at a
 // time, so that their operands stay in L2; 16 in kGlu, whose short K changes
-// tiles often (8192 x 2048 x 8192 in turn on one card: 398 us at 8, 377 at 16,
-// 372 at 32; the backward pass 877, 880 and 895).
+// tiles often.  Forward at 8, 16 and 32 rows, on one card: 8192 x 2048 x 8192
+// with codes 375, 355 and 343 us, 4096 x 2048 x 8192 with codes 204, 197 and 194,
+// 8192 x 1024 x 16384 390, 371 and 359, 8192 x 1024 x 4096 99.6, 98.4 and 97.1,
+// 16384 x 512 x 4096 107.1, 107.3 and 107.5: 32 would be up to 3 % faster than
+// 16 where there are many tiles.  The backward pass of 8192 x 2048 x 8192,
+// before it had tall tiles: 877, 880 and 895.
 // Where some tiles are tall, the others are the halves of the tall tiles that
 // come after them.
 template <int MODE, bool TALL>

@@ -130,9 +130,9 @@ cudaError_t by_tokens(const GluArgs& a, uint32_t pitch, cudaStream_t s) {
   return a.tokens == 1 ? run<ACT, 1, VEC>(a, pitch, s) : run<ACT, 2, VEC>(a, pitch, s);
 }
 
-// 2048 x 8192, a call: 1 token 13.2 us and 2 tokens 17.1 here, 3 tokens 22.7
-// (a third row of sums leaves too few registers for loads); in tiles any
-// number up to 128 takes about 20.
+// 2048 x 8192, a call: 1 token 12.6 us and 2 tokens 15.3 here, 3 tokens 22.7
+// (a third row of sums leaves too few registers for loads); in tiles 3 tokens
+// 21.3, 4 20.8, 16 20.4, 64 18.7 and 128 19.2.
 constexpr uint32_t kFewTokens = 2;
 constexpr uint32_t kFewSmem = 48 << 10;  // what a block gets without asking
 

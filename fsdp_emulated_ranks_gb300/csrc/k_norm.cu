@@ -14,10 +14,14 @@
 // kernel adds the partials in order.  Wide rows take a second pass over dy
 // and h for dweight.
 //
-// Measured, bf16: the forward pass of 8192 x 2048 with residual, sum, y and
-// 8-bit y (151 MB) 22.5 us, 6.7 TB/s, bound by memory; the backward pass (134
-// MB) 24 us, 5.4 TB/s, bound by latency (117 registers, 16 warps an SM; at 80
-// registers it spills and takes 41), and 4 us for the partials.
+// Measured, bf16, a call in a loop: the forward pass of 8192 x 2048 with residual,
+// sum, y and 8-bit y (151 MB) 26.4 us, 5.7 TB/s (a copy that moves as many
+// bytes takes 29.6 in such a loop); the backward pass (134 MB) 28.3, of which 24
+// in the rows (5.6 TB/s, bound by latency: 117 registers, 16 warps an SM; at 80
+// registers it spills and takes 41) and 4 in the partials.  fp32, 4096 x 2048:
+// 23.4 us forward, 6.1 TB/s, and 28.4 backward.  Rows above kWideFrom columns are
+// read twice: 2048 x 16384 bf16 63.4 us forward, 4.8 TB/s of what has to be
+// moved, and 106 backward, 2.5 TB/s, where dweight takes a pass of its own.
 //
 // Rows off the vector grid (an odd width or address) come to shared memory as
 // the aligned 16-byte granules that hold them, a row ahead of the one at work,

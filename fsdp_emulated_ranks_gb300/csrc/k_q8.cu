@@ -6,9 +6,11 @@
 // reduction.  A warp that loads few bytes a chunk loads several chunks before
 // it works on the first.
 //
-// Measured at 8192 x 8192: load to bf16 (203 MB) 30.5 us, 6.7 TB/s; the gate's
-// backward pass (675 MB) 105.5 us, 6.4 TB/s, both bound by memory.  The latter
-// at 64 registers and four blocks an SM, with a few spills: 122 us at 96
+// Measured at 8192 x 8192, a call in a loop: store from bf16 (203 MB) 34.0 us, 6.0
+// TB/s, load 32.5, 6.2 TB/s; the gate's backward pass (675 MB) 105.9 us with
+// SiLU, 6.4 TB/s, and 113 with GELU, bound by memory.  5000 x 5001, off the vector
+// grid: store 27.1 (a column a lane, a byte a store), load 20.1, gate 57.9.
+// The gate's pass runs at 64 registers and four blocks an SM, with a few spills: 122 us at 96
 // registers and two.
 #include <algorithm>
 #include <type_traits>
