@@ -232,7 +232,16 @@ def _mat(x, ld):
         if len(st) > 2 and any(n != 1 for n in x.shape[1:-1]):
             raise ValueError("a matrix has two dimensions")
         ld = st[0] if len(st) > 1 else 0
+    if _recording:
+        _hold(x)
     return x.data_ptr(), ld
+
+
+def _hold(x) -> None:
+    """Keeps x as long as the prepared call that this thread is recording."""
+    rec = getattr(_tls, "recorder", None)
+    if rec is not None:
+        rec.held.append(x)
 
 
 def _dense(x) -> int:
@@ -243,6 +252,8 @@ def _dense(x) -> int:
         return x
     if not x.is_contiguous():
         raise ValueError("a vector, dwg, dwu and a workspace must be contiguous")
+    if _recording:
+        _hold(x)
     return x.data_ptr()
 
 
@@ -731,7 +742,16 @@ _STORE, _LOAD, _NORM, _NORM_BACK, _GLU, _GLU_ACT, _GLU_BACK = (
 
 
 def _q8(q) -> int:
-    return 0 if q is None else C.addressof(q)
+    """Address of q, or of a copy that a prepared call keeps: what it recorded is an address
+    of host memory, and q may be changed or gone when it is issued."""
+    if q is None:
+        return 0
+    if _recording and getattr(_tls, "recorder", None) is not None:
+        copy = Q8(q.codes or 0, q.scales or 0, q.ld, q.lds)
+        copy._keep = q._keep
+        _hold(copy)
+        q = copy
+    return C.addressof(q)
 
 
 def _call(op: int, words: bytes) -> None:
@@ -855,6 +875,7 @@ class _Recorder:
     def __init__(self, real):
         self._real = real
         self.calls = []
+        self.held = []  # what the recorded calls address, beyond the wrapper's arguments
 
     def __getattr__(self, name):
         fn = getattr(self._real, name)
@@ -876,9 +897,9 @@ class Prepared:
     __slots__ = ("name", "_calls", "_keep")
 
     def __init__(self, name, calls, keep):
-        # keep: the wrapper and its arguments, so that the tensors, the bucket
-        # plan and the 8-bit matrices whose addresses were recorded outlive the
-        # prepared call
+        # keep: the wrapper, its arguments and what was held while it ran, so that
+        # the tensors, the bucket plan and the 8-bit matrices whose addresses were
+        # recorded live as long as the prepared call
         self.name, self._calls, self._keep = name, calls, keep
 
     def __call__(self) -> None:
@@ -901,7 +922,9 @@ def prepare(wrapper, *args, **kwargs) -> Prepared:
     direct call.  A cr_adamw_cfg is passed by reference and read at each
     invocation, so advancing cfg.step between invocations takes effect.
     The prepared call holds references to the arguments, so the tensors and
-    the bucket plan it addresses stay allocated while it exists."""
+    the bucket plan it addresses stay allocated while it exists.  Of the
+    feed-forward calls it also holds every tensor, and a copy of every 8-bit
+    matrix (Q8), that a recorded function made or looked up by itself."""
     global _recording
     if getattr(_tls, "recorder", None) is not None:
         raise RuntimeError("prepare() cannot be nested")
@@ -918,4 +941,4 @@ def prepare(wrapper, *args, **kwargs) -> Prepared:
     name = getattr(wrapper, "__name__", "call")
     if not rec.calls:
         raise ValueError(f"{name} launches nothing that prepare() could record")
-    return Prepared(name, rec.calls, (wrapper, args, kwargs))
+    return Prepared(name, rec.calls, (wrapper, args, kwargs, rec.held))
