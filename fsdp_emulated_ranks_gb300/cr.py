@@ -1,5 +1,5 @@
-"""ctypes binding of libcr (include/cr.h and include/cr_ffn.h): argument
-marshalling only.
+"""ctypes binding of libcr (include/cr.h, include/cr_ffn.h and include/cr_lm.h):
+argument marshalling only.
 
 Every function here has the name of the C entry point it calls and does
 nothing but turn Python arguments (torch tensors or integer device
@@ -59,6 +59,11 @@ FFN_EXPORTS = ["cr_q8_store", "cr_q8_load", "cr_rms_norm",
                "cr_glu_backward_workspace_bytes", "cr_glu_backward", "cr_ffn_call",
                "cr_glu_wait_word"]
 
+# Every symbol include/cr_lm.h declares.
+LM_EXPORTS = ["cr_embedding", "cr_embedding_backward_workspace_bytes", "cr_embedding_backward",
+              "cr_dropout", "cr_log_probs", "cr_log_probs_backward", "cr_lm_call"]
+
+MAX_TOP = 32  # most likely tokens of cr_log_probs, at most
 ACT_SILU, ACT_GELU = 0, 1
 _ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
 Q8_GROUP = 128  # columns per scale of an 8-bit matrix
@@ -191,11 +196,13 @@ def lib() -> C.CDLL:
     L.cr_comm_elems.argtypes = [i, i, i, sz, i, C.POINTER(C.c_uint64),
                                 C.POINTER(C.c_uint64), C.POINTER(i)]
     L.cr_ffn_call.argtypes = [i, vp]
+    L.cr_lm_call.argtypes = [i, vp]
     L.cr_glu_wait_word.restype, L.cr_glu_wait_word.argtypes = C.c_longlong, [i]
-    for name, n in (("cr_rms_norm_backward", 2), ("cr_glu", 3), ("cr_glu_backward", 3)):
+    for name, n in (("cr_rms_norm_backward", 2), ("cr_glu", 3), ("cr_glu_backward", 3),
+                    ("cr_embedding_backward", 3)):
         fn = getattr(L, name + "_workspace_bytes")
         fn.restype, fn.argtypes = sz, [sz] * n
-    for name in EXPORTS + FFN_EXPORTS:
+    for name in EXPORTS + FFN_EXPORTS + LM_EXPORTS:
         getattr(L, name).restype = getattr(L, name).restype or i
     L.cr_status_string.restype = C.c_char_p
     L.cr_last_error.restype = C.c_char_p
@@ -845,6 +852,88 @@ def cr_glu_wait_word(clear: bool = False) -> int:
     return lib().cr_glu_wait_word(1 if clear else 0)
 
 
+# ---- language model operators (include/cr_lm.h) ---------------------------------------
+#
+# Matrices as above.  Token ids are packed tensors of int32 or int64, whose type says
+# how wide they are, or device pointers, of 64-bit ids unless id_bits says 32.
+
+_LM_NAMES = ["cr_embedding", "cr_embedding_backward", "cr_dropout", "cr_log_probs",
+             "cr_log_probs_backward"]
+_EMBED, _EMBED_BACK, _DROPOUT, _LOGP, _LOGP_BACK = (
+    struct.Struct("=" + words).pack for words in
+    ("4Qq2Qqd2QqQ", "2QqQq3Qd4Qq3Q", "6QqdQQQ3Q", "3Qq2Qqd3Qq3Q", "3Qq2Qqd8Q"))
+
+
+def _ids(x, bits) -> tuple[int, int]:
+    """Address and width of token ids."""
+    if x is None or type(x) is int:
+        return x or 0, 64 if bits is None else bits
+    if bits is None:
+        if x.is_floating_point() or x.element_size() not in (4, 8):
+            raise ValueError(f"token ids are int32 or int64, not {x.dtype}")
+        bits = 8 * x.element_size()
+    return _dense(x), bits
+
+
+def _lm_call(op: int, words: bytes) -> None:
+    status = lib().cr_lm_call(op, words)
+    if status:
+        _check(status, _LM_NAMES[op])
+
+
+def cr_embedding(table, vocab, ids, tokens, dim, dtype, scale, out, out_dtype="bf16", stream=None,
+                 ldt=None, ldo=None, id_bits=None) -> None:
+    table, ldt = _mat(table, ldt)
+    ids, bits = _ids(ids, id_bits)
+    out, ldo = _mat(out, ldo)
+    _lm_call(0, _EMBED(table, ldt, vocab, ids, bits, tokens, dim, _dtype(dtype), scale, out, ldo,
+                       _dtype(out_dtype), _stream(stream)))
+
+
+def cr_embedding_backward_workspace_bytes(tokens: int, vocab: int, dim: int) -> int:
+    return lib().cr_embedding_backward_workspace_bytes(tokens, vocab, dim)
+
+
+def cr_embedding_backward(dout, dtype, ids, tokens, vocab, dim, scale, base, dtable,
+                          dt_dtype="bf16", workspace=None, workspace_bytes=0, stream=None,
+                          lddo=None, ldb=None, ldt=None, id_bits=None) -> None:
+    dout, lddo = _mat(dout, lddo)
+    ids, bits = _ids(ids, id_bits)
+    base, ldb = _mat(base, ldb)
+    dtable, ldt = _mat(dtable, ldt)
+    _lm_call(1, _EMBED_BACK(dout, lddo, _dtype(dtype), ids, bits, tokens, vocab, dim, scale, base,
+                            ldb, dtable, ldt, _dtype(dt_dtype), _dense(workspace), workspace_bytes,
+                            _stream(stream)))
+
+
+def cr_dropout(x, residual, rows, cols, dtype, p, rng, call, first_row, out, stream=None, ldx=None,
+               ldr=None, ldo=None) -> None:
+    x, ldx = _mat(x, ldx)
+    residual, ldr = _mat(residual, ldr)
+    out, ldo = _mat(out, ldo)
+    _lm_call(2, _DROPOUT(x, ldx, residual, ldr, rows, cols, _dtype(dtype), p, _dense(rng), call,
+                         first_row, out, ldo, _stream(stream)))
+
+
+def cr_log_probs(logits, targets, rows, vocab, dtype, scale, logp, entropy=None, lse=None, top=0,
+                 top_ids=None, top_logp=None, stream=None, ldl=None, id_bits=None) -> None:
+    logits, ldl = _mat(logits, ldl)
+    targets, bits = _ids(targets, id_bits)
+    _lm_call(3, _LOGP(logits, ldl, targets, bits, rows, vocab, _dtype(dtype), scale, _dense(logp),
+                      _dense(entropy), _dense(lse), top, _dense(top_ids), _dense(top_logp),
+                      _stream(stream)))
+
+
+def cr_log_probs_backward(logits, targets, rows, vocab, dtype, scale, lse, entropy, dlogp, dentropy,
+                          dlse, dlogits, stream=None, ldl=None, lddl=None, id_bits=None) -> None:
+    logits, ldl = _mat(logits, ldl)
+    targets, bits = _ids(targets, id_bits)
+    dlogits, lddl = _mat(dlogits, lddl)
+    _lm_call(4, _LOGP_BACK(logits, ldl, targets, bits, rows, vocab, _dtype(dtype), scale,
+                           _dense(lse), _dense(entropy), _dense(dlogp), _dense(dentropy),
+                           _dense(dlse), dlogits, lddl, _stream(stream)))
+
+
 # ---- prepared calls -----------------------------------------------------------------
 
 # Entry points that launch work on a stream: the ones prepare() can record.
@@ -857,13 +946,14 @@ _PREPARABLE = frozenset([
     "cr_fsdp2_step_planned", "cr_all_reduce_range", "cr_reduce_scatter_range",
     "cr_fsdp_step_range", "cr_accumulate", "cr_all_reduce_accumulate", "cr_adamw_step",
     "cr_q8_store", "cr_q8_load", "cr_rms_norm", "cr_rms_norm_backward", "cr_glu",
-    "cr_glu_act_backward", "cr_glu_backward", "cr_ffn_call"])
+    "cr_glu_act_backward", "cr_glu_backward", "cr_ffn_call", "cr_embedding",
+    "cr_embedding_backward", "cr_dropout", "cr_log_probs", "cr_log_probs_backward", "cr_lm_call"])
 # Functions without side effects that a wrapper may call while it marshals.
 _PURE = frozenset(["cr_last_error", "cr_status_string", "cr_chunk_len", "cr_version",
                    "cr_fsdp_clip_workspace_bytes", "cr_shard_range", "cr_slab_range",
                    "cr_comm_elems", "cr_fsdp2_plan_table_bytes",
                    "cr_rms_norm_backward_workspace_bytes", "cr_glu_workspace_bytes",
-                   "cr_glu_backward_workspace_bytes"])
+                   "cr_glu_backward_workspace_bytes", "cr_embedding_backward_workspace_bytes"])
 
 
 class _Recorder:
@@ -885,7 +975,8 @@ class _Recorder:
             raise TypeError(f"prepare() records launching entry points only, not {name}")
 
         def record(*args):
-            called = _FFN_NAMES[args[0]] if name == "cr_ffn_call" else name
+            names = {"cr_ffn_call": _FFN_NAMES, "cr_lm_call": _LM_NAMES}.get(name)
+            called = names[args[0]] if names else name
             self.calls.append((called, fn, args))
             return 0
         return record

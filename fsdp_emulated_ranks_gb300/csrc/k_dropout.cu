@@ -1,0 +1,135 @@
+// k_dropout.cu -- dropout with the residual's addition, from a counter-based generator.
+//
+// One pass over memory.  Eight consecutive columns share one Philox4x32-10 (twenty
+// 32 x 32-bit products), so a lane works on whole groups of eight: 16 columns in vectors; 8
+// from shifted granules where bf16 rows are off the vector grid (span.cuh); and for fp32
+// there, column by column, with the random numbers handed over in shared memory.  The
+// mask exists in registers only.
+#include <type_traits>
+
+#include "lm_internal.cuh"
+#include "pdl.cuh"
+
+namespace cr {
+
+namespace {
+
+constexpr int kAhead = 2;  // chunks of a warp in flight
+
+struct Key {
+  uint32_t k0, k1, off0, off1;
+};
+
+__device__ __forceinline__ Key read_key(const DropoutArgs& a) {
+  const uint64_t seed = a.rng[0], off = a.rng[1] + a.call;
+  return {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
+}
+
+// Philox4x32-10 with the paper's multipliers and key increments.
+__device__ __forceinline__ uint4 philox(uint32_t group, uint32_t row, const Key& key) {
+  uint32_t c0 = group, c1 = row, c2 = key.off0, c3 = key.off1, k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t p = (uint64_t)c0 * 0xD2511F53u, q = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(q >> 32) ^ c1 ^ k0;
+    c2 = (uint32_t)(p >> 32) ^ c3 ^ k1;
+    c1 = (uint32_t)q;
+    c3 = (uint32_t)p;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+__device__ __forceinline__ uint32_t half_of(const uint4& w, int i) {
+  const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+  return i & 1 ? x >> 16 : x & 0xffffu;
+}
+
+template <int DT, int MODE>
+struct Pair {
+  Loaded<DT, MODE> x, residual;
+};
+
+// A lane's columns in modes 0 to 2 are ffn_internal.cuh's.  Mode kSpan: spans without a
+// lead, so that a lane's columns are one group; only the stores are shifted.
+template <int DT, int MODE, bool RES>
+__global__ void __launch_bounds__(kBlock) k_dropout(const __grid_constant__ DropoutArgs a,
+                                                    const __grid_constant__ ChunkRange r) {
+  constexpr int vals = place_vals(MODE);
+  __shared__ __align__(16) uint16_t turned[MODE == 0 ? kBlock / 32 : 1][MODE == 0 ? 256 : 8];
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const Key key = read_key(a);
+  const uint64_t stride = (uint64_t)gridDim.x * (kBlock / 32);
+  for (uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); k < r.chunks;
+       k += kAhead * stride) {
+    Loaded<DT, MODE> x[kAhead], res[RES ? kAhead : 1];
+    uint64_t row[kAhead];
+    uint32_t base[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const uint64_t c = k + j * stride;
+      if (c >= r.chunks) break;
+      row[j] = fastdiv_div(r.per_row, c);
+      base[j] = (uint32_t)(c - row[j] * r.per_row.d) * place_cols(MODE);
+      const Place<MODE> at(base[j], a.cols, lane, nullptr);
+      x[j].load(row_at<DT>(a.x, row[j]), at);
+      if constexpr (RES) res[j].load(row_at<DT>(a.residual, row[j]), at);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (k + j * stride >= r.chunks) break;
+      const Place<MODE> at(base[j], a.cols, lane, nullptr);
+      const uint32_t rc = a.first_row + (uint32_t)row[j];
+      float v[vals];
+      x[j].ready();
+      if constexpr (RES) res[j].ready();
+      const auto set = [&](int i, uint32_t number) {
+        const float kept = number >= a.limit ? __fmul_rn(x[j].value(i), a.by) : 0.0f;
+        if constexpr (RES)
+          v[i] = __fadd_rn(res[j].value(i), kept);
+        else
+          v[i] = kept;
+      };
+      if constexpr (MODE == 0) {
+        uint16_t* t = turned[threadIdx.x >> 5];
+        __syncwarp();
+        reinterpret_cast<uint4*>(t)[lane] = philox(base[j] / 8 + lane, rc, key);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < vals; ++i) set(i, t[32 * i + lane]);
+      } else {
+#pragma unroll
+        for (int g = 0; g < vals / 8; ++g) {
+          const uint4 w = philox(base[j] / 8 + lane * (vals / 8) + g, rc, key);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) set(8 * g + i, half_of(w, i));
+        }
+      }
+      char* out = row_at<DT>(a.out, row[j]);
+      if constexpr (MODE == kSpan)
+        st_spans(out, at.span, a.cols, lane, v);
+      else
+        st_chunk<DT, MODE>(out, base[j], a.cols, lane, v);
+    }
+  }
+}
+
+template <int DT, int MODE>
+cudaError_t run(const DropoutArgs& a, cudaStream_t s) {
+  const uint64_t per_row = ((uint64_t)a.cols + place_cols(MODE) - 1) / place_cols(MODE);
+  const ChunkRange r = {a.rows * per_row, fastdiv_make(per_row, a.rows * per_row)};
+  return launch_pdl(a.residual.p ? k_dropout<DT, MODE, true> : k_dropout<DT, MODE, false>,
+                    chunk_grid(r, kAhead), kBlock, s, a, r);
+}
+
+}  // namespace
+
+cudaError_t launch_dropout(cr_dtype d, const DropoutArgs& a, int vec, cudaStream_t s) {
+  if (d == CR_BF16)
+    return vec == 2 ? run<CR_BF16, 2>(a, s) : vec == 1 ? run<CR_BF16, 1>(a, s) : run<CR_BF16, kSpan>(a, s);
+  return vec == 2 ? run<CR_F32, 2>(a, s) : vec == 1 ? run<CR_F32, 1>(a, s) : run<CR_F32, 0>(a, s);
+}
+
+}  // namespace cr
