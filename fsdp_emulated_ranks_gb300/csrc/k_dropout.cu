@@ -14,7 +14,11 @@ namespace cr {
 
 namespace {
 
-constexpr int kAhead = 2;  // chunks of a warp in flight
+#ifndef CR_D_AHEAD
+#define CR_D_AHEAD 1
+#define CR_D_OCC 5
+#endif
+constexpr int kAhead = CR_D_AHEAD;  // chunks of a warp in flight
 
 struct Key {
   uint32_t k0, k1, off0, off1;
@@ -41,9 +45,11 @@ __device__ __forceinline__ uint4 philox(uint32_t group, uint32_t row, const Key&
   return make_uint4(c0, c1, c2, c3);
 }
 
+// Column i's number in the upper half of a word whose lower half means nothing: against
+// limit << 16 it compares as the number does against limit.
 __device__ __forceinline__ uint32_t half_of(const uint4& w, int i) {
   const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
-  return i & 1 ? x >> 16 : x & 0xffffu;
+  return i & 1 ? x : x << 16;
 }
 
 template <int DT, int MODE>
@@ -54,13 +60,15 @@ struct Pair {
 // A lane's columns in modes 0 to 2 are ffn_internal.cuh's.  Mode kSpan: spans without a
 // lead, so that a lane's columns are one group; only the stores are shifted.
 template <int DT, int MODE, bool RES>
-__global__ void __launch_bounds__(kBlock) k_dropout(const __grid_constant__ DropoutArgs a,
+__global__ void __launch_bounds__(kBlock, CR_D_OCC) k_dropout(const __grid_constant__ DropoutArgs a,
                                                     const __grid_constant__ ChunkRange r) {
   constexpr int vals = place_vals(MODE);
   __shared__ __align__(16) uint16_t turned[MODE == 0 ? kBlock / 32 : 1][MODE == 0 ? 256 : 8];
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const Key key = read_key(a);
+  const bool some = a.limit < 65536;
+  const uint32_t limit = a.limit << 16;
   const uint64_t stride = (uint64_t)gridDim.x * (kBlock / 32);
   for (uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); k < r.chunks;
        k += kAhead * stride) {
@@ -86,7 +94,7 @@ __global__ void __launch_bounds__(kBlock) k_dropout(const __grid_constant__ Drop
       x[j].ready();
       if constexpr (RES) res[j].ready();
       const auto set = [&](int i, uint32_t number) {
-        const float kept = number >= a.limit ? __fmul_rn(x[j].value(i), a.by) : 0.0f;
+        const float kept = some && number >= limit ? __fmul_rn(x[j].value(i), a.by) : 0.0f;
         if constexpr (RES)
           v[i] = __fadd_rn(res[j].value(i), kept);
         else
@@ -98,7 +106,7 @@ __global__ void __launch_bounds__(kBlock) k_dropout(const __grid_constant__ Drop
         reinterpret_cast<uint4*>(t)[lane] = philox(base[j] / 8 + lane, rc, key);
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < vals; ++i) set(i, t[32 * i + lane]);
+        for (int i = 0; i < vals; ++i) set(i, (uint32_t)t[32 * i + lane] << 16);
       } else {
 #pragma unroll
         for (int g = 0; g < vals / 8; ++g) {

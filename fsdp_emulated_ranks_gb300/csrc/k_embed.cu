@@ -13,43 +13,38 @@ namespace cr {
 
 namespace {
 
-constexpr int kAhead = 2;  // chunks of a warp in flight
+#ifndef CR_E_AHEAD
+#define CR_E_AHEAD 2
+#endif
+constexpr int kAhead = CR_E_AHEAD;  // chunks of a warp in flight
 
+// A warp takes kAhead chunks of a row, next to each other, which share the id.
 template <int DT, int OT, int MODE>
 __global__ void __launch_bounds__(kBlock) k_embed(const __grid_constant__ EmbedArgs a,
                                                   const __grid_constant__ ChunkRange r) {
+  constexpr uint32_t cols = place_cols(MODE);
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const uint64_t stride = (uint64_t)gridDim.x * (kBlock / 32);
   for (uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); k < r.chunks;
-       k += kAhead * stride) {
+       k += stride) {
+    const uint64_t row = fastdiv_div(r.per_row, k);
+    const uint32_t base = (uint32_t)(k - row * r.per_row.d) * kAhead * cols;
+    const int32_t id = token_id(a.ids, row, a.vocab);
+    char* out = row_at<OT>(a.out, row);
     Loaded<DT, MODE> in[kAhead];
-    uint64_t row[kAhead];
-    uint32_t base[kAhead];
-    int32_t id[kAhead];
+    if (id >= 0) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const uint64_t c = k + j * stride;
-      if (c >= r.chunks) break;
-      row[j] = fastdiv_div(r.per_row, c);
-      base[j] = (uint32_t)(c - row[j] * r.per_row.d) * place_cols(MODE);
-      id[j] = token_id(a.ids, row[j], a.vocab);
+      for (int j = 0; j < kAhead; ++j)
+        in[j].load(row_at<DT>(a.table, id), Place<MODE>(base + j * cols, a.dim, lane, out));
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (k + j * stride >= r.chunks) break;
-      const Place<MODE> at(base[j], a.dim, lane, row_at<OT>(a.out, row[j]));
-      if (id[j] >= 0) in[j].load(row_at<DT>(a.table, id[j]), at);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (k + j * stride >= r.chunks) break;
-      char* out = row_at<OT>(a.out, row[j]);
-      const Place<MODE> at(base[j], a.dim, lane, out);
+      const Place<MODE> at(base + j * cols, a.dim, lane, out);
       float v[place_vals(MODE)];
-      in[j].ready();
+      if (id >= 0) in[j].ready();
 #pragma unroll
-      for (int i = 0; i < place_vals(MODE); ++i) v[i] = id[j] >= 0 ? in[j].value(i) * a.scale : 0.0f;
+      for (int i = 0; i < place_vals(MODE); ++i) v[i] = id >= 0 ? in[j].value(i) * a.scale : 0.0f;
       st_place<OT, MODE>(out, at, v);
     }
   }
@@ -57,9 +52,9 @@ __global__ void __launch_bounds__(kBlock) k_embed(const __grid_constant__ EmbedA
 
 template <int DT, int OT, int MODE>
 cudaError_t run(const EmbedArgs& a, cudaStream_t s) {
-  const uint64_t per_row = place_chunks(a.dim, MODE);
+  const uint64_t per_row = (place_chunks(a.dim, MODE) + kAhead - 1) / kAhead;
   const ChunkRange r = {a.tokens * per_row, fastdiv_make(per_row, a.tokens * per_row)};
-  return launch_pdl(k_embed<DT, OT, MODE>, chunk_grid(r, kAhead), kBlock, s, a, r);
+  return launch_pdl(k_embed<DT, OT, MODE>, chunk_grid(r, 1), kBlock, s, a, r);
 }
 
 template <int DT, int OT>

@@ -3,15 +3,16 @@
 //
 // Tokens are sorted by id first, so that a row's sum has a fixed order and every row is
 // written once, by whoever adds it up:
-//   1. k_sort   a block sorts 1024 tokens by (bucket, id, token), where an id's bucket is its
-//               low bits, and notes where each bucket begins
-//   2. k_group  a block takes a bucket: its part of every sorted 1024, in order, gives the
-//               tokens of each of its ids (256 at most), in order
-//   3. k_sum    a warp takes a chunk of a table row and adds up its tokens' rows; where more
-//               than kLong tokens name it, a warp each kPart of them, and the last to finish
-//               adds the parts' fp32 sums, in order
-// Few tokens leave most of the table without any: then the call is bound by writing it,
-// else by reading the tokens' gradients and writing the table.
+//   1. k_group  A block takes a bucket, the ids that share their low bits.  It reads all ids
+//               twice: to count its ids' tokens (and all tokens of earlier buckets, which is where
+//               its own begin), and to put its tokens in order of id, then of token.
+//   2. k_sum    A warp takes a chunk of the columns of kTile tokens next to each other in that
+//               order, and adds up rows until the id changes: the work of a warp does not depend on
+//               how often an id occurs.  A table row that lies in one tile is written at once; of one in
+//               several, each warp leaves an fp32 sum in the workspace, and the last to finish adds
+//               them up in order.  Other warps write the rows that no token names.
+// Reading the ids once for each bucket costs little: they stay in L2, and are 8 bytes to a row of dout's
+// thousands.  Bound by memory: dout is read and the table written once.
 #include <algorithm>
 
 #include "lm_internal.cuh"
@@ -21,45 +22,41 @@ namespace cr {
 
 namespace {
 
-constexpr uint32_t kChunk = 1024;      // tokens a block sorts
-constexpr uint32_t kLocals = 256;      // ids of a bucket at most
-constexpr uint32_t kLong = 64;         // tokens of a row that one warp adds up at most
-constexpr uint32_t kPart = 64;         // tokens of a part of a longer row
-constexpr uint32_t kNone = 1u << 21;   // the sort key's id of what is no token
-
-struct Item {  // a part of a long row
-  uint32_t id, part, first, parts;  // first: the row's first item
-};
+constexpr int kThreads = 1024;        // of a block of k_group
+constexpr int kEach = 4;              // ids of a thread at a time
+constexpr uint32_t kStep = kThreads * kEach;
+constexpr uint32_t kLocals = 2048;    // ids of a bucket at most
+constexpr uint32_t kLeastBuckets = 128;
 
 // The workspace.
 struct Sorted {
-  uint32_t* keys;     // [chunks][kChunk] (bucket, id within it) << 10 | token, sorted
-  uint16_t* ranks;    // [chunks][kChunk] place among the chunk's tokens of that id; the last one's | kLast
-  uint16_t* begins;   // [chunks][buckets + 1] where buckets begin
-  uint32_t* tokens;   // [tokens] by bucket, id, token
-  uint2* rows;        // [vocab] first of the row's tokens, and how many
-  Item* items;        // [cap]
-  uint32_t* ticks;    // [cap][slices] parts of a long row that are done (at its first item)
-  float* sums;        // [cap][pitch]
-  uint32_t* count;    // items in use
-  uint32_t chunks, buckets, bucket_bits, local_bits, cap, slices;
+  uint2* order;      // [tokens] id and token, by bucket, id, token
+  uint2* rows;       // [vocab] first place of the row's tokens in that order, and how many
+  uint32_t* total;   // places in use
+  uint32_t* ticks;   // [tiles][slices] parts that are done of the row that begins in a tile and goes on
+  float* sums;       // [tiles][2][pitch] sums of parts: of a row that began in an earlier tile, and of one that
+                     // goes on in the next
+  uint32_t buckets, bucket_bits, tile_bits, tiles, slices;
   uint64_t pitch;
 };
 
-constexpr uint16_t kLast = 0x8000;
-
 uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
+
+// Tokens of a tile: few where there are few tokens, so that warps are enough; more where there are
+// many, so that the sums left in the workspace (and the time to add up those of one row) stay small.
+#ifndef CR_EB_TILE
+#define CR_EB_TILE 4
+#endif
+uint32_t tile_bits(uint64_t tokens) { return tokens <= 16384 ? CR_EB_TILE : 5; }  // a lane a token
 
 // Everything but the addresses, then the addresses from `p` on; returns the bytes.
 uint64_t layout(Sorted* w, void* p, uint64_t tokens, uint64_t vocab, uint64_t dim, uint32_t slices) {
-  w->bucket_bits = 5;
-  while (((uint64_t)kLocals << w->bucket_bits) < vocab) ++w->bucket_bits;
+  w->bucket_bits = 0;
+  while ((1u << w->bucket_bits) < kLeastBuckets || ((uint64_t)kLocals << w->bucket_bits) < vocab)
+    ++w->bucket_bits;
   w->buckets = 1u << w->bucket_bits;
-  w->local_bits = 0;
-  while (vocab && ((vocab - 1) >> w->bucket_bits) >> w->local_bits) ++w->local_bits;
-  w->chunks = (uint32_t)std::max<uint64_t>(1, (tokens + kChunk - 1) / kChunk);
-  // a row of n > kLong tokens has ceil(n / kPart) parts
-  w->cap = (uint32_t)(tokens / kPart + tokens / (kLong + 1));
+  w->tile_bits = tile_bits(tokens);
+  w->tiles = (uint32_t)((tokens + (1u << w->tile_bits) - 1) >> w->tile_bits);
   w->slices = slices;
   w->pitch = up(dim + 7, 512);  // spans may lead by 7 columns
   char* at = static_cast<char*>(p);
@@ -68,255 +65,254 @@ uint64_t layout(Sorted* w, void* p, uint64_t tokens, uint64_t vocab, uint64_t di
     at += up(bytes, 128);
     return q;
   };
-  w->sums = reinterpret_cast<float*>(take(w->cap * w->pitch * 4));
-  w->keys = reinterpret_cast<uint32_t*>(take((uint64_t)w->chunks * kChunk * 4));
-  w->ranks = reinterpret_cast<uint16_t*>(take((uint64_t)w->chunks * kChunk * 2));
-  w->begins = reinterpret_cast<uint16_t*>(take((uint64_t)w->chunks * (w->buckets + 1) * 2));
-  w->tokens = reinterpret_cast<uint32_t*>(take(tokens * 4));
+  w->sums = reinterpret_cast<float*>(take((uint64_t)w->tiles * 2 * w->pitch * 4));
+  w->order = reinterpret_cast<uint2*>(take(tokens * 8));
   w->rows = reinterpret_cast<uint2*>(take(vocab * 8));
-  w->items = reinterpret_cast<Item*>(take((uint64_t)w->cap * sizeof(Item)));
-  w->ticks = reinterpret_cast<uint32_t*>(take((uint64_t)w->cap * slices * 4));
-  w->count = reinterpret_cast<uint32_t*>(take(4));
+  w->ticks = reinterpret_cast<uint32_t*>(take((uint64_t)w->tiles * slices * 4));
+  w->total = reinterpret_cast<uint32_t*>(take(4));
   return (uint64_t)(at - static_cast<char*>(p));
 }
 
-// ---- 1: sort ------------------------------------------------------------------------------
+// ---- 1: group -------------------------------------------------------------------------------
 
-__global__ void __launch_bounds__(kChunk) k_sort(const __grid_constant__ Ids ids, uint64_t tokens,
-                                                 uint32_t vocab, const __grid_constant__ Sorted w) {
-  __shared__ uint32_t s[2][kChunk];
-  pdl_enter();
-  const uint32_t t = threadIdx.x;
-  const uint64_t token = (uint64_t)blockIdx.x * kChunk + t;
-  const int32_t id = token < tokens ? token_id(ids, token, vocab) : -1;
-  uint32_t key = id < 0 ? kNone : (id & (w.buckets - 1)) << w.local_bits | (uint32_t)id >> w.bucket_bits;
-  key = key << 10 | t;
-  // bitonic: within a warp by shuffles, beyond it through shared memory
-  int side = 0;
-#pragma unroll
-  for (uint32_t size = 2; size <= kChunk; size <<= 1) {
-#pragma unroll
-    for (uint32_t step = size / 2; step; step >>= 1) {
-      uint32_t other;
-      if (step >= 32) {
-        s[side][t] = key;
-        __syncthreads();
-        other = s[side][t ^ step];
-        side ^= 1;
-      } else {
-        other = __shfl_xor_sync(~0u, key, step);
-      }
-      const bool low = ((t & step) == 0) == ((t & size) == 0);
-      key = low ? min(key, other) : max(key, other);
-    }
-  }
-  __syncthreads();
-  s[0][t] = key;
-  __syncthreads();
-  const auto bucket_of = [&](uint32_t k) { return min(k >> 10 >> w.local_bits, w.buckets); };
-  uint16_t* begins = w.begins + (uint64_t)blockIdx.x * (w.buckets + 1);
-  const uint32_t mine = bucket_of(key), before = t ? bucket_of(s[0][t - 1]) + 1 : 0;
-  for (uint32_t b = before; b <= mine; ++b) begins[b] = (uint16_t)t;
-  if (t == kChunk - 1)
-    for (uint32_t b = mine + 1; b <= w.buckets; ++b) begins[b] = kChunk;
-  // the first of the keys with this id
-  const uint32_t least = key & ~1023u;
-  uint32_t lo = 0, hi = t;
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi) / 2;
-    if (s[0][mid] < least)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  const bool last = t == kChunk - 1 || s[0][t + 1] >> 10 != key >> 10;
-  w.keys[(uint64_t)blockIdx.x * kChunk + t] = key;
-  w.ranks[(uint64_t)blockIdx.x * kChunk + t] = (uint16_t)((t - lo) | (last ? kLast : 0));
-  if (blockIdx.x == 0 && t == 0) *w.count = 0;
-}
-
-// ---- 2: group ------------------------------------------------------------------------------
-
-__global__ void __launch_bounds__(kLocals) k_group(uint32_t vocab, const __grid_constant__ Sorted w) {
-  __shared__ uint32_t count[kLocals], next[kLocals], warp_sum[kLocals / 32 + 1];
-  __shared__ unsigned long long first_sum;
-  pdl_enter();
-  const uint32_t t = threadIdx.x, lane = t & 31, warp = t / 32, b = blockIdx.x;
-  const uint64_t pitch = w.buckets + 1;
-  const uint32_t local_mask = (1u << w.local_bits) - 1;
-  count[t] = 0;
-  if (t == 0) first_sum = 0;
-  __syncthreads();
-  // tokens of earlier buckets, and of each id of this one
-  uint64_t earlier = 0;
-  for (uint32_t c = t; c < w.chunks; c += kLocals) earlier += w.begins[c * pitch + b];
-  if (earlier) atomicAdd(&first_sum, (unsigned long long)earlier);
-  for (uint32_t c = warp; c < w.chunks; c += kLocals / 32) {
-    const uint32_t lo = w.begins[c * pitch + b], hi = w.begins[c * pitch + b + 1];
-    for (uint32_t i = lo + lane; i < hi; i += 32) {
-      const uint32_t rank = w.ranks[(uint64_t)c * kChunk + i];
-      if (rank & kLast)
-        atomicAdd(&count[w.keys[(uint64_t)c * kChunk + i] >> 10 & local_mask], (rank & ~kLast) + 1);
-    }
-  }
-  __syncthreads();
-  // where each id's tokens begin
-  const uint32_t n = count[t];
+// Exclusive sum over the block's threads, and the total; `s` holds a word a warp and one more.
+__device__ __forceinline__ uint32_t block_scan(uint32_t n, uint32_t* s, uint32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   uint32_t sum = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t v = __shfl_up_sync(~0u, sum, o);
     if (lane >= o) sum += v;
   }
-  if (lane == 31) warp_sum[warp] = sum;
+  if (lane == 31) s[warp] = sum;
   __syncthreads();
-  uint32_t start = sum - n;
-  for (uint32_t k = 0; k < warp; ++k) start += warp_sum[k];
-  const uint32_t first = (uint32_t)first_sum;
-  next[t] = first + start;
-  const uint64_t id = (uint64_t)t << w.bucket_bits | b;
-  if (id < vocab) {
-    w.rows[id] = make_uint2(first + start, n);
-    if (n > kLong) {
-      const uint32_t parts = (n + kPart - 1) / kPart, at = atomicAdd(w.count, parts);
-      for (uint32_t k = 0; k < parts; ++k) w.items[at + k] = Item{(uint32_t)id, k, at, parts};
-      for (uint32_t k = 0; k < w.slices; ++k) w.ticks[(uint64_t)at * w.slices + k] = 0;
+  if (warp == 0) {
+    uint32_t w = s[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(~0u, w, o);
+      if (lane >= o) w += v;
     }
+    s[lane] = w;
   }
   __syncthreads();
-  // Tokens to their places.  A warp goes through all of the bucket's tokens in order but
-  // places those of its share of the ids alone, so that warps need not wait for each other.
-  constexpr uint32_t warps = kLocals / 32;
-  for (uint32_t c = 0; c < w.chunks; ++c) {
-    const uint32_t lo = w.begins[c * pitch + b], hi = w.begins[c * pitch + b + 1];
-    for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
-      const uint32_t i = i0 + lane;
-      uint32_t key = 0, rank = 0;
-      bool mine = i < hi;
-      if (mine) {
-        key = w.keys[(uint64_t)c * kChunk + i];
-        rank = w.ranks[(uint64_t)c * kChunk + i];
-        mine = (key >> 10) % warps == warp;
+  *total = s[31];
+  const uint32_t before = warp ? s[warp - 1] : 0;
+  __syncthreads();
+  return before + sum - n;
+}
+
+__global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids ids, uint32_t tokens,
+                                                    uint32_t vocab,
+                                                    const __grid_constant__ Sorted w) {
+  __shared__ uint32_t next[kLocals];  // counts, then where an id's next token goes
+  __shared__ uint2 list[kStep];       // a step's tokens of this bucket, in order
+  __shared__ uint32_t scan[32];
+  __shared__ uint32_t earlier_all, valid_all;
+  pdl_enter();
+  const uint32_t t = threadIdx.x, lane = t & 31, warp = t / 32, b = blockIdx.x;
+  const uint32_t mask = w.buckets - 1;
+  for (uint32_t k = t; k < kLocals; k += kThreads) next[k] = 0;
+  if (t == 0) earlier_all = valid_all = 0;
+  __syncthreads();
+  // an id's tokens, and the tokens of earlier buckets
+  uint32_t earlier = 0, valid = 0;
+  for (uint64_t i0 = 0; i0 < tokens; i0 += kStep) {
+    int32_t id[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const uint64_t i = i0 + j * kThreads + t;
+      id[j] = i < tokens ? token_id(ids, i, vocab) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      if (id[j] < 0) continue;
+      ++valid;
+      earlier += (id[j] & mask) < b;
+      if ((id[j] & mask) == b) atomicAdd(&next[id[j] >> w.bucket_bits], 1u);
+    }
+  }
+  earlier = __reduce_add_sync(~0u, earlier);
+  valid = __reduce_add_sync(~0u, valid);
+  if (lane == 0) atomicAdd(&earlier_all, earlier), atomicAdd(&valid_all, valid);
+  __syncthreads();
+  // each id's first place: a thread takes two ids next to each other
+  const uint32_t first = earlier_all;
+  static_assert(kLocals == 2 * kThreads, "two ids a thread");
+  const uint32_t n0 = next[2 * t], n1 = next[2 * t + 1];
+  uint32_t all;
+  const uint32_t at = first + block_scan(n0 + n1, scan, &all);
+  next[2 * t] = at, next[2 * t + 1] = at + n0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint64_t id = (uint64_t)(2 * t + k) << w.bucket_bits | b;
+    const uint32_t n = k ? n1 : n0, start = k ? at + n0 : at;
+    if (id >= vocab) continue;
+    w.rows[id] = make_uint2(start, n);
+    const uint32_t tile = start >> w.tile_bits;
+    if (n && (start + n - 1) >> w.tile_bits != tile)
+      for (uint32_t q = 0; q < w.slices; ++q) w.ticks[(uint64_t)tile * w.slices + q] = 0;
+  }
+  if (b == 0 && t == 0) *w.total = valid_all;
+  if (all == 0) return;
+  __syncthreads();
+  // tokens to their places
+  for (uint64_t i0 = 0; i0 < tokens; i0 += kStep) {
+    // a thread's ids are next to each other here, so that its place in the list is one sum
+    int32_t id[kEach];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const uint64_t i = i0 + kEach * t + j;
+      id[j] = i < tokens ? token_id(ids, i, vocab) : -1;
+      if (id[j] >= 0 && (id[j] & mask) != b) id[j] = -1;
+      mine += id[j] >= 0;
+    }
+    uint32_t m;
+    uint32_t slot = block_scan(mine, scan, &m);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (id[j] >= 0) list[slot++] = make_uint2((uint32_t)id[j], (uint32_t)(i0 + kEach * t + j));
+    __syncthreads();
+    // a warp places its share of the ids, so that it alone moves their `next`
+    for (uint32_t s = 0; s < m; s += 32) {
+      const uint2 e = s + lane < m ? list[s + lane] : make_uint2(~0u, 0);
+      const uint32_t local = e.x >> w.bucket_bits;
+      const bool own = s + lane < m && local % 32 == warp;
+      if (!__any_sync(~0u, own)) continue;
+      const uint32_t same = __match_any_sync(~0u, own ? local : ~0u);
+      if (own) {
+        const uint32_t place = next[local] + __popc(same & ((1u << lane) - 1));
+        w.order[place] = e;
       }
-      const uint32_t local = key >> 10 & local_mask;
-      if (mine) w.tokens[next[local] + (rank & ~kLast)] = c * kChunk + (key & 1023);
       __syncwarp();
-      if (mine && (rank & kLast)) next[local] += (rank & ~kLast) + 1;
+      if (own && (same >> lane) == 1) next[local] += __popc(same);
       __syncwarp();
     }
+    __syncthreads();
   }
 }
 
-// ---- 3: sum ---------------------------------------------------------------------------------
+// ---- 2: sum ---------------------------------------------------------------------------------
 
-constexpr int kAhead = 4;  // rows of a warp in flight
-
-// acc += rows tokens[0 .. n - 1] of dout, in order.
-template <int DT, int MODE>
-__device__ __forceinline__ void add_rows(const Mat& dout, const uint32_t* tokens, uint32_t n,
-                                         const Place<MODE>& at, float* acc) {
-  for (uint32_t i0 = 0; i0 < n; i0 += 32) {
-    const uint32_t here = min(n - i0, 32u);
-    const uint32_t token = (uint32_t)at.lane < here ? tokens[i0 + at.lane] : 0;
-    for (uint32_t i = 0; i < here; i += kAhead) {
-      Loaded<DT, MODE> in[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const uint32_t row = __shfl_sync(~0u, token, (i + j) & 31);
-        if (i + j < here) in[j].load(row_at<DT>(dout, row), at);
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (i + j >= here) break;
-        in[j].ready();
-#pragma unroll
-        for (int e = 0; e < place_vals(MODE); ++e) acc[e] += in[j].value(e);
-      }
-    }
-  }
-}
+#ifndef CR_EB_BYTES
+#define CR_EB_BYTES 128
+#define CR_EB_OCC 4
+#endif
 
 // Table row `id`: base + scale * acc.
 template <int OT, int MODE>
-__device__ __forceinline__ void finish(const EmbedBackArgs& a, uint32_t id, const Place<MODE>& at,
+__device__ __forceinline__ void finish(const EmbedBackArgs& a, uint32_t id, uint32_t col, int lane,
                                        float* acc) {
+  constexpr int vals = place_vals(MODE);
+  char* out = row_at<OT>(a.dtable, id);
+  const Place<MODE> at(col, a.dim, lane, out);
 #pragma unroll
-  for (int e = 0; e < place_vals(MODE); ++e) acc[e] *= a.scale;
+  for (int e = 0; e < vals; ++e) acc[e] = __fmul_rn(acc[e], a.scale);
   if (a.base.p) {
     Loaded<OT, MODE> base;
     base.load(row_at<OT>(a.base, id), at);
     base.ready();
 #pragma unroll
-    for (int e = 0; e < place_vals(MODE); ++e) acc[e] += base.value(e);
+    for (int e = 0; e < vals; ++e) acc[e] += base.value(e);
   }
-  st_place<OT, MODE>(row_at<OT>(a.dtable, id), at, acc);
+  st_place<OT, MODE>(out, at, acc);
 }
 
-// Warps [0, cap * slices) take the parts of long rows, the others a chunk of a row each.
+// Warps [0, tiles * slices) take the tokens' tiles; the others the rows without tokens,
+// a chunk each.
 template <int DT, int OT, int MODE>
-__global__ void __launch_bounds__(kBlock) k_sum(const __grid_constant__ EmbedBackArgs a,
+__global__ void __launch_bounds__(kBlock, CR_EB_OCC) k_sum(const __grid_constant__ EmbedBackArgs a,
                                                 const __grid_constant__ Sorted w,
                                                 const __grid_constant__ FastDiv slices) {
   constexpr int vals = place_vals(MODE);
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5);
-  const uint64_t part_warps = (uint64_t)w.cap * w.slices;
+  const uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5);
+  const uint64_t n = fastdiv_div(slices, k);
+  const uint32_t slice = (uint32_t)(k - n * w.slices), col = slice * place_cols(MODE);
   float acc[vals];
 #pragma unroll
   for (int e = 0; e < vals; ++e) acc[e] = 0.0f;
-  if (k >= part_warps) {
-    k -= part_warps;
-    const uint64_t id = fastdiv_div(slices, k);
-    if (id >= a.vocab) return;
-    const uint2 row = w.rows[id];
-    if (row.y > kLong || (row.y == 0 && a.in_place)) return;
-    const uint32_t base = (uint32_t)(k - id * w.slices) * place_cols(MODE);
-    const Place<MODE> at(base, a.dim, lane, row_at<OT>(a.dtable, id));
-    add_rows<DT, MODE>(a.dout, w.tokens + row.x, row.y, at, acc);
-    finish<OT, MODE>(a, (uint32_t)id, at, acc);
+  if (n >= w.tiles) {
+    const uint64_t id = n - w.tiles;
+    if (id < a.vocab && w.rows[id].y == 0) finish<OT, MODE>(a, (uint32_t)id, col, lane, acc);
     return;
   }
-  const uint64_t n = fastdiv_div(slices, k);
-  if (n >= *w.count) return;
-  const Item item = w.items[n];
-  const uint2 row = w.rows[item.id];
-  const uint32_t slice = (uint32_t)(k - n * w.slices), base = slice * place_cols(MODE);
-  const Place<MODE> at(base, a.dim, lane, row_at<OT>(a.dtable, item.id));
-  const uint32_t from = item.part * kPart;
-  add_rows<DT, MODE>(a.dout, w.tokens + row.x + from, min(kPart, row.y - from), at, acc);
-  // a lane's sums, 16 bytes apart: the place of lane `lane` of slice `slice`
-  float* sums = w.sums + (uint64_t)item.first * w.pitch + base + 4 * lane;
+  const uint32_t tile = (uint32_t)n, total = *w.total, begin = tile << w.tile_bits;
+  if (begin >= total) return;
+  const uint32_t end = min(total, begin + (1u << w.tile_bits));
+  const uint32_t after = end < total ? w.order[end].x : ~0u;
+  const uint32_t before = begin ? w.order[begin - 1].x : ~0u;
+  const uint2 entry = begin + lane < end ? w.order[begin + lane] : make_uint2(~0u, 0);
+  // rows in flight: as many as make CR_EB_BYTES of a lane
+  constexpr int ahead = CR_EB_BYTES / (place_vals(MODE) * (DT == CR_BF16 ? 2 : 4));
+  Loaded<DT, MODE> in[ahead];
+  const auto load = [&](Loaded<DT, MODE>& to, uint32_t i) {
+    const uint32_t id = __shfl_sync(~0u, entry.x, i & 31), token = __shfl_sync(~0u, entry.y, i & 31);
+    if (i < end - begin)
+      to.load(row_at<DT>(a.dout, token), Place<MODE>(col, a.dim, lane, row_at<OT>(a.dtable, id)));
+  };
 #pragma unroll
-  for (int e = 0; e < vals; e += 4)
-    *reinterpret_cast<float4*>(sums + item.part * w.pitch + 32 * e) =
-        make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-  __threadfence();
-  __syncwarp();
-  uint32_t done = 0;
-  if (lane == 0) done = atomicAdd(&w.ticks[(uint64_t)item.first * w.slices + slice], 1u);
-  if (__shfl_sync(~0u, done, 0) != item.parts - 1) return;
-  __threadfence();  // the last part: the others' sums are there
+  for (int j = 0; j < ahead; ++j) load(in[j], j);
+  bool joined = __shfl_sync(~0u, entry.x, 0) == before;  // the row at work began in an earlier tile
+#pragma unroll 1
+  for (uint32_t i = 0; i < end - begin; ++i) {
+    const uint32_t id = __shfl_sync(~0u, entry.x, i), next = __shfl_sync(~0u, entry.x, (i + 1) & 31);
+    in[0].ready();
 #pragma unroll
-  for (int e = 0; e < vals; ++e) acc[e] = 0.0f;
-  for (uint32_t p = 0; p < item.parts; ++p) {
+    for (int e = 0; e < vals; ++e) acc[e] += in[0].value(e);
 #pragma unroll
-    for (int e = 0; e < vals; e += 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(sums + p * w.pitch + 32 * e));
-      acc[e] += v.x, acc[e + 1] += v.y, acc[e + 2] += v.z, acc[e + 3] += v.w;
+    for (int j = 1; j < ahead; ++j) in[j - 1] = in[j];
+    load(in[ahead - 1], i + ahead);
+    const bool ends = i + 1 == end - begin, goes_on = ends && after == id;
+    if (!ends && next == id) continue;
+    bool whole = true;
+    if (joined || goes_on) {
+      // a lane's sums, 16 bytes apart
+      float* sums = w.sums + col + 4 * lane;
+      float* mine = sums + (2 * (uint64_t)tile + (joined ? 0 : 1)) * w.pitch;
+#pragma unroll
+      for (int e = 0; e < vals; e += 4)
+        *reinterpret_cast<float4*>(mine + 32 * e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+      __threadfence();
+      __syncwarp();
+      const uint2 row = w.rows[id];
+      const uint32_t from = row.x >> w.tile_bits, parts = ((row.x + row.y - 1) >> w.tile_bits) - from + 1;
+      uint32_t done = 0;
+      if (lane == 0) done = atomicAdd(&w.ticks[(uint64_t)from * w.slices + slice], 1u);
+      whole = __shfl_sync(~0u, done, 0) == parts - 1;
+      joined = false;
+      if (whole) {  // the others' sums are there
+        __threadfence();
+#pragma unroll
+        for (int e = 0; e < vals; ++e) acc[e] = 0.0f;
+#pragma unroll 1
+        for (uint32_t p = 0; p < parts; ++p) {
+          const float* part = sums + (2 * (uint64_t)(from + p) + (p ? 0 : 1)) * w.pitch;
+#pragma unroll
+          for (int e = 0; e < vals; e += 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + 32 * e));
+            acc[e] += v.x, acc[e + 1] += v.y, acc[e + 2] += v.z, acc[e + 3] += v.w;
+          }
+        }
+      }
     }
+    if (whole) finish<OT, MODE>(a, id, col, lane, acc);
+#pragma unroll
+    for (int e = 0; e < vals; ++e) acc[e] = 0.0f;
   }
-  finish<OT, MODE>(a, item.id, at, acc);
 }
 
 template <int DT, int OT, int MODE>
 cudaError_t run(const EmbedBackArgs& a, void* workspace, cudaStream_t s) {
   Sorted w;
   layout(&w, workspace, a.tokens, a.vocab, a.dim, place_chunks(a.dim, MODE));
-  cudaError_t e = launch_pdl(k_sort, dim3(w.chunks), kChunk, s, a.ids, a.tokens, a.vocab, w);
-  if (e == cudaSuccess) e = launch_pdl(k_group, dim3(w.buckets), kLocals, s, a.vocab, w);
+  const cudaError_t e = launch_pdl(k_group, dim3(w.buckets), kThreads, s, a.ids, (uint32_t)a.tokens,
+                                   a.vocab, w);
   if (e != cudaSuccess) return e;
-  const uint64_t warps = ((uint64_t)w.cap + a.vocab) * w.slices;
+  const uint64_t warps = ((uint64_t)w.tiles + (a.in_place ? 0 : a.vocab)) * w.slices;
+  if (warps == 0) return cudaSuccess;
   return launch_pdl(k_sum<DT, OT, MODE>, dim3((unsigned)((warps + kBlock / 32 - 1) / (kBlock / 32))),
                     kBlock, s, a, w, fastdiv_make(w.slices, warps));
 }

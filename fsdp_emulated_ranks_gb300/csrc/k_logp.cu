@@ -31,31 +31,43 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+#ifndef CR_LOGP_FILL
+#define CR_LOGP_FILL 4
+#define CR_LOGP_ROWS 4
+#define CR_LOGP_TEAM 128
+#endif
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kFar = -1e30f;  // 2^kFar = 0
-constexpr int kUnroll = 4;      // 16-byte vectors of a thread in flight
-constexpr int kWarpMaxCl = 8;   // blocks of a cluster at most
+#ifndef CR_LOGP_UNROLL
+#define CR_LOGP_UNROLL 4
+#endif
+constexpr int kUnroll = CR_LOGP_UNROLL;      // 16-byte vectors of a thread in flight
+constexpr uint32_t kMostParts = 8;  // blocks of a cluster at most
 
 // Sums over some columns of a row: see above.  s = 0: none, or all -infinity.
 struct Stat {
   float m, s, w;
 };
 
-__device__ __forceinline__ Stat merge(const Stat& a, const Stat& b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  const float da = a.m == -kInf ? 0.0f : (a.m - m) * c, db = b.m == -kInf ? 0.0f : (b.m - m) * c;
-  const float fa = fast_exp2(da), fb = fast_exp2(db);
-  // what is far below adds nothing, and 0 times -infinity is not to be formed
-  return {m, fmaf(fa, a.s, fb * b.s),
-          fmaf(fa, fmaf(fmaxf(da, kFar), a.s, a.w), fb * fmaf(fmaxf(db, kFar), b.s, b.w))};
+// v's sums with the reference m >= v.m.  What is far below adds nothing, and 0 times
+// -infinity is not to be formed.
+__device__ __forceinline__ Stat moved(const Stat& v, float m, float c) {
+  const float d = v.m == -kInf ? 0.0f : (v.m - m) * c, f = fast_exp2(d);
+  return {m, f * v.s, f * fmaf(fmaxf(d, kFar), v.s, v.w)};
 }
 
-__device__ __forceinline__ Stat warp_merge(Stat v, float c) {
+// The sums of N neighbouring lanes, for all of them.
+template <int N>
+__device__ __forceinline__ Stat lanes_merge(Stat v, float c) {
+  float m = v.m;
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
-    v = merge(v, Stat{__shfl_xor_sync(~0u, v.m, o), __shfl_xor_sync(~0u, v.s, o),
-                      __shfl_xor_sync(~0u, v.w, o)},
-              c);
+  for (int o = N / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  v = moved(v, m, c);
+#pragma unroll
+  for (int o = N / 2; o; o >>= 1) {
+    v.s += __shfl_xor_sync(~0u, v.s, o);
+    v.w += __shfl_xor_sync(~0u, v.w, o);
+  }
   return v;
 }
 
@@ -124,55 +136,122 @@ struct RowPart {
   }
 };
 
-// The largest of two packed bf16 pairs (NaN passed over).
+// Largest and smallest of packed bf16 pairs, NaN passed over.
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
+// Largest (x) and smallest (y) logit of N vectors, NaN passed over.
 template <int DT, int N>
-__device__ __forceinline__ float largest(const uint4 (&v)[N]) {
+__device__ __forceinline__ float2 extremes(const uint4 (&v)[N]) {
   if constexpr (DT == CR_BF16) {
-    uint32_t m = v[0].x;
+    uint32_t hi = v[0].x, lo = v[0].x;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (i) m = max_bf16x2(m, v[i].x);
-      m = max_bf16x2(max_bf16x2(m, v[i].y), max_bf16x2(v[i].z, v[i].w));
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int e = i ? 0 : 1; e < 4; ++e) hi = max_bf16x2(hi, w[e]), lo = min_bf16x2(lo, w[e]);
     }
-    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    return make_float2(fmaxf(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)),
+                       fminf(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u)));
   } else {
-    float m = -kInf;
+    float hi = -kInf, lo = kInf;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      m = fmaxf(m, fmaxf(__uint_as_float(v[i].x), __uint_as_float(v[i].y)));
-      m = fmaxf(m, fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w)));
+      const float x = __uint_as_float(v[i].x), y = __uint_as_float(v[i].y);
+      const float z = __uint_as_float(v[i].z), w = __uint_as_float(v[i].w);
+      hi = fmaxf(fmaxf(hi, x), y), lo = fminf(fminf(lo, x), y);
+      hi = fmaxf(fmaxf(hi, z), w), lo = fminf(fminf(lo, z), w);
     }
-    return m;
+    return make_float2(hi, lo);
   }
 }
 
-// A thread's running sums.
-template <bool ENT>
+// Two floats in a 64-bit register, and the operations on both at once.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(Two a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A thread's running sums, of two columns at a time: fp32 instructions are what bounds
+// the sum, and packed ones do two columns' work.
 struct Running {
-  Stat v = {-kInf, 0.0f, 0.0f};
+  float m = -kInf;  // largest logit
+  Two s = 0, w = 0;
 
   __device__ __forceinline__ void reach(float x, float c) {
-    if (!(x > v.m)) return;
-    if (v.m != -kInf) {
-      const float d = (v.m - x) * c, f = fast_exp2(d);
-      if constexpr (ENT) v.w = f * fmaf(fmaxf(d, kFar), v.s, v.w);
-      v.s *= f;
+    if (!(x > m)) return;
+    if (m != -kInf) {
+      const float d = (m - x) * c, f = fast_exp2(d), far = fmaxf(d, kFar);
+      w = mul2(two(f, f), fma2(two(far, far), s, w));
+      s = mul2(two(f, f), s);
     }
-    v.m = x;
+    m = x;
   }
-  __device__ __forceinline__ void add(float x, float c, float m) {
-    const float t = (x - m) * c, e = fast_exp2(t);
-    v.s += e;
-    if constexpr (ENT) v.w = fmaf(e, fmaxf(t, kFar), v.w);  // 0 times -infinity is 0 here
+  // What is subtracted of a logit: -infinity less -infinity is not to be formed.
+  __device__ __forceinline__ float reference() const { return m == -kInf ? 0.0f : m; }
+
+  // x less the reference, times c.  FAR: some x may be -infinity, and 0 times that is 0 here.
+  template <bool FAR>
+  __device__ __forceinline__ void add(Two x, Two minus, Two c) {
+    const Two t = mul2(add2(x, minus), c);
+    float2 u = both(t);
+    const Two e = two(fast_exp2(u.x), fast_exp2(u.y));
+    s = add2(s, e);
+    w = fma2(e, FAR ? two(fmaxf(u.x, kFar), fmaxf(u.y, kFar)) : t, w);
   }
-  // What add() subtracts: -infinity less -infinity is not to be formed.
-  __device__ __forceinline__ float reference() const { return v.m == -kInf ? 0.0f : v.m; }
+  template <int DT, bool FAR, int N>
+  __device__ __forceinline__ void add_vectors(const uint4 (&v)[N], float c) {
+    const float r = reference();
+    const Two minus = two(-r, -r), cc = two(c, c);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < RowPart<DT>::kVec; e += 2)
+        add<FAR>(two(RowPart<DT>::value(v[i], e), RowPart<DT>::value(v[i], e + 1)), minus, cc);
+  }
+  template <int DT, int N>
+  __device__ __forceinline__ void take(const uint4 (&v)[N], float c) {
+    const float2 ends = extremes<DT>(v);
+    reach(ends.x, c);
+    if ((ends.y - reference()) * c >= kFar)
+      add_vectors<DT, false>(v, c);
+    else
+      add_vectors<DT, true>(v, c);
+  }
+  __device__ __forceinline__ Stat stat() const {
+    const float2 a = both(s), b = both(w);
+    return {m, a.x + a.y, b.x + b.y};
+  }
 };
 
 // What the threads of a team (a warp, or a block) share for the most likely tokens.
@@ -180,7 +259,7 @@ template <int TEAM>
 struct TopShared {
   static constexpr int kGroups = TEAM == 32 ? 32 : 64;
   static constexpr int kCands = TEAM == 32 ? 256 : 1024;
-  uint64_t keys[kGroups];
+  alignas(16) uint64_t keys[kGroups];
   uint64_t cand[kCands];
   uint64_t best[CR_MAX_TOP];
   uint64_t bound;
@@ -196,26 +275,31 @@ __device__ __forceinline__ void team_sync() {
     __syncthreads();
 }
 
-// sh.bound = the k-th largest of the groups' largest keys.
-template <int TEAM>
-__device__ __forceinline__ void find_bound(TopShared<TEAM>& sh, uint64_t key, int k, int t) {
-  constexpr int per = TEAM / TopShared<TEAM>::kGroups;
+// sh.bound = the k-th largest of the groups' largest keys (KEY: 32 bits, a pair's upper
+// half, or 64).
+template <int TEAM, typename KEY>
+__device__ __forceinline__ void find_bound(TopShared<TEAM>& sh, KEY key, int k, int t) {
+  constexpr int groups = TopShared<TEAM>::kGroups, per = TEAM / groups, wide = 16 / sizeof(KEY);
+  KEY* keys = reinterpret_cast<KEY*>(sh.keys);
 #pragma unroll
   for (int o = 1; o < per; o <<= 1) {
-    const uint64_t other = __shfl_xor_sync(~0u, key, o);
+    const KEY other = __shfl_xor_sync(~0u, key, o);
     key = other > key ? other : key;
   }
-  if (t % per == 0) sh.keys[t / per] = key;
+  if (t % per == 0) keys[t / per] = key;
   if (t == 0) sh.count = sh.threads = 0;
   team_sync<TEAM>();
-  if (t < TopShared<TEAM>::kGroups) {
-    const uint64_t mine = sh.keys[t];
+  if (t < groups) {
+    const KEY mine = keys[t];
     int rank = 0;
-    for (int i = 0; i < TopShared<TEAM>::kGroups; ++i) {
-      const uint64_t other = sh.keys[i];
-      rank += other > mine || (other == mine && i < t);
+#pragma unroll 4
+    for (int i = 0; i < groups; i += wide) {
+      KEY other[wide];
+      *reinterpret_cast<uint4*>(other) = *reinterpret_cast<const uint4*>(keys + i);
+#pragma unroll
+      for (int e = 0; e < wide; ++e) rank += other[e] > mine || (other[e] == mine && i + e < t);
     }
-    if (rank == k - 1) sh.bound = mine;
+    if (rank == k - 1) sh.bound = sizeof(KEY) == 4 ? (uint64_t)mine << 32 : (uint64_t)mine;
   }
   team_sync<TEAM>();
 }
@@ -257,18 +341,17 @@ template <int DT, int TEAM>
 __device__ __forceinline__ void find_top(TopShared<TEAM>& sh, const RowPart<DT>& row, float most,
                                          bool any, int k, int t) {
   constexpr uint32_t cands = TopShared<TEAM>::kCands;
-  // a pair of the thread's largest logit is at least this
-  uint64_t key = any ? (uint64_t)order_key(most) << 32 : 0;
-  find_bound<TEAM>(sh, key, k, t);
-  collect<DT, TEAM>(sh, row, any ? key | 0xffffffffu : 0, t);
+  const uint32_t upper = any ? order_key(most) : 0;
+  find_bound<TEAM, uint32_t>(sh, upper, k, t);
+  collect<DT, TEAM>(sh, row, any ? (uint64_t)upper << 32 | 0xffffffffu : 0, t);
   if (sh.count > cands) {
-    key = 0;
+    uint64_t key = 0;
     row.each_of(t, TEAM, [&](uint32_t col, float x) {
       const uint64_t pair = pair_key(x, row.begin + col);
       key = pair > key ? pair : key;
     });
     team_sync<TEAM>();  // sh.count has been read
-    find_bound<TEAM>(sh, key, k, t);
+    find_bound<TEAM, uint64_t>(sh, key, k, t);
     collect<DT, TEAM>(sh, row, key, t);
   }
   const uint32_t n = sh.count;
@@ -304,48 +387,39 @@ __device__ __forceinline__ void find_top(TopShared<TEAM>& sh, const RowPart<DT>&
   team_sync<TEAM>();
 }
 
-// Sums and most likely tokens of a part of a row, by the threads of a team.  Every
-// thread returns the sums.  `stats`: TEAM / 32 of them in shared memory.
-template <int DT, int TEAM, bool ENT, bool TOP>
+// Sums and most likely tokens of a part of a row, by the threads of a team.  The first
+// warp returns the sums.  `stats`: TEAM / 32 of them in shared memory.
+template <int DT, int TEAM, bool TOP>
 __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k, int t,
                                           TopShared<TEAM>* sh, Stat* stats) {
   using Part = RowPart<DT>;
-  Running<ENT> run;
+  Running run;
   for (uint64_t j = t; j < row.vectors; j += (uint64_t)TEAM * kUnroll) {
     uint4 v[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i)
       v[i] = j + i * TEAM < row.vectors ? row.vec((uint32_t)(j + i * TEAM)) : Part::none();
-    run.reach(largest<DT>(v), c);
-    const float m = run.reference();
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i)
-#pragma unroll
-      for (int e = 0; e < Part::kVec; ++e) run.add(Part::value(v[i], e), c, m);
+    run.take<DT>(v, c);
   }
-#pragma unroll
-  for (int end = 0; end < 2; ++end) {
-    if ((uint32_t)t >= (end ? row.tail : row.head)) continue;
-    const float x = row.one(end ? row.head + row.vectors * Part::kVec + t : t);
-    run.reach(x, c);
-    run.add(x, c, run.reference());
+  if ((uint32_t)t < row.head || (uint32_t)t < row.tail) {
+    const float x = (uint32_t)t < row.head ? row.one(t) : -kInf;
+    const float y = (uint32_t)t < row.tail ? row.one(row.head + row.vectors * Part::kVec + t) : -kInf;
+    run.reach(fmaxf(x, y), c);
+    const float r = run.reference();
+    run.add<true>(two(x, y), two(-r, -r), two(c, c));
   }
-  Stat all = warp_merge(run.v, c);
+  Stat all = lanes_merge<32>(run.stat(), c);
   if constexpr (TEAM > 32) {
     if (t % 32 == 0) stats[t / 32] = all;
     __syncthreads();
-    all = stats[0];
-#pragma unroll
-    for (int w = 1; w < TEAM / 32; ++w) all = merge(all, stats[w], c);
+    if (t < 32) all = lanes_merge<TEAM / 32>(stats[t % (TEAM / 32)], c);
   }
   if constexpr (TOP) {
     const bool any = (uint32_t)t < row.vectors || (uint32_t)t < row.head || (uint32_t)t < row.tail;
     // a largest logit of -infinity may stand for NaN alone, which is below it
-    uint32_t has = 0;
-    if (any && run.v.m == -kInf)
-      row.each_of(t, TEAM, [&](uint32_t, float x) { has |= x == -kInf; });
-    const float most = any && run.v.m == -kInf && !has ? __int_as_float(0x7fc00000) : run.v.m;
-    find_top<DT, TEAM>(*sh, row, most, any, k, t);
+    bool has = run.m != -kInf;
+    if (any && !has) row.each_of(t, TEAM, [&](uint32_t, float x) { has = has || x == -kInf; });
+    find_top<DT, TEAM>(*sh, row, has ? run.m : __int_as_float(0x7fc00000), any, k, t);
   }
   return all;
 }
@@ -385,7 +459,7 @@ __device__ __forceinline__ void write_top(const LogProbArgs& a, uint64_t row, in
 }
 
 // A warp a row.
-template <int DT, bool ENT, bool TOP>
+template <int DT, bool TOP>
 __global__ void __launch_bounds__(kBlock) k_logp_warp(const __grid_constant__ LogProbArgs a) {
   __shared__ TopShared<32> top[TOP ? kBlock / 32 : 1];
   pdl_enter();
@@ -396,7 +470,7 @@ __global__ void __launch_bounds__(kBlock) k_logp_warp(const __grid_constant__ Lo
     const char* logits = row_at<DT>(a.logits, row);
     const RowPart<DT> part(logits, 0, a.vocab);
     TopShared<32>* sh = TOP ? &top[warp] : nullptr;
-    const Stat v = read_part<DT, 32, ENT, TOP>(part, c, a.top, lane, sh, nullptr);
+    const Stat v = read_part<DT, 32, TOP>(part, c, a.top, lane, sh, nullptr);
     if (lane == 0) write_row<DT>(a, row, v, logits);
     if constexpr (TOP) {
       if (lane < a.top) write_top<DT>(a, row, lane, sh->best[lane], v, logits);
@@ -405,13 +479,13 @@ __global__ void __launch_bounds__(kBlock) k_logp_warp(const __grid_constant__ Lo
   }
 }
 
-// A block a row, or a cluster a row (gridDim.x a multiple of the cluster).
-template <int DT, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kBlock) k_logp_block(const __grid_constant__ LogProbArgs a,
-                                                       uint32_t per) {
-  __shared__ TopShared<kBlock> top[1];
-  __shared__ Stat stats[kBlock / 32];
-  __shared__ Stat shared_stat;
+// A block of TEAM threads a row, or a cluster a row (gridDim.x a multiple of the cluster).
+template <int DT, int TEAM, bool TOP>
+__global__ void __launch_bounds__(TEAM) k_logp_block(const __grid_constant__ LogProbArgs a,
+                                                     uint32_t per) {
+  __shared__ TopShared<TOP ? TEAM : 32> top[1];
+  __shared__ Stat stats[TEAM / 32];
+  __shared__ Stat sums;
   pdl_enter();
   const float c = a.scale * kLog2E;
   const int t = threadIdx.x;
@@ -421,58 +495,53 @@ __global__ void __launch_bounds__(kBlock) k_logp_block(const __grid_constant__ L
     const char* logits = row_at<DT>(a.logits, row);
     const uint32_t begin = min(part_no * per, a.vocab);
     const RowPart<DT> part(logits, begin, min(per, a.vocab - begin));
-    Stat v = read_part<DT, kBlock, ENT, TOP>(part, c, a.top, t, top, stats);
-    if (parts == 1) {
-      if (t == 0) write_row<DT>(a, row, v, logits);
-      if constexpr (TOP) {
-        if (t < a.top) write_top<DT>(a, row, t, top->best[t], v, logits);
-      }
-      __syncthreads();
-      continue;
+    TopShared<TEAM>* sh = nullptr;
+    if constexpr (TOP) sh = top;
+    Stat v = read_part<DT, TEAM, TOP>(part, c, a.top, t, sh, stats);
+    if (parts > 1) {
+      if (t == 0) sums = v;
+      cluster.sync();
+      if (part_no == 0 && t < 32)
+        v = lanes_merge<kMostParts>(t % kMostParts < parts ? *cluster.map_shared_rank(&sums, t % kMostParts)
+                                                           : Stat{-kInf, 0.0f, 0.0f}, c);
     }
-    if (t == 0) shared_stat = v;
-    cluster.sync();
     if (part_no == 0) {
-      for (uint32_t q = 1; q < parts; ++q) v = merge(v, *cluster.map_shared_rank(&shared_stat, q), c);
       if (t == 0) write_row<DT>(a, row, v, logits);
       if constexpr (TOP) {
-        // rank the parts' best among each other
+        if (t == 0) sums = v;
         const int n = (int)parts * a.top;
-        static_assert(kWarpMaxCl * CR_MAX_TOP <= kBlock, "a thread for every pair");
         uint64_t mine = 0;
-        if (t < n) {
-          mine = cluster.map_shared_rank(top, t / a.top)->best[t % a.top];
-          top->cand[t] = mine;
-        }
+        if (parts > 1)  // rank the parts' best among each other
+          for (int i = t; i < n; i += TEAM)
+            top->cand[i] = cluster.map_shared_rank(top, i / a.top)->best[i % a.top];
         __syncthreads();
-        if (t < n) {
-          int rank = 0;
-          for (int i = 0; i < n; ++i) rank += top->cand[i] > mine;
+        v = sums;
+        for (int i = t; i < n; i += TEAM) {
+          int rank = i;
+          if (parts > 1) {
+            mine = top->cand[i];
+            rank = 0;
+            for (int j = 0; j < n; ++j) rank += top->cand[j] > mine;
+          } else {
+            mine = top->best[i];
+          }
           if (rank < a.top) write_top<DT>(a, row, rank, mine, v, logits);
         }
       }
     }
-    cluster.sync();
+    if (parts > 1)
+      cluster.sync();
+    else
+      __syncthreads();
   }
 }
 
-template <int DT, bool ENT, bool TOP>
-cudaError_t run(const LogProbArgs& a, cudaStream_t s) {
-  int sms = 0;
-  cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
-  if (a.vocab <= 2048 && a.rows >= (uint64_t)sms)
-    return launch_pdl(k_logp_warp<DT, ENT, TOP>, dim3(flat_grid(a.rows * 32)), kBlock, s, a);
-  // Parts of a row: while rows are too few to fill the SMs, and parts keep two vectors a
-  // thread (and more columns than are wanted of them).
-  uint32_t parts = 1;
-  while (parts < kWarpMaxCl && a.rows * parts < 4 * (uint64_t)sms &&
-         a.vocab / (2 * parts) >= 2 * kBlock * RowPart<DT>::kVec)
-    parts *= 2;
+template <int DT, int TEAM, bool TOP>
+cudaError_t run_block(const LogProbArgs& a, uint32_t parts, cudaStream_t s) {
   const uint32_t per = (uint32_t)((((uint64_t)a.vocab + parts - 1) / parts + 63) / 64 * 64);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(std::min<uint64_t>(a.rows, 1u << 27) * parts));
-  cfg.blockDim = dim3(kBlock);
+  cfg.blockDim = dim3(TEAM);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -482,19 +551,31 @@ cudaError_t run(const LogProbArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_logp_block<DT, ENT, TOP>, a, per);
+  return cudaLaunchKernelEx(&cfg, k_logp_block<DT, TEAM, TOP>, a, per);
 }
 
-template <int DT>
-cudaError_t by_outputs(const LogProbArgs& a, cudaStream_t s) {
-  if (a.top) return a.entropy ? run<DT, true, true>(a, s) : run<DT, false, true>(a, s);
-  return a.entropy ? run<DT, true, false>(a, s) : run<DT, false, false>(a, s);
+template <int DT, bool TOP>
+cudaError_t run(const LogProbArgs& a, cudaStream_t s) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  if (a.vocab <= 2048 && a.rows >= (uint64_t)sms)
+    return launch_pdl(k_logp_warp<DT, TOP>, dim3(flat_grid(a.rows * 32)), kBlock, s, a);
+  // Parts of a row: while rows are too few to fill the SMs, and parts keep two vectors a
+  // thread (and more columns than are wanted of them).
+  uint32_t parts = 1;
+  while (parts < kMostParts && a.rows * parts < CR_LOGP_FILL * (uint64_t)sms &&
+         a.vocab / (2 * parts) >= 2 * kBlock * RowPart<DT>::kVec)
+    parts *= 2;
+  if (parts == 1 && a.rows >= CR_LOGP_ROWS * (uint64_t)sms) return run_block<DT, CR_LOGP_TEAM, TOP>(a, 1, s);
+  return run_block<DT, kBlock, TOP>(a, parts, s);
 }
 
 }  // namespace
 
 cudaError_t launch_log_probs(cr_dtype d, const LogProbArgs& a, cudaStream_t s) {
-  return d == CR_BF16 ? by_outputs<CR_BF16>(a, s) : by_outputs<CR_F32>(a, s);
+  if (d == CR_BF16) return a.top ? run<CR_BF16, true>(a, s) : run<CR_BF16, false>(a, s);
+  return a.top ? run<CR_F32, true>(a, s) : run<CR_F32, false>(a, s);
 }
 
 }  // namespace cr

@@ -14,7 +14,11 @@ namespace cr {
 
 namespace {
 
-constexpr int kAhead = 2;  // chunks of a warp in flight
+#ifndef CR_LB_AHEAD
+#define CR_LB_AHEAD 2
+#define CR_LB_OCC 4
+#endif
+constexpr int kAhead = CR_LB_AHEAD;  // chunks of a warp in flight
 
 // An lse at or below this has no token left: nothing of the row's logits is known better than that.
 constexpr float kNoToken = -1.2676506e30f;  // -2^100
@@ -52,45 +56,42 @@ __device__ __forceinline__ float gradient(float x, float scale, const RowTerms& 
   return p * fmaf(-r.ent, fmaxf(log_p, -1e30f), r.by);  // 0 times -infinity is 0 here
 }
 
+// A warp takes kAhead chunks of a row, next to each other, so that the row's numbers are read once.
 template <int DT, int MODE, bool ENT>
-__global__ void __launch_bounds__(kBlock) k_logp_back(const __grid_constant__ LogProbBackArgs a,
+__global__ void __launch_bounds__(kBlock, CR_LB_OCC) k_logp_back(const __grid_constant__ LogProbBackArgs a,
                                                       const __grid_constant__ ChunkRange r) {
   constexpr int vals = place_vals(MODE);
+  constexpr uint32_t cols = place_cols(MODE);
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const uint64_t stride = (uint64_t)gridDim.x * (kBlock / 32);
   for (uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); k < r.chunks;
-       k += kAhead * stride) {
+       k += stride) {
+    const uint64_t row = fastdiv_div(r.per_row, k);
+    const uint32_t base = (uint32_t)(k - row * r.per_row.d) * kAhead * cols;
+    const char* from = row_at<DT>(a.logits, row);
+    char* out = row_at<DT>(a.dlogits, row);
     Loaded<DT, MODE> in[kAhead];
-    RowTerms terms[kAhead];
-    uint64_t row[kAhead];
-    uint32_t base[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      in[j].load(from, Place<MODE>(base + j * cols, a.vocab, lane, out));
+    const RowTerms terms = row_terms<ENT>(a, row);
+    const uint32_t near = (uint32_t)terms.target - base + 7;  // spans lead by up to 7 columns
+    const bool hit = terms.target >= 0 && near < kAhead * cols + 7;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const uint64_t n = k + j * stride;
-      if (n >= r.chunks) break;
-      row[j] = fastdiv_div(r.per_row, n);
-      base[j] = (uint32_t)(n - row[j] * r.per_row.d) * place_cols(MODE);
-      const Place<MODE> at(base[j], a.vocab, lane, row_at<DT>(a.dlogits, row[j]));
-      in[j].load(row_at<DT>(a.logits, row[j]), at);
-      terms[j] = row_terms<ENT>(a, row[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (k + j * stride >= r.chunks) break;
-      char* out = row_at<DT>(a.dlogits, row[j]);
-      const Place<MODE> at(base[j], a.vocab, lane, out);
+      const Place<MODE> at(base + j * cols, a.vocab, lane, out);
       float v[vals];
       in[j].ready();
 #pragma unroll
-      for (int i = 0; i < vals; ++i) v[i] = gradient<ENT>(in[j].value(i), a.scale, terms[j]);
-      if (terms[j].target >= 0) {
-        int64_t first = base[j] + (MODE == 0 ? lane : lane * vals);
+      for (int i = 0; i < vals; ++i) v[i] = gradient<ENT>(in[j].value(i), a.scale, terms);
+      if (hit) {
+        int64_t first = base + j * cols + (MODE == 0 ? lane : lane * vals);
         if constexpr (MODE == kSpan) first = at.span.first;
-        const int64_t d = terms[j].target - first;
+        const int64_t d = terms.target - first;
 #pragma unroll
         for (int i = 0; i < vals; ++i)
-          if (d == (MODE == 0 ? 32 * i : i)) v[i] += terms[j].hit;
+          if (d == (MODE == 0 ? 32 * i : i)) v[i] += terms.hit;
       }
       st_place<DT, MODE>(out, at, v);
     }
@@ -99,10 +100,10 @@ __global__ void __launch_bounds__(kBlock) k_logp_back(const __grid_constant__ Lo
 
 template <int DT, int MODE>
 cudaError_t run(const LogProbBackArgs& a, cudaStream_t s) {
-  const uint64_t per_row = place_chunks(a.vocab, MODE);
+  const uint64_t per_row = (place_chunks(a.vocab, MODE) + kAhead - 1) / kAhead;
   const ChunkRange r = {a.rows * per_row, fastdiv_make(per_row, a.rows * per_row)};
   return launch_pdl(a.dentropy ? k_logp_back<DT, MODE, true> : k_logp_back<DT, MODE, false>,
-                    chunk_grid(r, kAhead), kBlock, s, a, r);
+                    chunk_grid(r, 1), kBlock, s, a, r);
 }
 
 }  // namespace
