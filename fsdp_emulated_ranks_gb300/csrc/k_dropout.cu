@@ -94,11 +94,11 @@ __global__ void __launch_bounds__(kBlock, CR_D_OCC) k_dropout(const __grid_const
       x[j].ready();
       if constexpr (RES) res[j].ready();
       const auto set = [&](int i, uint32_t number) {
-        const float kept = some && number >= limit ? __fmul_rn(x[j].value(i), a.by) : 0.0f;
+        const float kept = some && number >= limit ? x[j].value(i) : 0.0f;
         if constexpr (RES)
-          v[i] = __fadd_rn(res[j].value(i), kept);
+          v[i] = fmaf(kept, a.by, res[j].value(i));
         else
-          v[i] = kept;
+          v[i] = kept * a.by;
       };
       if constexpr (MODE == 0) {
         uint16_t* t = turned[threadIdx.x >> 5];

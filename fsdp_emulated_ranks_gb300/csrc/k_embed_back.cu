@@ -23,8 +23,9 @@ namespace cr {
 namespace {
 
 constexpr int kThreads = 1024;        // of a block of k_group
-constexpr int kEach = 4;              // ids of a thread at a time
-constexpr uint32_t kStep = kThreads * kEach;
+constexpr int kEach = 8;              // ids of a thread at a time
+constexpr uint32_t kStepBits = 13, kStep = 1u << kStepBits;
+static_assert(kStep == kThreads * kEach, "a step is every thread's ids");
 constexpr uint32_t kLocals = 2048;    // ids of a bucket at most
 constexpr uint32_t kLeastBuckets = 128;
 
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids 
                                                     uint32_t vocab,
                                                     const __grid_constant__ Sorted w) {
   __shared__ uint32_t next[kLocals];  // counts, then where an id's next token goes
-  __shared__ uint2 list[kStep];       // a step's tokens of this bucket, in order
+  __shared__ uint32_t list[kStep];    // a step's tokens of this bucket, in order: id in the bucket, place in the step
   __shared__ uint32_t scan[32];
   __shared__ uint32_t earlier_all, valid_all;
   pdl_enter();
@@ -115,15 +116,19 @@ __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids 
   for (uint32_t k = t; k < kLocals; k += kThreads) next[k] = 0;
   if (t == 0) earlier_all = valid_all = 0;
   __syncthreads();
+  // A thread's ids are next to each other, so that its place in the list is one sum.
+  int32_t id[kEach];
+  const auto read = [&](uint64_t i0) {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const uint64_t i = i0 + kEach * t + j;
+      id[j] = i < tokens ? token_id(ids, i, vocab) : -1;
+    }
+  };
   // an id's tokens, and the tokens of earlier buckets
   uint32_t earlier = 0, valid = 0;
   for (uint64_t i0 = 0; i0 < tokens; i0 += kStep) {
-    int32_t id[kEach];
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const uint64_t i = i0 + j * kThreads + t;
-      id[j] = i < tokens ? token_id(ids, i, vocab) : -1;
-    }
+    read(i0);
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
       if (id[j] < 0) continue;
@@ -158,32 +163,26 @@ __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids 
   __syncthreads();
   // tokens to their places
   for (uint64_t i0 = 0; i0 < tokens; i0 += kStep) {
-    // a thread's ids are next to each other here, so that its place in the list is one sum
-    int32_t id[kEach];
+    if (tokens > kStep) read(i0);  // else they are still there
     uint32_t mine = 0;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const uint64_t i = i0 + kEach * t + j;
-      id[j] = i < tokens ? token_id(ids, i, vocab) : -1;
-      if (id[j] >= 0 && (id[j] & mask) != b) id[j] = -1;
-      mine += id[j] >= 0;
-    }
+    for (int j = 0; j < kEach; ++j) mine += id[j] >= 0 && (id[j] & mask) == b;
     uint32_t m;
     uint32_t slot = block_scan(mine, scan, &m);
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
-      if (id[j] >= 0) list[slot++] = make_uint2((uint32_t)id[j], (uint32_t)(i0 + kEach * t + j));
+      if (id[j] >= 0 && (id[j] & mask) == b)
+        list[slot++] = (uint32_t)id[j] >> w.bucket_bits << kStepBits | (kEach * t + j);
     __syncthreads();
     // a warp places its share of the ids, so that it alone moves their `next`
     for (uint32_t s = 0; s < m; s += 32) {
-      const uint2 e = s + lane < m ? list[s + lane] : make_uint2(~0u, 0);
-      const uint32_t local = e.x >> w.bucket_bits;
+      const uint32_t e = s + lane < m ? list[s + lane] : 0, local = e >> kStepBits;
       const bool own = s + lane < m && local % 32 == warp;
       if (!__any_sync(~0u, own)) continue;
       const uint32_t same = __match_any_sync(~0u, own ? local : ~0u);
       if (own) {
         const uint32_t place = next[local] + __popc(same & ((1u << lane) - 1));
-        w.order[place] = e;
+        w.order[place] = make_uint2(local << w.bucket_bits | b, (uint32_t)i0 + (e & (kStep - 1)));
       }
       __syncwarp();
       if (own && (same >> lane) == 1) next[local] += __popc(same);
@@ -219,8 +218,53 @@ __device__ __forceinline__ void finish(const EmbedBackArgs& a, uint32_t id, uint
   st_place<OT, MODE>(out, at, acc);
 }
 
-// Warps [0, tiles * slices) take the tokens' tiles; the others the rows without tokens,
-// a chunk each.
+constexpr uint32_t kFree = 16;  // chunks of the table that a warp looks at for rows without tokens
+
+// Warp n's chunks of rows without tokens: base, or zeros.
+template <int OT, int MODE>
+__device__ __forceinline__ void free_rows(const EmbedBackArgs& a, const Sorted& w, const FastDiv& slices,
+                                          uint64_t n, int lane) {
+  constexpr int vals = place_vals(MODE), ahead = 2;
+  const uint64_t first = n * kFree, all = (uint64_t)a.vocab * w.slices;
+  // a lane a chunk
+  const uint64_t mine = first + lane;
+  uint32_t id = 0, slice = 0;
+  bool is_free = false;
+  if (lane < kFree && mine < all) {
+    id = (uint32_t)fastdiv_div(slices, mine);
+    slice = (uint32_t)(mine - (uint64_t)id * w.slices);
+    is_free = w.rows[id].y == 0;
+  }
+  uint32_t left = __ballot_sync(~0u, is_free);
+  while (left) {
+    Loaded<OT, MODE> base[ahead];
+    uint32_t row[ahead], col[ahead];
+    int n_here = 0;
+#pragma unroll
+    for (int j = 0; j < ahead; ++j) {
+      if (!left) break;
+      const int at = __ffs(left) - 1;
+      left &= left - 1;
+      row[j] = __shfl_sync(~0u, id, at), col[j] = __shfl_sync(~0u, slice, at) * place_cols(MODE);
+      n_here = j + 1;
+      if (a.base.p)
+        base[j].load(row_at<OT>(a.base, row[j]),
+                     Place<MODE>(col[j], a.dim, lane, row_at<OT>(a.dtable, row[j])));
+    }
+#pragma unroll
+    for (int j = 0; j < ahead; ++j) {
+      if (j >= n_here) break;
+      char* out = row_at<OT>(a.dtable, row[j]);
+      float v[vals];
+      if (a.base.p) base[j].ready();
+#pragma unroll
+      for (int e = 0; e < vals; ++e) v[e] = a.base.p ? base[j].value(e) : 0.0f;
+      st_place<OT, MODE>(out, Place<MODE>(col[j], a.dim, lane, out), v);
+    }
+  }
+}
+
+// Warps [0, tiles * slices) take the tokens' tiles; the others the rows without tokens.
 template <int DT, int OT, int MODE>
 __global__ void __launch_bounds__(kBlock, CR_EB_OCC) k_sum(const __grid_constant__ EmbedBackArgs a,
                                                 const __grid_constant__ Sorted w,
@@ -229,16 +273,13 @@ __global__ void __launch_bounds__(kBlock, CR_EB_OCC) k_sum(const __grid_constant
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5);
+  const uint64_t tile_warps = (uint64_t)w.tiles * w.slices;
+  if (k >= tile_warps) return free_rows<OT, MODE>(a, w, slices, k - tile_warps, lane);
   const uint64_t n = fastdiv_div(slices, k);
   const uint32_t slice = (uint32_t)(k - n * w.slices), col = slice * place_cols(MODE);
   float acc[vals];
 #pragma unroll
   for (int e = 0; e < vals; ++e) acc[e] = 0.0f;
-  if (n >= w.tiles) {
-    const uint64_t id = n - w.tiles;
-    if (id < a.vocab && w.rows[id].y == 0) finish<OT, MODE>(a, (uint32_t)id, col, lane, acc);
-    return;
-  }
   const uint32_t tile = (uint32_t)n, total = *w.total, begin = tile << w.tile_bits;
   if (begin >= total) return;
   const uint32_t end = min(total, begin + (1u << w.tile_bits));
@@ -311,10 +352,11 @@ cudaError_t run(const EmbedBackArgs& a, void* workspace, cudaStream_t s) {
   const cudaError_t e = launch_pdl(k_group, dim3(w.buckets), kThreads, s, a.ids, (uint32_t)a.tokens,
                                    a.vocab, w);
   if (e != cudaSuccess) return e;
-  const uint64_t warps = ((uint64_t)w.tiles + (a.in_place ? 0 : a.vocab)) * w.slices;
+  const uint64_t chunks = (uint64_t)a.vocab * w.slices;
+  const uint64_t warps = (uint64_t)w.tiles * w.slices + (a.in_place ? 0 : (chunks + kFree - 1) / kFree);
   if (warps == 0) return cudaSuccess;
   return launch_pdl(k_sum<DT, OT, MODE>, dim3((unsigned)((warps + kBlock / 32 - 1) / (kBlock / 32))),
-                    kBlock, s, a, w, fastdiv_make(w.slices, warps));
+                    kBlock, s, a, w, fastdiv_make(w.slices, std::max(warps, chunks)));
 }
 
 template <int DT, int OT>

@@ -79,6 +79,12 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// The logit of such a key (0 for -0).
+__device__ __forceinline__ float key_logit(uint32_t key) {
+  if (key == 1) return __int_as_float(0x7fc00000);
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
 // A logit and its column as one number: larger for what comes first.
 __device__ __forceinline__ uint64_t pair_key(float x, uint32_t col) {
   return (uint64_t)order_key(x) << 32 | (0xffffffffu - col);
@@ -260,7 +266,7 @@ struct TopShared {
   static constexpr int kGroups = TEAM == 32 ? 32 : 64;
   static constexpr int kCands = TEAM == 32 ? 256 : 1024;
   alignas(16) uint64_t keys[kGroups];
-  uint64_t cand[kCands];
+  alignas(16) uint64_t cand[kCands];
   uint64_t best[CR_MAX_TOP];
   uint64_t bound;
   uint32_t count, threads;
@@ -318,21 +324,40 @@ __device__ __forceinline__ void collect(TopShared<TEAM>& sh, const RowPart<DT>& 
     const uint32_t slot = atomicAdd(&sh.count, 1u);
     if (slot < TopShared<TEAM>::kCands) sh.cand[slot] = pair;
   };
-  const int lane = t & 31;
-  for (uint32_t i = t / 32; i < n; i += TEAM / 32) {  // a warp takes a thread's columns
+  // Eight lanes take a thread's columns, so that a step of the team usually reads all there are.
+  const int sub = t % 8;
+  for (uint32_t i = t / 8; i < n; i += TEAM / 8) {
     const uint32_t who = sh.thread[i];
-    if (lane == 0 && who < row.head) look(who, row.one(who));
-    if (lane == 0 && who < row.tail)
+    if (sub == 0 && who < row.head) look(who, row.one(who));
+    if (sub == 1 && who < row.tail)
       look(row.head + row.vectors * RowPart<DT>::kVec + who,
            row.one(row.head + row.vectors * RowPart<DT>::kVec + who));
-    for (uint64_t j = who + (uint64_t)lane * TEAM; j < row.vectors; j += 32 * TEAM) {
-      const uint4 v = row.vec((uint32_t)j);
+    for (uint64_t j = who + (uint64_t)sub * TEAM; j < row.vectors; j += 16 * TEAM) {
+      uint4 v[2];
 #pragma unroll
-      for (int e = 0; e < RowPart<DT>::kVec; ++e)
-        look(row.head + (uint32_t)j * RowPart<DT>::kVec + e, RowPart<DT>::value(v, e));
+      for (int q = 0; q < 2; ++q)
+        v[q] = j + q * 8 * TEAM < row.vectors ? row.vec((uint32_t)j + q * 8 * TEAM) : RowPart<DT>::none();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (q && j + 8 * TEAM >= row.vectors) break;
+#pragma unroll
+        for (int e = 0; e < RowPart<DT>::kVec; ++e)
+          look(row.head + ((uint32_t)j + q * 8 * TEAM) * RowPart<DT>::kVec + e, RowPart<DT>::value(v[q], e));
+      }
     }
   }
   team_sync<TEAM>();
+}
+
+// How many of the n pairs are above `mine`; where n is odd, pairs[n] is 0.
+__device__ __forceinline__ int rank_of(const uint64_t* pairs, int n, uint64_t mine) {
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; j += 2) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(pairs + j);
+    rank += (v.x > mine) + (v.y > mine);
+  }
+  return rank;
 }
 
 // sh.best[0 .. k - 1] = the k largest pairs of the row part, which has at least k columns,
@@ -356,10 +381,11 @@ __device__ __forceinline__ void find_top(TopShared<TEAM>& sh, const RowPart<DT>&
   }
   const uint32_t n = sh.count;
   if (n <= cands) {
+    if (t == 0 && n % 2) sh.cand[n] = 0;  // n is even where the array is full
+    team_sync<TEAM>();
     for (uint32_t i = t; i < n; i += TEAM) {
       const uint64_t mine = sh.cand[i];
-      int rank = 0;
-      for (uint32_t j = 0; j < n && rank < k; ++j) rank += sh.cand[j] > mine;
+      const int rank = rank_of(sh.cand, n, mine);
       if (rank < k) sh.best[rank] = mine;
     }
   } else {
@@ -394,11 +420,20 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
                                           TopShared<TEAM>* sh, Stat* stats) {
   using Part = RowPart<DT>;
   Running run;
-  for (uint64_t j = t; j < row.vectors; j += (uint64_t)TEAM * kUnroll) {
-    uint4 v[kUnroll];
+  constexpr uint64_t step = (uint64_t)TEAM * kUnroll;
+  const auto load = [&](uint4 (&v)[kUnroll], uint64_t j) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i)
       v[i] = j + i * TEAM < row.vectors ? row.vec((uint32_t)(j + i * TEAM)) : Part::none();
+  };
+  // the next vectors are on their way while these are added
+  uint4 u[kUnroll], v[kUnroll];
+  load(u, t);
+  for (uint64_t j = t; j < row.vectors; j += 2 * step) {
+    load(v, j + step);
+    run.take<DT>(u, c);
+    if (j + step >= row.vectors) break;
+    load(u, j + 2 * step);
     run.take<DT>(v, c);
   }
   if ((uint32_t)t < row.head || (uint32_t)t < row.tail) {
@@ -445,14 +480,11 @@ __device__ __forceinline__ void write_row(const LogProbArgs& a, uint64_t row, co
   }
 }
 
-template <int DT>
 __device__ __forceinline__ void write_top(const LogProbArgs& a, uint64_t row, int i, uint64_t pair,
-                                          const Stat& v, const char* logits) {
-  const uint32_t col = 0xffffffffu - (uint32_t)pair;
-  if (a.top_ids) a.top_ids[row * a.top + i] = (int32_t)col;
+                                          const Stat& v) {
+  if (a.top_ids) a.top_ids[row * a.top + i] = (int32_t)(0xffffffffu - (uint32_t)pair);
   if (a.top_logp) {
-    const float x = DT == CR_BF16 ? ffn_bf16(reinterpret_cast<const uint16_t*>(logits)[col])
-                                  : reinterpret_cast<const float*>(logits)[col];
+    const float x = key_logit((uint32_t)(pair >> 32));
     a.top_logp[row * a.top + i] =
         v.s == 0.0f ? -kInf : fmaf(x - v.m, a.scale, -kLn2 * log2f(v.s));
   }
@@ -473,7 +505,7 @@ __global__ void __launch_bounds__(kBlock) k_logp_warp(const __grid_constant__ Lo
     const Stat v = read_part<DT, 32, TOP>(part, c, a.top, lane, sh, nullptr);
     if (lane == 0) write_row<DT>(a, row, v, logits);
     if constexpr (TOP) {
-      if (lane < a.top) write_top<DT>(a, row, lane, sh->best[lane], v, logits);
+      if (lane < a.top) write_top(a, row, lane, sh->best[lane], v);
       __syncwarp();
     }
   }
@@ -517,15 +549,9 @@ __global__ void __launch_bounds__(TEAM) k_logp_block(const __grid_constant__ Log
         __syncthreads();
         v = sums;
         for (int i = t; i < n; i += TEAM) {
-          int rank = i;
-          if (parts > 1) {
-            mine = top->cand[i];
-            rank = 0;
-            for (int j = 0; j < n; ++j) rank += top->cand[j] > mine;
-          } else {
-            mine = top->best[i];
-          }
-          if (rank < a.top) write_top<DT>(a, row, rank, mine, v, logits);
+          mine = parts > 1 ? top->cand[i] : top->best[i];
+          const int rank = parts > 1 ? rank_of(top->cand, n, mine) : i;  // parts is even
+          if (rank < a.top) write_top(a, row, rank, mine, v);
         }
       }
     }
