@@ -34,12 +34,21 @@ struct Sorted {
   uint2* order;      // [tokens] id and token, by bucket, id, token
   uint2* rows;       // [vocab] first place of the row's tokens in that order, and how many
   uint32_t* total;   // places in use
-  uint32_t* ticks;   // [tiles][slices] parts that are done of the row that begins in a tile and goes on
-  float* sums;       // [tiles][2][pitch] sums of parts: of a row that began in an earlier tile, and of one that
-                     // goes on in the next
+  // Of rows in several tiles: a part's slot is 2 * tile for a row that began in an earlier tile, and one
+  // more for a row that goes on in the next.  kGroup parts are a group, at its first part's slot.
+  float* sums;       // [slots][pitch] a part's sum, then its group's
+  uint32_t* ticks;   // [slots][slices] parts of a group that are done
+  uint32_t* groups;  // [slots][slices] groups of a row that are done, at its first part's slot
   uint32_t buckets, bucket_bits, tile_bits, tiles, slices;
   uint64_t pitch;
 };
+
+constexpr uint32_t kGroup = 8;  // parts that one warp adds up, one after another
+
+// The slot of part p of a row that begins in tile `from`.
+__device__ __forceinline__ uint64_t slot_of(uint32_t from, uint32_t p) {
+  return 2 * ((uint64_t)from + p) + (p ? 0 : 1);
+}
 
 uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
@@ -69,7 +78,8 @@ uint64_t layout(Sorted* w, void* p, uint64_t tokens, uint64_t vocab, uint64_t di
   w->sums = reinterpret_cast<float*>(take((uint64_t)w->tiles * 2 * w->pitch * 4));
   w->order = reinterpret_cast<uint2*>(take(tokens * 8));
   w->rows = reinterpret_cast<uint2*>(take(vocab * 8));
-  w->ticks = reinterpret_cast<uint32_t*>(take((uint64_t)w->tiles * slices * 4));
+  w->ticks = reinterpret_cast<uint32_t*>(take((uint64_t)w->tiles * 2 * slices * 4));
+  w->groups = reinterpret_cast<uint32_t*>(take((uint64_t)w->tiles * 2 * slices * 4));
   w->total = reinterpret_cast<uint32_t*>(take(4));
   return (uint64_t)(at - static_cast<char*>(p));
 }
@@ -154,9 +164,12 @@ __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids 
     const uint32_t n = k ? n1 : n0, start = k ? at + n0 : at;
     if (id >= vocab) continue;
     w.rows[id] = make_uint2(start, n);
-    const uint32_t tile = start >> w.tile_bits;
-    if (n && (start + n - 1) >> w.tile_bits != tile)
-      for (uint32_t q = 0; q < w.slices; ++q) w.ticks[(uint64_t)tile * w.slices + q] = 0;
+    if (n == 0) continue;
+    const uint32_t tile = start >> w.tile_bits, parts = ((start + n - 1) >> w.tile_bits) - tile + 1;
+    if (parts == 1) continue;
+    for (uint32_t q = 0; q < w.slices; ++q) w.groups[slot_of(tile, 0) * w.slices + q] = 0;
+    for (uint32_t p = 0; p < parts; p += kGroup)
+      for (uint32_t q = 0; q < w.slices; ++q) w.ticks[slot_of(tile, p) * w.slices + q] = 0;
   }
   if (b == 0 && t == 0) *w.total = valid_all;
   if (all == 0) return;
@@ -196,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids 
 
 #ifndef CR_EB_BYTES
 #define CR_EB_BYTES 128
-#define CR_EB_OCC 4
+#define CR_EB_OCC 3
 #endif
 
 // Table row `id`: base + scale * acc.
@@ -216,6 +229,45 @@ __device__ __forceinline__ void finish(const EmbedBackArgs& a, uint32_t id, uint
     for (int e = 0; e < vals; ++e) acc[e] += base.value(e);
   }
   st_place<OT, MODE>(out, at, acc);
+}
+
+// acc at a slot of the workspace: a lane's values 16 bytes each, next to its neighbours'.
+template <int MODE>
+__device__ __forceinline__ void put_sum(const Sorted& w, uint64_t slot, uint32_t col, int lane,
+                                        const float* acc) {
+  float* to = w.sums + slot * w.pitch + col + 4 * lane;
+#pragma unroll
+  for (int e = 0; e < place_vals(MODE); e += 4)
+    __stcg(reinterpret_cast<float4*>(to + 32 * e), make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]));
+}
+
+// Whether this warp, whose sum is written, is the last of n to come here; if so, it sees the others'.
+__device__ __forceinline__ bool last_of(uint32_t* tick, uint32_t n, int lane) {
+  __threadfence();
+  __syncwarp();
+  uint32_t before = 0;
+  if (lane == 0) before = atomicAdd(tick, 1u);
+  const bool last = __shfl_sync(~0u, before, 0) == n - 1;
+  if (last) __threadfence();
+  return last;
+}
+
+// acc = the sums of parts p, p + step, ... below `end`, in order.
+template <int MODE>
+__device__ __forceinline__ void get_sums(const Sorted& w, uint32_t from, uint32_t p, uint32_t end,
+                                         uint32_t step, uint32_t col, int lane, float* acc) {
+  constexpr int vals = place_vals(MODE);
+#pragma unroll
+  for (int e = 0; e < vals; ++e) acc[e] = 0.0f;
+#pragma unroll 2
+  for (; p < end; p += step) {
+    const float* at = w.sums + slot_of(from, p) * w.pitch + col + 4 * lane;
+#pragma unroll
+    for (int e = 0; e < vals; e += 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(at + 32 * e));
+      acc[e] += v.x, acc[e + 1] += v.y, acc[e + 2] += v.z, acc[e + 3] += v.w;
+    }
+  }
 }
 
 constexpr uint32_t kFree = 16;  // chunks of the table that a warp looks at for rows without tokens
@@ -310,34 +362,21 @@ __global__ void __launch_bounds__(kBlock, CR_EB_OCC) k_sum(const __grid_constant
     if (!ends && next == id) continue;
     bool whole = true;
     if (joined || goes_on) {
-      // a lane's sums, 16 bytes apart
-      float* sums = w.sums + col + 4 * lane;
-      float* mine = sums + (2 * (uint64_t)tile + (joined ? 0 : 1)) * w.pitch;
-#pragma unroll
-      for (int e = 0; e < vals; e += 4)
-        *reinterpret_cast<float4*>(mine + 32 * e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-      __threadfence();
-      __syncwarp();
       const uint2 row = w.rows[id];
       const uint32_t from = row.x >> w.tile_bits, parts = ((row.x + row.y - 1) >> w.tile_bits) - from + 1;
-      uint32_t done = 0;
-      if (lane == 0) done = atomicAdd(&w.ticks[(uint64_t)from * w.slices + slice], 1u);
-      whole = __shfl_sync(~0u, done, 0) == parts - 1;
-      joined = false;
-      if (whole) {  // the others' sums are there
-        __threadfence();
-#pragma unroll
-        for (int e = 0; e < vals; ++e) acc[e] = 0.0f;
-#pragma unroll 1
-        for (uint32_t p = 0; p < parts; ++p) {
-          const float* part = sums + (2 * (uint64_t)(from + p) + (p ? 0 : 1)) * w.pitch;
-#pragma unroll
-          for (int e = 0; e < vals; e += 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + 32 * e));
-            acc[e] += v.x, acc[e + 1] += v.y, acc[e + 2] += v.z, acc[e + 3] += v.w;
-          }
+      const uint32_t part = tile - from, first = part / kGroup * kGroup;
+      // parts to groups, groups to the row
+      put_sum<MODE>(w, slot_of(from, part), col, lane, acc);
+      whole = last_of(&w.ticks[slot_of(from, first) * w.slices + slice], min(kGroup, parts - first), lane);
+      if (whole) {
+        get_sums<MODE>(w, from, first, min(parts, first + kGroup), 1, col, lane, acc);
+        if (parts > kGroup) {
+          put_sum<MODE>(w, slot_of(from, first), col, lane, acc);
+          whole = last_of(&w.groups[slot_of(from, 0) * w.slices + slice], (parts + kGroup - 1) / kGroup, lane);
+          if (whole) get_sums<MODE>(w, from, 0, parts, kGroup, col, lane, acc);
         }
       }
+      joined = false;
     }
     if (whole) finish<OT, MODE>(a, id, col, lane, acc);
 #pragma unroll

@@ -9,13 +9,14 @@
 // first (a product more than one fma with m scaled) because a row masked with the type's lowest
 // value has no scaled m.
 //
-// Most likely tokens.  A thread also keeps its columns' largest logit, which the sum
-// needs anyway.  Of 64 groups of four threads (or 32 lanes) the top-th largest maximum
-// is a lower bound of the top-th largest logit, so only columns at or above it can be
-// wanted, and only threads whose maximum reaches it can hold one: these columns are
-// looked at again (from L2) and those that reach the bound ranked by counting.  Where
-// too many reach it (equal logits: a masked row, a row of zeros), the bound is taken
-// once more over (logit, column) pairs, which are all different.
+// Most likely tokens.  Of its lanes' largest logits so far, which the sums need anyway, each warp notes
+// the share-th largest.  Where `need` warps' notes are at or above a value, and share * need is at least the
+// wanted number, so are as many logits: one below that value is not wanted.  The vectors of a step
+// of a thread whose largest may be wanted go to a list, few, and are read again at the end (from L2): what
+// is at or above the last such value is ranked by counting.  (Testing every logit on the way instead took
+// 283 us for 8192 x 32000 against 81 without: that much code runs out of the instruction cache.)  Where a
+// list overflows (equal logits: a masked row, a row of zeros) or NaN leaves it short, the row is
+// looked at again with a bound over (logit, column) pairs, which are all different.
 //
 // A row is read by a warp, by a block, or by a cluster of blocks where rows are few.
 #include <cooperative_groups.h>
@@ -31,17 +32,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-#ifndef CR_LOGP_FILL
-#define CR_LOGP_FILL 4
-#define CR_LOGP_ROWS 4
-#define CR_LOGP_TEAM 128
-#endif
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kFar = -1e30f;  // 2^kFar = 0
-#ifndef CR_LOGP_UNROLL
-#define CR_LOGP_UNROLL 4
-#endif
-constexpr int kUnroll = CR_LOGP_UNROLL;      // 16-byte vectors of a thread in flight
+constexpr int kUnroll = 8;        // 16-byte vectors of a thread in flight
+constexpr int kThreadsPerSm = 1024;  // at 64 registers
 constexpr uint32_t kMostParts = 8;  // blocks of a cluster at most
 
 // Sums over some columns of a row: see above.  s = 0: none, or all -infinity.
@@ -90,11 +84,12 @@ __device__ __forceinline__ uint64_t pair_key(float x, uint32_t col) {
   return (uint64_t)order_key(x) << 32 | (0xffffffffu - col);
 }
 
-// Part of a row: its vectors (16-byte aligned), and the single columns before and
-// behind them, fewer than a vector each.
+// Part of a row: its vectors, and the single columns before and behind them, fewer than 32 each.
+// Vectors start where the row passes kAlign bytes, so that a warp's 512 bytes are whole sectors.
 template <int DT>
 struct RowPart {
   static constexpr int kVec = DT == CR_BF16 ? 8 : 4;  // columns of a vector
+  static constexpr uintptr_t kAlign = 32 * 16 / kVec;   // 32 columns
   const char* p;
   uint32_t begin;  // its first column in the row
   uint32_t head, vectors, tail;
@@ -102,7 +97,7 @@ struct RowPart {
   __device__ __forceinline__ RowPart(const void* row, uint32_t b, uint32_t n) : begin(b) {
     constexpr uint32_t es = 16 / kVec;
     p = static_cast<const char*>(row) + (uint64_t)b * es;
-    head = (uint32_t)(-reinterpret_cast<intptr_t>(p) & 15) / es;
+    head = (uint32_t)(-reinterpret_cast<intptr_t>(p) & (kAlign - 1)) / es;
     if (head > n) head = n;
     vectors = (n - head) / kVec;
     tail = n - head - vectors * kVec;
@@ -180,6 +175,11 @@ __device__ __forceinline__ float2 extremes(const uint4 (&v)[N]) {
   }
 }
 
+template <int DT, int N>
+__device__ __forceinline__ float largest(const uint4 (&v)[N]) {
+  return extremes<DT>(v).x;
+}
+
 // Two floats in a 64-bit register, and the operations on both at once.
 using Two = unsigned long long;
 __device__ __forceinline__ Two two(float a, float b) {
@@ -246,13 +246,14 @@ struct Running {
         add<FAR>(two(RowPart<DT>::value(v[i], e), RowPart<DT>::value(v[i], e + 1)), minus, cc);
   }
   template <int DT, int N>
-  __device__ __forceinline__ void take(const uint4 (&v)[N], float c) {
+  __device__ __forceinline__ float take(const uint4 (&v)[N], float c) {  // returns their largest
     const float2 ends = extremes<DT>(v);
     reach(ends.x, c);
     if ((ends.y - reference()) * c >= kFar)
       add_vectors<DT, false>(v, c);
     else
       add_vectors<DT, true>(v, c);
+    return ends.x;
   }
   __device__ __forceinline__ Stat stat() const {
     const float2 a = both(s), b = both(w);
@@ -264,13 +265,20 @@ struct Running {
 template <int TEAM>
 struct TopShared {
   static constexpr int kGroups = TEAM == 32 ? 32 : 64;
-  static constexpr int kCands = TEAM == 32 ? 256 : 1024;
+  static constexpr int kCands = TEAM == 32 ? 512 : 1024;
   alignas(16) uint64_t keys[kGroups];
   alignas(16) uint64_t cand[kCands];
   uint64_t best[CR_MAX_TOP];
   uint64_t bound;
-  uint32_t count, threads;
+  alignas(16) float notes[TEAM / 32];
+  uint32_t count, threads, steps;
+  uint32_t step[kCands];  // TEAM * the step + the thread
   uint16_t thread[TEAM];
+
+  __device__ __forceinline__ void push(uint64_t pair) {
+    const uint32_t slot = atomicAdd(&count, 1u);
+    if (slot < kCands) cand[slot] = pair;
+  }
 };
 
 template <int TEAM>
@@ -281,48 +289,67 @@ __device__ __forceinline__ void team_sync() {
     __syncthreads();
 }
 
-// sh.bound = the k-th largest of the groups' largest keys (KEY: 32 bits, a pair's upper
-// half, or 64).
-template <int TEAM, typename KEY>
-__device__ __forceinline__ void find_bound(TopShared<TEAM>& sh, KEY key, int k, int t) {
-  constexpr int groups = TopShared<TEAM>::kGroups, per = TEAM / groups, wide = 16 / sizeof(KEY);
-  KEY* keys = reinterpret_cast<KEY*>(sh.keys);
+// A value that at least k of the warp's are not below (k up to 32): the k-th largest where all
+// differ.  NaN counts as -infinity.
+__device__ __forceinline__ float warp_bound(float x, int k) {
+  uint32_t key = order_key(x), most = 0;
+  for (int i = 0; i < k;) {
+    most = __reduce_max_sync(~0u, key);
+    i += __popc(__ballot_sync(~0u, key == most));
+    if (key == most) key = 0;
+  }
+  return most > 1 ? key_logit(most) : -kInf;
+}
+
+// A value that at least share * need of the team's logits are not below: the need-th largest note.
+template <int TEAM>
+__device__ __forceinline__ float least_wanted(const TopShared<TEAM>& sh, int need) {
+  constexpr int warps = TEAM / 32;
+  if constexpr (warps == 1) return sh.notes[0];
+  const volatile float* notes = sh.notes;
+  const int lane = threadIdx.x & 31;
+  const float mine = notes[lane % warps];
+  int rank = 0;  // above it, or equal and of an earlier warp
+#pragma unroll
+  for (int w = 0; w < warps; ++w) {
+    const float other = __shfl_sync(~0u, mine, w);
+    rank += other > mine || (other == mine && w < lane % warps);
+  }
+  return __shfl_sync(~0u, mine, __ffs(__ballot_sync(~0u, rank == need - 1)) - 1);
+}
+
+// sh.bound = the k-th largest of the groups' largest pairs; no candidates yet.
+template <int TEAM>
+__device__ __forceinline__ void find_bound(TopShared<TEAM>& sh, uint64_t key, int k, int t) {
+  constexpr int groups = TopShared<TEAM>::kGroups, per = TEAM / groups;
 #pragma unroll
   for (int o = 1; o < per; o <<= 1) {
-    const KEY other = __shfl_xor_sync(~0u, key, o);
+    const uint64_t other = __shfl_xor_sync(~0u, key, o);
     key = other > key ? other : key;
   }
-  if (t % per == 0) keys[t / per] = key;
+  if (t % per == 0) sh.keys[t / per] = key;
   if (t == 0) sh.count = sh.threads = 0;
   team_sync<TEAM>();
   if (t < groups) {
-    const KEY mine = keys[t];
+    const uint64_t mine = sh.keys[t];
     int rank = 0;
-#pragma unroll 4
-    for (int i = 0; i < groups; i += wide) {
-      KEY other[wide];
-      *reinterpret_cast<uint4*>(other) = *reinterpret_cast<const uint4*>(keys + i);
-#pragma unroll
-      for (int e = 0; e < wide; ++e) rank += other[e] > mine || (other[e] == mine && i + e < t);
-    }
-    if (rank == k - 1) sh.bound = sizeof(KEY) == 4 ? (uint64_t)mine << 32 : (uint64_t)mine;
+    for (int i = 0; i < groups; ++i) rank += sh.keys[i] > mine || (sh.keys[i] == mine && i < t);
+    if (rank == k - 1) sh.bound = mine;
   }
   team_sync<TEAM>();
 }
 
-// sh.cand = the pairs at or above sh.bound, of the threads whose key reaches it.
+// sh.cand = the pairs at or above `bound`, of the threads whose key reaches it.
 template <int DT, int TEAM>
-__device__ __forceinline__ void collect(TopShared<TEAM>& sh, const RowPart<DT>& row, uint64_t key,
-                                        int t) {
-  const uint64_t bound = sh.bound;
+__device__ __forceinline__ void collect(TopShared<TEAM>& sh, const RowPart<DT>& row, uint64_t bound,
+                                        uint64_t key, int t) {
   if (key >= bound) sh.thread[atomicAdd(&sh.threads, 1u)] = (uint16_t)t;
   team_sync<TEAM>();
   const uint32_t n = sh.threads;
   const auto look = [&](uint32_t col, float x) {
     const uint64_t pair = pair_key(x, row.begin + col);
     if (pair < bound) return;
-    const uint32_t slot = atomicAdd(&sh.count, 1u);
-    if (slot < TopShared<TEAM>::kCands) sh.cand[slot] = pair;
+    sh.push(pair);
   };
   // Eight lanes take a thread's columns, so that a step of the team usually reads all there are.
   const int sub = t % 8;
@@ -349,112 +376,143 @@ __device__ __forceinline__ void collect(TopShared<TEAM>& sh, const RowPart<DT>& 
   team_sync<TEAM>();
 }
 
-// How many of the n pairs are above `mine`; where n is odd, pairs[n] is 0.
+// How many of the n pairs are above `mine`.
 __device__ __forceinline__ int rank_of(const uint64_t* pairs, int n, uint64_t mine) {
-  int rank = 0;
+  int rank = 0, j = 0;
 #pragma unroll 4
-  for (int j = 0; j < n; j += 2) {
+  for (; j + 1 < n; j += 2) {
     const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(pairs + j);
     rank += (v.x > mine) + (v.y > mine);
   }
+  if (j < n) rank += pairs[j] > mine;
   return rank;
 }
 
-// sh.best[0 .. k - 1] = the k largest pairs of the row part, which has at least k columns,
-// in falling order.  `most`: the thread's largest logit.
-template <int DT, int TEAM>
-__device__ __forceinline__ void find_top(TopShared<TEAM>& sh, const RowPart<DT>& row, float most,
-                                         bool any, int k, int t) {
+// put(i, pair) for the k largest pairs of the row part, which has at least k columns: i-th in
+// falling order.  sh.cand holds sh.count pairs, or lacks some.
+template <int DT, int TEAM, typename Put>
+__device__ __forceinline__ void find_top(TopShared<TEAM>& sh, const RowPart<DT>& row, int k, int t,
+                                         Put put) {
   constexpr uint32_t cands = TopShared<TEAM>::kCands;
-  const uint32_t upper = any ? order_key(most) : 0;
-  find_bound<TEAM, uint32_t>(sh, upper, k, t);
-  collect<DT, TEAM>(sh, row, any ? (uint64_t)upper << 32 | 0xffffffffu : 0, t);
-  if (sh.count > cands) {
+  if (sh.count > cands || sh.count < k) {
     uint64_t key = 0;
     row.each_of(t, TEAM, [&](uint32_t col, float x) {
       const uint64_t pair = pair_key(x, row.begin + col);
       key = pair > key ? pair : key;
     });
     team_sync<TEAM>();  // sh.count has been read
-    find_bound<TEAM, uint64_t>(sh, key, k, t);
-    collect<DT, TEAM>(sh, row, key, t);
+    find_bound<TEAM>(sh, key, k, t);
+    collect<DT, TEAM>(sh, row, sh.bound, key, t);
   }
   const uint32_t n = sh.count;
   if (n <= cands) {
-    if (t == 0 && n % 2) sh.cand[n] = 0;  // n is even where the array is full
-    team_sync<TEAM>();
     for (uint32_t i = t; i < n; i += TEAM) {
       const uint64_t mine = sh.cand[i];
       const int rank = rank_of(sh.cand, n, mine);
-      if (rank < k) sh.best[rank] = mine;
+      if (rank < k) put(rank, mine);
     }
-  } else {
-    // the wanted pairs crowd in few threads' columns: one after another
-    uint64_t last = ~0ull;
-    for (int i = 0; i < k; ++i) {
-      uint64_t mine = 0;
-      row.each_of(t, TEAM, [&](uint32_t col, float x) {
-        const uint64_t pair = pair_key(x, row.begin + col);
-        if (pair < last && pair > mine) mine = pair;
-      });
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const uint64_t other = __shfl_xor_sync(~0u, mine, o);
-        mine = other > mine ? other : mine;
-      }
-      team_sync<TEAM>();
-      if (t % 32 == 0) sh.keys[t / 32] = mine;
-      team_sync<TEAM>();
-      for (int w = 0; w < TEAM / 32; ++w) mine = sh.keys[w] > mine ? sh.keys[w] : mine;
-      if (t == 0) sh.best[i] = mine;
-      last = mine;
-    }
+    return;
   }
-  team_sync<TEAM>();
+  // the wanted pairs crowd in few threads' columns: one after another
+  uint64_t last = ~0ull;
+  for (int i = 0; i < k; ++i) {
+    uint64_t mine = 0;
+    row.each_of(t, TEAM, [&](uint32_t col, float x) {
+      const uint64_t pair = pair_key(x, row.begin + col);
+      if (pair < last && pair > mine) mine = pair;
+    });
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(~0u, mine, o);
+      mine = other > mine ? other : mine;
+    }
+    team_sync<TEAM>();
+    if (t % 32 == 0) sh.keys[t / 32] = mine;
+    team_sync<TEAM>();
+    for (int w = 0; w < TEAM / 32; ++w) mine = sh.keys[w] > mine ? sh.keys[w] : mine;
+    if (t == 0) put(i, mine);
+    last = mine;
+  }
 }
 
-// Sums and most likely tokens of a part of a row, by the threads of a team.  The first
-// warp returns the sums.  `stats`: TEAM / 32 of them in shared memory.
+// Sums of a part of a row, by the threads of a team, for all of them; find_top may follow where
+// TOP.  `stats`: TEAM / 32 of them in shared memory.
 template <int DT, int TEAM, bool TOP>
 __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k, int t,
                                           TopShared<TEAM>* sh, Stat* stats) {
   using Part = RowPart<DT>;
+  constexpr int unroll = kUnroll, warps = TEAM / 32;
+  constexpr uint64_t step = (uint64_t)TEAM * unroll;
   Running run;
-  constexpr uint64_t step = (uint64_t)TEAM * kUnroll;
-  const auto load = [&](uint4 (&v)[kUnroll], uint64_t j) {
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i)
-      v[i] = j + i * TEAM < row.vectors ? row.vec((uint32_t)(j + i * TEAM)) : Part::none();
+  // twice the average share, of which half the warps are needed: the better half
+  const int share = min(k, (2 * k + warps - 1) / warps), need = TOP ? (k + share - 1) / share : 0;
+  float least = -kInf;
+  const auto note = [&] {
+    const float bound = warp_bound(run.m, share);
+    if (t % 32 == 0) *const_cast<volatile float*>(&sh->notes[t / 32]) = bound;
   };
-  // the next vectors are on their way while these are added
-  uint4 u[kUnroll], v[kUnroll];
-  load(u, t);
-  for (uint64_t j = t; j < row.vectors; j += 2 * step) {
-    load(v, j + step);
-    run.take<DT>(u, c);
-    if (j + step >= row.vectors) break;
-    load(u, j + 2 * step);
-    run.take<DT>(v, c);
+  // notes after 1, 2, 4, ... steps: all warps take as many
+  const uint32_t steps = (uint32_t)max((uint64_t)1, (row.vectors + step - 1) / step);
+  for (uint32_t b = 0; b < steps; ++b) {
+    const uint64_t j = b * step + t;
+    uint4 v[unroll];
+#pragma unroll
+    for (int i = 0; i < unroll; ++i)
+      v[i] = j + i * TEAM < row.vectors ? row.vec((uint32_t)(j + i * TEAM)) : Part::none();
+    const float most = run.take<DT>(v, c);
+    if constexpr (TOP) {
+      if ((b & (b + 1)) == 0) {
+        note();
+        if (b == 0) {
+          if (t == 0) sh->count = sh->threads = sh->steps = 0;
+          team_sync<TEAM>();
+        } else {
+          __syncwarp();
+        }
+        least = least_wanted(*sh, need);
+      }
+      if (most >= least) {
+        const uint32_t slot = atomicAdd(&sh->steps, 1u);
+        if (slot < TopShared<TEAM>::kCands) sh->step[slot] = b * TEAM + t;
+      }
+    }
   }
-  if ((uint32_t)t < row.head || (uint32_t)t < row.tail) {
-    const float x = (uint32_t)t < row.head ? row.one(t) : -kInf;
-    const float y = (uint32_t)t < row.tail ? row.one(row.head + row.vectors * Part::kVec + t) : -kInf;
+  const bool single = (uint32_t)t < row.head, behind = (uint32_t)t < row.tail;
+  const uint32_t col = row.head + row.vectors * Part::kVec + t;
+  const float x = single ? row.one(t) : -kInf, y = behind ? row.one(col) : -kInf;
+  if (single || behind) {
     run.reach(fmaxf(x, y), c);
     const float r = run.reference();
     run.add<true>(two(x, y), two(-r, -r), two(c, c));
   }
   Stat all = lanes_merge<32>(run.stat(), c);
+  if constexpr (TOP) note();
   if constexpr (TEAM > 32) {
     if (t % 32 == 0) stats[t / 32] = all;
     __syncthreads();
-    if (t < 32) all = lanes_merge<TEAM / 32>(stats[t % (TEAM / 32)], c);
+    all = lanes_merge<warps>(stats[t % warps], c);
+  } else if constexpr (TOP) {
+    __syncwarp();
   }
   if constexpr (TOP) {
-    const bool any = (uint32_t)t < row.vectors || (uint32_t)t < row.head || (uint32_t)t < row.tail;
-    // a largest logit of -infinity may stand for NaN alone, which is below it
-    bool has = run.m != -kInf;
-    if (any && !has) row.each_of(t, TEAM, [&](uint32_t, float x) { has = has || x == -kInf; });
-    find_top<DT, TEAM>(*sh, row, has ? run.m : __int_as_float(0x7fc00000), any, k, t);
+    least = least_wanted(*sh, need);
+    if (single && x >= least) sh->push(pair_key(x, row.begin + t));
+    if (behind && y >= least) sh->push(pair_key(y, row.begin + col));
+    const uint32_t n = min(sh->steps, (uint32_t)TopShared<TEAM>::kCands);
+    if (t == 0 && sh->steps > n) sh->count = TopShared<TEAM>::kCands + 1;
+    for (uint32_t i = t; i < n * unroll; i += TEAM) {
+      const uint32_t at = sh->step[i / unroll];
+      const uint64_t vec = at / TEAM * step + at % TEAM + i % unroll * TEAM;
+      if (vec >= row.vectors) continue;
+      const uint4 one[1] = {row.vec((uint32_t)vec)};
+      if (!(largest<DT>(one) >= least)) continue;
+#pragma unroll
+      for (int e = 0; e < Part::kVec; ++e) {
+        const float z = Part::value(one[0], e);
+        if (z >= least) sh->push(pair_key(z, row.begin + row.head + (uint32_t)vec * Part::kVec + e));
+      }
+    }
+    team_sync<TEAM>();
   }
   return all;
 }
@@ -505,7 +563,8 @@ __global__ void __launch_bounds__(kBlock) k_logp_warp(const __grid_constant__ Lo
     const Stat v = read_part<DT, 32, TOP>(part, c, a.top, lane, sh, nullptr);
     if (lane == 0) write_row<DT>(a, row, v, logits);
     if constexpr (TOP) {
-      if (lane < a.top) write_top(a, row, lane, sh->best[lane], v);
+      find_top<DT, 32>(*sh, part, a.top, lane,
+                       [&](int i, uint64_t pair) { write_top(a, row, i, pair, v); });
       __syncwarp();
     }
   }
@@ -513,7 +572,7 @@ __global__ void __launch_bounds__(kBlock) k_logp_warp(const __grid_constant__ Lo
 
 // A block of TEAM threads a row, or a cluster a row (gridDim.x a multiple of the cluster).
 template <int DT, int TEAM, bool TOP>
-__global__ void __launch_bounds__(TEAM) k_logp_block(const __grid_constant__ LogProbArgs a,
+__global__ void __launch_bounds__(TEAM, kThreadsPerSm / TEAM) k_logp_block(const __grid_constant__ LogProbArgs a,
                                                      uint32_t per) {
   __shared__ TopShared<TOP ? TEAM : 32> top[1];
   __shared__ Stat stats[TEAM / 32];
@@ -530,35 +589,36 @@ __global__ void __launch_bounds__(TEAM) k_logp_block(const __grid_constant__ Log
     TopShared<TEAM>* sh = nullptr;
     if constexpr (TOP) sh = top;
     Stat v = read_part<DT, TEAM, TOP>(part, c, a.top, t, sh, stats);
-    if (parts > 1) {
-      if (t == 0) sums = v;
-      cluster.sync();
-      if (part_no == 0 && t < 32)
-        v = lanes_merge<kMostParts>(t % kMostParts < parts ? *cluster.map_shared_rank(&sums, t % kMostParts)
-                                                           : Stat{-kInf, 0.0f, 0.0f}, c);
+    if (parts == 1) {
+      if (t == 0) write_row<DT>(a, row, v, logits);
+      if constexpr (TOP)
+        find_top<DT, TEAM>(*sh, part, a.top, t,
+                           [&](int i, uint64_t pair) { write_top(a, row, i, pair, v); });
+      __syncthreads();
+      continue;
     }
+    if (t == 0) sums = v;
+    if constexpr (TOP)
+      find_top<DT, TEAM>(*sh, part, a.top, t, [&](int i, uint64_t pair) { sh->best[i] = pair; });
+    cluster.sync();
     if (part_no == 0) {
+      v = lanes_merge<kMostParts>(t % kMostParts < parts ? *cluster.map_shared_rank(&sums, t % kMostParts)
+                                                         : Stat{-kInf, 0.0f, 0.0f}, c);
       if (t == 0) write_row<DT>(a, row, v, logits);
       if constexpr (TOP) {
-        if (t == 0) sums = v;
+        // rank the parts' best among each other
         const int n = (int)parts * a.top;
-        uint64_t mine = 0;
-        if (parts > 1)  // rank the parts' best among each other
-          for (int i = t; i < n; i += TEAM)
-            top->cand[i] = cluster.map_shared_rank(top, i / a.top)->best[i % a.top];
+        for (int i = t; i < n; i += TEAM)
+          top->cand[i] = cluster.map_shared_rank(top, i / a.top)->best[i % a.top];
         __syncthreads();
-        v = sums;
         for (int i = t; i < n; i += TEAM) {
-          mine = parts > 1 ? top->cand[i] : top->best[i];
-          const int rank = parts > 1 ? rank_of(top->cand, n, mine) : i;  // parts is even
+          const uint64_t mine = top->cand[i];
+          const int rank = rank_of(top->cand, n, mine);
           if (rank < a.top) write_top(a, row, rank, mine, v);
         }
       }
     }
-    if (parts > 1)
-      cluster.sync();
-    else
-      __syncthreads();
+    cluster.sync();
   }
 }
 
@@ -585,15 +645,20 @@ cudaError_t run(const LogProbArgs& a, cudaStream_t s) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  if (a.vocab <= 2048 && a.rows >= (uint64_t)sms)
+  if (a.vocab <= 2048)
     return launch_pdl(k_logp_warp<DT, TOP>, dim3(flat_grid(a.rows * 32)), kBlock, s, a);
   // Parts of a row: while rows are too few to fill the SMs, and parts keep two vectors a
   // thread (and more columns than are wanted of them).
   uint32_t parts = 1;
-  while (parts < kMostParts && a.rows * parts < CR_LOGP_FILL * (uint64_t)sms &&
+  while (parts < kMostParts && a.rows * parts < 4 * (uint64_t)sms &&
          a.vocab / (2 * parts) >= 2 * kBlock * RowPart<DT>::kVec)
     parts *= 2;
-  if (parts == 1 && a.rows >= CR_LOGP_ROWS * (uint64_t)sms) return run_block<DT, CR_LOGP_TEAM, TOP>(a, 1, s);
+  // Many short rows: fewer threads each, so that a row's end costs less of it (8192 x 32000 bf16 81.0 us
+  // with 128 threads, 87.8 with 256; 1531 x 50257 fp32, top 8, 67.8 and 62.4: rows of 200 KB, of which more
+  // at a time do not fit in L2 until their second look).
+  constexpr uint64_t kShort = 128 << 10;
+  if (a.rows >= 4 * (uint64_t)sms && a.vocab * (16 / RowPart<DT>::kVec) <= kShort)
+    return run_block<DT, 128, TOP>(a, 1, s);
   return run_block<DT, kBlock, TOP>(a, parts, s);
 }
 

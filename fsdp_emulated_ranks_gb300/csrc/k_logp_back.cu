@@ -16,7 +16,7 @@ namespace {
 
 #ifndef CR_LB_AHEAD
 #define CR_LB_AHEAD 2
-#define CR_LB_OCC 4
+#define CR_LB_OCC 5
 #endif
 constexpr int kAhead = CR_LB_AHEAD;  // chunks of a warp in flight
 
