@@ -14,12 +14,6 @@ namespace cr {
 
 namespace {
 
-#ifndef CR_D_AHEAD
-#define CR_D_AHEAD 1
-#define CR_D_OCC 5
-#endif
-constexpr int kAhead = CR_D_AHEAD;  // chunks of a warp in flight
-
 struct Key {
   uint32_t k0, k1, off0, off1;
 };
@@ -52,15 +46,10 @@ __device__ __forceinline__ uint32_t half_of(const uint4& w, int i) {
   return i & 1 ? x : x << 16;
 }
 
-template <int DT, int MODE>
-struct Pair {
-  Loaded<DT, MODE> x, residual;
-};
-
 // A lane's columns in modes 0 to 2 are ffn_internal.cuh's.  Mode kSpan: spans without a
 // lead, so that a lane's columns are one group; only the stores are shifted.
 template <int DT, int MODE, bool RES>
-__global__ void __launch_bounds__(kBlock, CR_D_OCC) k_dropout(const __grid_constant__ DropoutArgs a,
+__global__ void __launch_bounds__(kBlock, DT == CR_F32 && MODE ? 4 : 6) k_dropout(const __grid_constant__ DropoutArgs a,
                                                     const __grid_constant__ ChunkRange r) {
   constexpr int vals = place_vals(MODE);
   __shared__ __align__(16) uint16_t turned[MODE == 0 ? kBlock / 32 : 1][MODE == 0 ? 256 : 8];
@@ -71,56 +60,44 @@ __global__ void __launch_bounds__(kBlock, CR_D_OCC) k_dropout(const __grid_const
   const uint32_t limit = a.limit << 16;
   const uint64_t stride = (uint64_t)gridDim.x * (kBlock / 32);
   for (uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5); k < r.chunks;
-       k += kAhead * stride) {
-    Loaded<DT, MODE> x[kAhead], res[RES ? kAhead : 1];
-    uint64_t row[kAhead];
-    uint32_t base[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const uint64_t c = k + j * stride;
-      if (c >= r.chunks) break;
-      row[j] = fastdiv_div(r.per_row, c);
-      base[j] = (uint32_t)(c - row[j] * r.per_row.d) * place_cols(MODE);
-      const Place<MODE> at(base[j], a.cols, lane, nullptr);
-      x[j].load(row_at<DT>(a.x, row[j]), at);
-      if constexpr (RES) res[j].load(row_at<DT>(a.residual, row[j]), at);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (k + j * stride >= r.chunks) break;
-      const Place<MODE> at(base[j], a.cols, lane, nullptr);
-      const uint32_t rc = a.first_row + (uint32_t)row[j];
-      float v[vals];
-      x[j].ready();
-      if constexpr (RES) res[j].ready();
-      const auto set = [&](int i, uint32_t number) {
-        const float kept = some && number >= limit ? x[j].value(i) : 0.0f;
-        if constexpr (RES)
-          v[i] = fmaf(kept, a.by, res[j].value(i));
-        else
-          v[i] = kept * a.by;
-      };
-      if constexpr (MODE == 0) {
-        uint16_t* t = turned[threadIdx.x >> 5];
-        __syncwarp();
-        reinterpret_cast<uint4*>(t)[lane] = philox(base[j] / 8 + lane, rc, key);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < vals; ++i) set(i, (uint32_t)t[32 * i + lane] << 16);
-      } else {
-#pragma unroll
-        for (int g = 0; g < vals / 8; ++g) {
-          const uint4 w = philox(base[j] / 8 + lane * (vals / 8) + g, rc, key);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) set(8 * g + i, half_of(w, i));
-        }
-      }
-      char* out = row_at<DT>(a.out, row[j]);
-      if constexpr (MODE == kSpan)
-        st_spans(out, at.span, a.cols, lane, v);
+       k += stride) {
+    const uint64_t row = fastdiv_div(r.per_row, k);
+    const uint32_t base = (uint32_t)(k - row * r.per_row.d) * place_cols(MODE);
+    const Place<MODE> at(base, a.cols, lane, nullptr);
+    Loaded<DT, MODE> x, res;
+    x.load(row_at<DT>(a.x, row), at);
+    if constexpr (RES) res.load(row_at<DT>(a.residual, row), at);
+    x.ready();
+    if constexpr (RES) res.ready();
+    const uint32_t rc = a.first_row + (uint32_t)row;
+    float v[vals];
+    const auto set = [&](int i, uint32_t number) {
+      const float kept = some && number >= limit ? x.value(i) : 0.0f;
+      if constexpr (RES)
+        v[i] = fmaf(kept, a.by, res.value(i));
       else
-        st_chunk<DT, MODE>(out, base[j], a.cols, lane, v);
+        v[i] = kept * a.by;
+    };
+    if constexpr (MODE == 0) {
+      uint16_t* t = turned[threadIdx.x >> 5];
+      __syncwarp();
+      reinterpret_cast<uint4*>(t)[lane] = philox(base / 8 + lane, rc, key);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < vals; ++i) set(i, (uint32_t)t[32 * i + lane] << 16);
+    } else {
+#pragma unroll
+      for (int g = 0; g < vals / 8; ++g) {
+        const uint4 w = philox(base / 8 + lane * (vals / 8) + g, rc, key);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) set(8 * g + i, half_of(w, i));
+      }
     }
+    char* out = row_at<DT>(a.out, row);
+    if constexpr (MODE == kSpan)
+      st_spans(out, at.span, a.cols, lane, v);
+    else
+      st_chunk<DT, MODE>(out, base, a.cols, lane, v);
   }
 }
 
@@ -129,7 +106,7 @@ cudaError_t run(const DropoutArgs& a, cudaStream_t s) {
   const uint64_t per_row = ((uint64_t)a.cols + place_cols(MODE) - 1) / place_cols(MODE);
   const ChunkRange r = {a.rows * per_row, fastdiv_make(per_row, a.rows * per_row)};
   return launch_pdl(a.residual.p ? k_dropout<DT, MODE, true> : k_dropout<DT, MODE, false>,
-                    chunk_grid(r, kAhead), kBlock, s, a, r);
+                    chunk_grid(r, 1), kBlock, s, a, r);
 }
 
 }  // namespace

@@ -13,10 +13,7 @@ namespace cr {
 
 namespace {
 
-#ifndef CR_E_AHEAD
-#define CR_E_AHEAD 2
-#endif
-constexpr int kAhead = CR_E_AHEAD;  // chunks of a warp in flight
+constexpr int kAhead = 2;  // chunks of a warp in flight
 
 // A warp takes kAhead chunks of a row, next to each other, which share the id.
 template <int DT, int OT, int MODE>

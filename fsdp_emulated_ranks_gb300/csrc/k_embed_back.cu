@@ -6,11 +6,14 @@
 //   1. k_group  A block takes a bucket, the ids that share their low bits.  It reads all ids
 //               twice: to count its ids' tokens (and all tokens of earlier buckets, which is where
 //               its own begin), and to put its tokens in order of id, then of token.
-//   2. k_sum    A warp takes a chunk of the columns of kTile tokens next to each other in that
+//   2. k_sum    A warp takes a chunk of the columns of a tile of tokens next to each other in that
 //               order, and adds up rows until the id changes: the work of a warp does not depend on
 //               how often an id occurs.  A table row that lies in one tile is written at once; of one in
 //               several, each warp leaves an fp32 sum in the workspace, and the last to finish adds
-//               them up in order.  Other warps write the rows that no token names.
+//               them up in order.
+//   3. k_free   Writes the rows that no token names.  It starts when k_sum's blocks have
+//               started, not when they have ended: the table's zeros fill the time in which k_sum waits for
+//               dout.
 // Reading the ids once for each bucket costs little: they stay in L2, and are 8 bytes to a row of dout's
 // thousands.  Bound by memory: dout is read and the table written once.
 #include <algorithm>
@@ -54,10 +57,7 @@ uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
 // Tokens of a tile: few where there are few tokens, so that warps are enough; more where there are
 // many, so that the sums left in the workspace (and the time to add up those of one row) stay small.
-#ifndef CR_EB_TILE
-#define CR_EB_TILE 4
-#endif
-uint32_t tile_bits(uint64_t tokens) { return tokens <= 16384 ? CR_EB_TILE : 5; }  // a lane a token
+uint32_t tile_bits(uint64_t tokens) { return tokens <= 16384 ? 4 : 5; }  // a lane a token
 
 // Everything but the addresses, then the addresses from `p` on; returns the bytes.
 uint64_t layout(Sorted* w, void* p, uint64_t tokens, uint64_t vocab, uint64_t dim, uint32_t slices) {
@@ -120,18 +120,20 @@ __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids 
   __shared__ uint32_t list[kStep];    // a step's tokens of this bucket, in order: id in the bucket, place in the step
   __shared__ uint32_t scan[32];
   __shared__ uint32_t earlier_all, valid_all;
+  // tokens of this bucket among the 32 of a warp at j, then in all such cells before
+  __shared__ __align__(16) uint32_t cells[kEach * (kThreads / 32)];
+  __shared__ uint32_t in_step;
   pdl_enter();
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t / 32, b = blockIdx.x;
   const uint32_t mask = w.buckets - 1;
   for (uint32_t k = t; k < kLocals; k += kThreads) next[k] = 0;
   if (t == 0) earlier_all = valid_all = 0;
   __syncthreads();
-  // A thread's ids are next to each other, so that its place in the list is one sum.
-  int32_t id[kEach];
+  int32_t id[kEach];  // of tokens i0 + j * kThreads + t
   const auto read = [&](uint64_t i0) {
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-      const uint64_t i = i0 + kEach * t + j;
+      const uint64_t i = i0 + j * kThreads + t;
       id[j] = i < tokens ? token_id(ids, i, vocab) : -1;
     }
   };
@@ -177,15 +179,39 @@ __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids 
   // tokens to their places
   for (uint64_t i0 = 0; i0 < tokens; i0 += kStep) {
     if (tokens > kStep) read(i0);  // else they are still there
-    uint32_t mine = 0;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) mine += id[j] >= 0 && (id[j] & mask) == b;
-    uint32_t m;
-    uint32_t slot = block_scan(mine, scan, &m);
+    for (int j = 0; j < kEach; ++j) {
+      const uint32_t at = __ballot_sync(~0u, id[j] >= 0 && (id[j] & mask) == b);
+      if (lane == 0) cells[j * (kThreads / 32) + warp] = __popc(at);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      static_assert(kEach == 8 && kThreads == 1024, "eight cells a lane");
+      uint4* mine = reinterpret_cast<uint4*>(cells) + 2 * lane;
+      uint4 p = mine[0], q = mine[1];
+      const uint32_t n = p.x + p.y + p.z + p.w + q.x + q.y + q.z + q.w;
+      uint32_t sum = n;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j)
-      if (id[j] >= 0 && (id[j] & mask) == b)
-        list[slot++] = (uint32_t)id[j] >> w.bucket_bits << kStepBits | (kEach * t + j);
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (lane == 31) in_step = sum;
+      uint32_t before = sum - n;
+      const auto turn = [&](uint32_t& c) { const uint32_t k = c; c = before, before += k; };
+      turn(p.x), turn(p.y), turn(p.z), turn(p.w), turn(q.x), turn(q.y), turn(q.z), turn(q.w);
+      mine[0] = p, mine[1] = q;
+    }
+    __syncthreads();
+    const uint32_t m = in_step;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const bool own = id[j] >= 0 && (id[j] & mask) == b;
+      const uint32_t at = __ballot_sync(~0u, own);
+      if (own)
+        list[cells[j * (kThreads / 32) + warp] + __popc(at & ((1u << lane) - 1))] =
+            (uint32_t)id[j] >> w.bucket_bits << kStepBits | (j * kThreads + t);
+    }
     __syncthreads();
     // a warp places its share of the ids, so that it alone moves their `next`
     for (uint32_t s = 0; s < m; s += 32) {
@@ -206,11 +232,6 @@ __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids 
 }
 
 // ---- 2: sum ---------------------------------------------------------------------------------
-
-#ifndef CR_EB_BYTES
-#define CR_EB_BYTES 128
-#define CR_EB_OCC 3
-#endif
 
 // Table row `id`: base + scale * acc.
 template <int OT, int MODE>
@@ -259,7 +280,7 @@ __device__ __forceinline__ void get_sums(const Sorted& w, uint32_t from, uint32_
   constexpr int vals = place_vals(MODE);
 #pragma unroll
   for (int e = 0; e < vals; ++e) acc[e] = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
   for (; p < end; p += step) {
     const float* at = w.sums + slot_of(from, p) * w.pitch + col + 4 * lane;
 #pragma unroll
@@ -270,76 +291,30 @@ __device__ __forceinline__ void get_sums(const Sorted& w, uint32_t from, uint32_
   }
 }
 
-constexpr uint32_t kFree = 16;  // chunks of the table that a warp looks at for rows without tokens
-
-// Warp n's chunks of rows without tokens: base, or zeros.
-template <int OT, int MODE>
-__device__ __forceinline__ void free_rows(const EmbedBackArgs& a, const Sorted& w, const FastDiv& slices,
-                                          uint64_t n, int lane) {
-  constexpr int vals = place_vals(MODE), ahead = 2;
-  const uint64_t first = n * kFree, all = (uint64_t)a.vocab * w.slices;
-  // a lane a chunk
-  const uint64_t mine = first + lane;
-  uint32_t id = 0, slice = 0;
-  bool is_free = false;
-  if (lane < kFree && mine < all) {
-    id = (uint32_t)fastdiv_div(slices, mine);
-    slice = (uint32_t)(mine - (uint64_t)id * w.slices);
-    is_free = w.rows[id].y == 0;
-  }
-  uint32_t left = __ballot_sync(~0u, is_free);
-  while (left) {
-    Loaded<OT, MODE> base[ahead];
-    uint32_t row[ahead], col[ahead];
-    int n_here = 0;
-#pragma unroll
-    for (int j = 0; j < ahead; ++j) {
-      if (!left) break;
-      const int at = __ffs(left) - 1;
-      left &= left - 1;
-      row[j] = __shfl_sync(~0u, id, at), col[j] = __shfl_sync(~0u, slice, at) * place_cols(MODE);
-      n_here = j + 1;
-      if (a.base.p)
-        base[j].load(row_at<OT>(a.base, row[j]),
-                     Place<MODE>(col[j], a.dim, lane, row_at<OT>(a.dtable, row[j])));
-    }
-#pragma unroll
-    for (int j = 0; j < ahead; ++j) {
-      if (j >= n_here) break;
-      char* out = row_at<OT>(a.dtable, row[j]);
-      float v[vals];
-      if (a.base.p) base[j].ready();
-#pragma unroll
-      for (int e = 0; e < vals; ++e) v[e] = a.base.p ? base[j].value(e) : 0.0f;
-      st_place<OT, MODE>(out, Place<MODE>(col[j], a.dim, lane, out), v);
-    }
-  }
-}
-
-// Warps [0, tiles * slices) take the tokens' tiles; the others the rows without tokens.
+// A warp a tile and chunk of columns.
 template <int DT, int OT, int MODE>
-__global__ void __launch_bounds__(kBlock, CR_EB_OCC) k_sum(const __grid_constant__ EmbedBackArgs a,
+__global__ void __launch_bounds__(kBlock, 2) k_sum(const __grid_constant__ EmbedBackArgs a,
                                                 const __grid_constant__ Sorted w,
                                                 const __grid_constant__ FastDiv slices) {
   constexpr int vals = place_vals(MODE);
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const uint64_t k = (uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5);
-  const uint64_t tile_warps = (uint64_t)w.tiles * w.slices;
-  if (k >= tile_warps) return free_rows<OT, MODE>(a, w, slices, k - tile_warps, lane);
   const uint64_t n = fastdiv_div(slices, k);
   const uint32_t slice = (uint32_t)(k - n * w.slices), col = slice * place_cols(MODE);
   float acc[vals];
 #pragma unroll
   for (int e = 0; e < vals; ++e) acc[e] = 0.0f;
-  const uint32_t tile = (uint32_t)n, total = *w.total, begin = tile << w.tile_bits;
+  const uint32_t tile = (uint32_t)n;
+  if (tile >= w.tiles) return;
+  const uint32_t total = *w.total, begin = tile << w.tile_bits;
   if (begin >= total) return;
   const uint32_t end = min(total, begin + (1u << w.tile_bits));
   const uint32_t after = end < total ? w.order[end].x : ~0u;
   const uint32_t before = begin ? w.order[begin - 1].x : ~0u;
   const uint2 entry = begin + lane < end ? w.order[begin + lane] : make_uint2(~0u, 0);
-  // rows in flight: as many as make CR_EB_BYTES of a lane
-  constexpr int ahead = CR_EB_BYTES / (place_vals(MODE) * (DT == CR_BF16 ? 2 : 4));
+  // rows in flight: as many as make 128 bytes of a lane
+  constexpr int ahead = 128 / (place_vals(MODE) * (DT == CR_BF16 ? 2 : 4));
   Loaded<DT, MODE> in[ahead];
   const auto load = [&](Loaded<DT, MODE>& to, uint32_t i) {
     const uint32_t id = __shfl_sync(~0u, entry.x, i & 31), token = __shfl_sync(~0u, entry.y, i & 31);
@@ -384,18 +359,77 @@ __global__ void __launch_bounds__(kBlock, CR_EB_OCC) k_sum(const __grid_constant
   }
 }
 
+// ---- 3: rows without tokens ---------------------------------------------------------------------
+
+constexpr uint32_t kFree = 16;  // chunks of the table that a warp looks at at a time
+
+// base, or zeros.  chained: launched after k_sum, whose blocks have all started, so that k_group has
+// ended; it is k_sum that one block waits for at its end, so that this launch ends after it (pdl.cuh).
+template <int OT, int MODE>
+__global__ void __launch_bounds__(kBlock) k_free(const __grid_constant__ EmbedBackArgs a,
+                                                 const __grid_constant__ Sorted w,
+                                                 const __grid_constant__ FastDiv slices, bool chained) {
+  constexpr int vals = place_vals(MODE), ahead = 4;  // of a warp in flight
+  if (!chained) pdl_wait_prerequisites();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const uint64_t all = (uint64_t)a.vocab * w.slices, stride = (uint64_t)gridDim.x * (kBlock / 32) * kFree;
+  for (uint64_t first = ((uint64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5)) * kFree; first < all;
+       first += stride) {
+    // a lane a chunk
+    const uint64_t mine = first + lane;
+    uint32_t id = 0, slice = 0;
+    bool is_free = false;
+    if (lane < kFree && mine < all) {
+      id = (uint32_t)fastdiv_div(slices, mine);
+      slice = (uint32_t)(mine - (uint64_t)id * w.slices);
+      is_free = w.rows[id].y == 0;
+    }
+    uint32_t left = __ballot_sync(~0u, is_free);
+    while (left) {
+      Loaded<OT, MODE> base[ahead];
+      uint32_t row[ahead], col[ahead];
+      int n_here = 0;
+#pragma unroll
+      for (int j = 0; j < ahead; ++j) {
+        if (!left) break;
+        const int at = __ffs(left) - 1;
+        left &= left - 1;
+        row[j] = __shfl_sync(~0u, id, at), col[j] = __shfl_sync(~0u, slice, at) * place_cols(MODE);
+        n_here = j + 1;
+        if (a.base.p)
+          base[j].load(row_at<OT>(a.base, row[j]),
+                       Place<MODE>(col[j], a.dim, lane, row_at<OT>(a.dtable, row[j])));
+      }
+#pragma unroll
+      for (int j = 0; j < ahead; ++j) {
+        if (j >= n_here) break;
+        char* out = row_at<OT>(a.dtable, row[j]);
+        float v[vals];
+        if (a.base.p) base[j].ready();
+#pragma unroll
+        for (int e = 0; e < vals; ++e) v[e] = a.base.p ? base[j].value(e) : 0.0f;
+        st_place<OT, MODE>(out, Place<MODE>(col[j], a.dim, lane, out), v);
+      }
+    }
+  }
+  if (chained && blockIdx.x == 0) pdl_wait_prerequisites();
+}
+
 template <int DT, int OT, int MODE>
 cudaError_t run(const EmbedBackArgs& a, void* workspace, cudaStream_t s) {
   Sorted w;
   layout(&w, workspace, a.tokens, a.vocab, a.dim, place_chunks(a.dim, MODE));
-  const cudaError_t e = launch_pdl(k_group, dim3(w.buckets), kThreads, s, a.ids, (uint32_t)a.tokens,
-                                   a.vocab, w);
-  if (e != cudaSuccess) return e;
-  const uint64_t chunks = (uint64_t)a.vocab * w.slices;
-  const uint64_t warps = (uint64_t)w.tiles * w.slices + (a.in_place ? 0 : (chunks + kFree - 1) / kFree);
-  if (warps == 0) return cudaSuccess;
-  return launch_pdl(k_sum<DT, OT, MODE>, dim3((unsigned)((warps + kBlock / 32 - 1) / (kBlock / 32))),
-                    kBlock, s, a, w, fastdiv_make(w.slices, std::max(warps, chunks)));
+  cudaError_t e = launch_pdl(k_group, dim3(w.buckets), kThreads, s, a.ids, (uint32_t)a.tokens, a.vocab, w);
+  const uint64_t warps = (uint64_t)w.tiles * w.slices, chunks = (uint64_t)a.vocab * w.slices;
+  const FastDiv slices = fastdiv_make(w.slices, std::max(warps + kBlock / 32, chunks));
+  if (e == cudaSuccess && warps)
+    e = launch_pdl(k_sum<DT, OT, MODE>, dim3((unsigned)((warps + kBlock / 32 - 1) / (kBlock / 32))), kBlock,
+                   s, a, w, slices);
+  if (e != cudaSuccess || a.in_place) return e;
+  const uint64_t blocks = (chunks + kFree * (kBlock / 32) - 1) / (kFree * (kBlock / 32));
+  return launch_pdl(k_free<OT, MODE>, dim3((unsigned)std::min(blocks, (uint64_t)1 << 30)), kBlock, s, a, w,
+                    slices, warps != 0);
 }
 
 template <int DT, int OT>

@@ -14,11 +14,7 @@ namespace cr {
 
 namespace {
 
-#ifndef CR_LB_AHEAD
-#define CR_LB_AHEAD 2
-#define CR_LB_OCC 5
-#endif
-constexpr int kAhead = CR_LB_AHEAD;  // chunks of a warp in flight
+constexpr int kAhead = 2;  // chunks of a warp in flight
 
 // An lse at or below this has no token left: nothing of the row's logits is known better than that.
 constexpr float kNoToken = -1.2676506e30f;  // -2^100
@@ -58,7 +54,7 @@ __device__ __forceinline__ float gradient(float x, float scale, const RowTerms& 
 
 // A warp takes kAhead chunks of a row, next to each other, so that the row's numbers are read once.
 template <int DT, int MODE, bool ENT>
-__global__ void __launch_bounds__(kBlock, CR_LB_OCC) k_logp_back(const __grid_constant__ LogProbBackArgs a,
+__global__ void __launch_bounds__(kBlock, 5) k_logp_back(const __grid_constant__ LogProbBackArgs a,
                                                       const __grid_constant__ ChunkRange r) {
   constexpr int vals = place_vals(MODE);
   constexpr uint32_t cols = place_cols(MODE);
