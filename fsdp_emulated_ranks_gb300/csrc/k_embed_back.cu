@@ -113,9 +113,33 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t n, uint32_t* s, uint32_t
   return before + sum - n;
 }
 
+// dout as bytes, for the blocks of k_group beyond the buckets: they ask for its rows while the others
+// sort, so that k_sum finds them in L2.
+struct Ahead {
+  const char* p;
+  uint64_t pitch;
+  uint32_t width;
+};
+constexpr uint32_t kAheadBlocks = 32;
+// Where dout is less, its rows arrive in time anyway; where it is more, it would not stay in L2.
+constexpr uint64_t kAheadLeast = 4 << 20, kAheadMost = 64 << 20;
+
+// A warp a token's row, 128 bytes a lane.
+__device__ __forceinline__ void bring(const Ids& ids, uint32_t tokens, uint32_t vocab, const Ahead& dout,
+                                      uint32_t block) {
+  constexpr uint32_t warps = kThreads / 32;
+  for (uint64_t k = (uint64_t)block * warps + threadIdx.x / 32; k < tokens; k += kAheadBlocks * warps) {
+    if (token_id(ids, k, vocab) < 0) continue;
+    const char* row = dout.p + k * dout.pitch;
+    for (uint32_t at = (threadIdx.x & 31) * 128; at < dout.width; at += 32 * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
+  }
+}
+
 __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids ids, uint32_t tokens,
                                                     uint32_t vocab,
-                                                    const __grid_constant__ Sorted w) {
+                                                    const __grid_constant__ Sorted w,
+                                                    const __grid_constant__ Ahead dout) {
   __shared__ uint32_t next[kLocals];  // counts, then where an id's next token goes
   __shared__ uint32_t list[kStep];    // a step's tokens of this bucket, in order: id in the bucket, place in the step
   __shared__ uint32_t scan[32];
@@ -125,6 +149,7 @@ __global__ void __launch_bounds__(kThreads) k_group(const __grid_constant__ Ids 
   __shared__ uint32_t in_step;
   pdl_enter();
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t / 32, b = blockIdx.x;
+  if (b >= w.buckets) return bring(ids, tokens, vocab, dout, b - w.buckets);
   const uint32_t mask = w.buckets - 1;
   for (uint32_t k = t; k < kLocals; k += kThreads) next[k] = 0;
   if (t == 0) earlier_all = valid_all = 0;
@@ -420,7 +445,12 @@ template <int DT, int OT, int MODE>
 cudaError_t run(const EmbedBackArgs& a, void* workspace, cudaStream_t s) {
   Sorted w;
   layout(&w, workspace, a.tokens, a.vocab, a.dim, place_chunks(a.dim, MODE));
-  cudaError_t e = launch_pdl(k_group, dim3(w.buckets), kThreads, s, a.ids, (uint32_t)a.tokens, a.vocab, w);
+  constexpr uint64_t es = DT == CR_BF16 ? 2 : 4;
+  const Ahead dout = {static_cast<const char*>(a.dout.p), a.dout.ld * es, (uint32_t)(a.dim * es)};
+  const uint64_t bytes = a.tokens * a.dim * es;
+  const bool ahead = bytes >= kAheadLeast && bytes <= kAheadMost;
+  cudaError_t e = launch_pdl(k_group, dim3(w.buckets + (ahead ? kAheadBlocks : 0)), kThreads, s, a.ids,
+                             (uint32_t)a.tokens, a.vocab, w, dout);
   const uint64_t warps = (uint64_t)w.tiles * w.slices, chunks = (uint64_t)a.vocab * w.slices;
   const FastDiv slices = fastdiv_make(w.slices, std::max(warps + kBlock / 32, chunks));
   if (e == cudaSuccess && warps)

@@ -486,7 +486,9 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
     run.add<true>(two(x, y), two(-r, -r), two(c, c));
   }
   Stat all = lanes_merge<32>(run.stat(), c);
-  if constexpr (TOP) note();
+  if constexpr (TOP) {
+    if (steps & (steps - 1)) note();  // else the last step did
+  }
   if constexpr (TEAM > 32) {
     if (t % 32 == 0) stats[t / 32] = all;
     __syncthreads();
@@ -647,11 +649,12 @@ cudaError_t run(const LogProbArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (a.vocab <= 2048)
     return launch_pdl(k_logp_warp<DT, TOP>, dim3(flat_grid(a.rows * 32)), kBlock, s, a);
-  // Parts of a row: while rows are too few to fill the SMs, and parts keep two vectors a
-  // thread (and more columns than are wanted of them).
+  // Parts of a row: while rows are too few to give each SM two, and parts keep a step of loads a
+  // thread (200 x 32000 bf16: 5.6 us so, 10.5 with parts of a quarter step; 400 rows: 7.6 so, 10.4 with parts up to four
+  // an SM).
   uint32_t parts = 1;
-  while (parts < kMostParts && a.rows * parts < 4 * (uint64_t)sms &&
-         a.vocab / (2 * parts) >= 2 * kBlock * RowPart<DT>::kVec)
+  while (parts < kMostParts && a.rows * parts < 2 * (uint64_t)sms &&
+         a.vocab / (2 * parts) >= kUnroll * kBlock * RowPart<DT>::kVec)
     parts *= 2;
   // Many short rows: fewer threads each, so that a row's end costs less of it (8192 x 32000 bf16 81.0 us
   // with 128 threads, 87.8 with 256; 1531 x 50257 fp32, top 8, 67.8 and 62.4: rows of 200 KB, of which more

@@ -167,7 +167,8 @@ def test_workspace_sizes():
     size = cr.cr_embedding_backward_workspace_bytes
     assert size(10, 0, 5) == size(10, 5, 0) == size(10, (1 << 21) + 1, 5) == size(1 << 31, 5, 5) == 0
     for t, v, d in ((0, 1, 1), (1, 1, 1), (8192, 32000, 2048), (65536, 131072, 4096), (1000, 1 << 21, 8)):
-        assert 0 < size(t, v, d) <= 64 * t + 8 * v + t * (d + 519) // 4 + 4096 * 8 + 2 * (t // 1024 + 1) * 8193
+        parts = 2 * (t // 16 + 1)  # at most: two for every 16 tokens, an fp32 row and two counters a chunk each
+        assert 8 * (t + v) < size(t, v, d) <= 8 * (t + v) + parts * (4 * (d + 519) + 8 * ((d + 7) // 256 + 1)) + 1024
 
 
 def test_random_numbers_of_the_references_agree():
