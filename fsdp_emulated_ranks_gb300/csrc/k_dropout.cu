@@ -5,6 +5,9 @@
 // from shifted granules where bf16 rows are off the vector grid (span.cuh); and for fp32
 // there, column by column, with the random numbers handed over in shared memory.  The
 // mask exists in registers only.
+//
+// Measured: 8192 x 2048 bf16 with a residual (101 MB) 16.3 us a call in a loop, 6.2 TB/s; without one
+// 15.2, bound by instructions (the generator's products among them); 1777 x 4099 fp32 10.8, 5.4 TB/s.
 #include <type_traits>
 
 #include "lm_internal.cuh"

@@ -2,8 +2,12 @@
 //
 // A gather: bound by memory (each distinct row of the table read once, every output
 // written once).  A warp copies a chunk of a row (ffn_internal.cuh; rows off the vector
-// grid in spans, span.cuh), two chunks in flight, since each begins with two dependent
-// loads, the id and the row.
+// grid in spans, span.cuh): two next to each other, which share the id, since a row's load
+// waits for the id's.
+//
+// Measured: 8192 x 2048 bf16 of 32000 rows (47 MB) 9.3 us a call in a loop, 5.1 TB/s, with the start and
+// end of a short launch in it (one chunk a warp 10.3, four 9.2 but idle for narrow rows); 8192 x
+// 2047, in spans, 15.1.
 #include <type_traits>
 
 #include "lm_internal.cuh"

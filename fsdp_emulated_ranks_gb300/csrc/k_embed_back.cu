@@ -16,6 +16,10 @@
 //               dout.
 // Reading the ids once for each bucket costs little: they stay in L2, and are 8 bytes to a row of dout's
 // thousands.  Bound by memory: dout is read and the table written once.
+//
+// Measured, 8192 x 2048 bf16 into 32000 rows (165 MB): 36.6 us a call in a loop, 4.5 TB/s; 27.4 with no
+// token at all, of which 8 are the sort and the launches' starts.  With k_free's work at the end of k_sum's launch
+// (80 registers a thread for stores) 43.
 #include <algorithm>
 
 #include "lm_internal.cuh"

