@@ -1014,7 +1014,7 @@ def prepare(wrapper, *args, **kwargs) -> Prepared:
     invocation, so advancing cfg.step between invocations takes effect.
     The prepared call holds references to the arguments, so the tensors and
     the bucket plan it addresses stay allocated while it exists.  Of the
-    feed-forward calls it also holds every tensor, and a copy of every 8-bit
+    feed-forward and language model calls it also holds every tensor, and a copy of every 8-bit
     matrix (Q8), that a recorded function made or looked up by itself."""
     global _recording
     if getattr(_tls, "recorder", None) is not None:

@@ -50,8 +50,8 @@ cr_status cr_embedding(const void* table, size_t ldt, size_t vocab,
  *           that no token names are then neither read nor written, which
  *           makes a small batch's call cheap.
  *   dtable  vocab x dim of dt_dtype, every row written (but see base)
- * A row's sum is fp32 and its order depends on the ids alone: tokens in
- * order, and where more than 64 name the row, sums of consecutive parts of them.
+ * A row's sum is fp32 and its order depends on the ids alone: the row's tokens in
+ * order, or sums of consecutive parts of them.
  * vocab is at most 2^21 (CR_ERR_UNSUPPORTED).
  *   workspace  cr_embedding_backward_workspace_bytes(tokens, vocab, dim)
  *              bytes, 16-byte aligned; contents mean nothing before and after
