@@ -11,17 +11,18 @@
 //
 // Most likely tokens.  Of its lanes' largest logits so far, which the sums need anyway, each warp notes
 // the share-th largest.  Where `need` warps' notes are at or above a value, and share * need is at least the
-// wanted number, so are as many logits: one below that value is not wanted.  The vectors of a step
-// of a thread whose largest may be wanted go to a list, few, and are read again at the end (from L2): what
-// is at or above the last such value is ranked by counting.  (Testing every logit on the way instead took
+// wanted number, so are as many logits: one below that value is not wanted.  Vectors whose
+// largest may be wanted go to a list, few, and are read again at the end (from L2): what is at or
+// above the last such value is ranked by counting.  (Testing every logit on the way instead took
 // 283 us for 8192 x 32000 against 81 without: that much code runs out of the instruction cache.)  Where a
 // list overflows (equal logits: a masked row, a row of zeros) or NaN leaves it short, the row is
 // looked at again with a bound over (logit, column) pairs, which are all different.
 //
 // A row is read by a warp, by a block, or by a cluster of blocks where rows are few.
 //
-// Measured, a call in a loop: 8192 x 32000 bf16 (525 MB) 81 us, 6.5 TB/s, top 8 111; 6124 x 50304 fp32
-// (1.23 GB) 176, 7.0 TB/s, top 8 226; 1 x 32000 5.2, top 20 7.8.
+// Measured, a call in a loop: 8192 x 32000 bf16 (525 MB) 81 us, 6.5 TB/s, top 8 115, top 32 147;
+// 6124 x 50304 fp32 (1.23 GB) 176, 7.0 TB/s, top 8 215; 1 x 32000 5.2, top 20 8.2.  (With a step of a thread
+// listed in place of a vector: 111, 174, 226, 7.9.)
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -274,8 +275,8 @@ struct TopShared {
   uint64_t best[CR_MAX_TOP];
   uint64_t bound;
   alignas(16) float notes[TEAM / 32];
-  uint32_t count, threads, steps;
-  uint32_t step[kCands];  // TEAM * the step + the thread
+  uint32_t count, threads, listed;
+  uint32_t vector[kCands];
   uint16_t thread[TEAM];
 
   __device__ __forceinline__ void push(uint64_t pair) {
@@ -467,7 +468,7 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
       if ((b & (b + 1)) == 0) {
         note();
         if (b == 0) {
-          if (t == 0) sh->count = sh->threads = sh->steps = 0;
+          if (t == 0) sh->count = sh->threads = sh->listed = 0;
           team_sync<TEAM>();
         } else {
           __syncwarp();
@@ -475,8 +476,14 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
         least = least_wanted(*sh, need);
       }
       if (most >= least) {
-        const uint32_t slot = atomicAdd(&sh->steps, 1u);
-        if (slot < TopShared<TEAM>::kCands) sh->step[slot] = b * TEAM + t;
+        uint32_t some = 0;  // bit i: vector i has one that may be wanted
+#pragma unroll
+        for (int i = 0; i < unroll; ++i) {
+          const uint4 one[1] = {v[i]};
+          some |= (largest<DT>(one) >= least ? 1u : 0u) << i;
+        }
+        for (uint32_t at = atomicAdd(&sh->listed, (uint32_t)__popc(some)); some; some &= some - 1, ++at)
+          if (at < TopShared<TEAM>::kCands) sh->vector[at] = (uint32_t)j + (__ffs(some) - 1) * TEAM;
       }
     }
   }
@@ -503,18 +510,17 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
     least = least_wanted(*sh, need);
     if (single && x >= least) sh->push(pair_key(x, row.begin + t));
     if (behind && y >= least) sh->push(pair_key(y, row.begin + col));
-    const uint32_t n = min(sh->steps, (uint32_t)TopShared<TEAM>::kCands);
-    if (t == 0 && sh->steps > n) sh->count = TopShared<TEAM>::kCands + 1;
-    for (uint32_t i = t; i < n * unroll; i += TEAM) {
-      const uint32_t at = sh->step[i / unroll];
-      const uint64_t vec = at / TEAM * step + at % TEAM + i % unroll * TEAM;
-      if (vec >= row.vectors) continue;
-      const uint4 one[1] = {row.vec((uint32_t)vec)};
+    const uint32_t n = min(sh->listed, (uint32_t)TopShared<TEAM>::kCands);
+    if (t == 0 && sh->listed > n) sh->count = TopShared<TEAM>::kCands + 1;
+    for (uint32_t i = t; i < n; i += TEAM) {
+      const uint32_t vec = sh->vector[i];
+      if (vec >= row.vectors) continue;  // past the end: -infinity, where all may be wanted
+      const uint4 one[1] = {row.vec(vec)};
       if (!(largest<DT>(one) >= least)) continue;
 #pragma unroll
       for (int e = 0; e < Part::kVec; ++e) {
         const float z = Part::value(one[0], e);
-        if (z >= least) sh->push(pair_key(z, row.begin + row.head + (uint32_t)vec * Part::kVec + e));
+        if (z >= least) sh->push(pair_key(z, row.begin + row.head + vec * Part::kVec + e));
       }
     }
     team_sync<TEAM>();
