@@ -268,7 +268,7 @@ struct Running {
 // What the threads of a team (a warp, or a block) share for the most likely tokens.
 template <int TEAM>
 struct TopShared {
-  static constexpr int kGroups = TEAM == 32 ? 32 : 64;
+  static constexpr int kGroups = 64;
   static constexpr int kCands = TEAM == 32 ? 512 : 1024;
   alignas(16) uint64_t keys[kGroups];
   alignas(16) uint64_t cand[kCands];
@@ -322,22 +322,34 @@ __device__ __forceinline__ float least_wanted(const TopShared<TEAM>& sh, int nee
   return __shfl_sync(~0u, mine, __ffs(__ballot_sync(~0u, rank == need - 1)) - 1);
 }
 
-// sh.bound = the k-th largest of the groups' largest pairs; no candidates yet.
+// sh.bound = the k-th largest of the groups' largest pairs; no candidates yet.  Groups are neighbouring
+// threads, or halves of a lane's columns: `key` and `other` are the thread's largest pairs of two
+// halves.
 template <int TEAM>
-__device__ __forceinline__ void find_bound(TopShared<TEAM>& sh, uint64_t key, int k, int t) {
-  constexpr int groups = TopShared<TEAM>::kGroups, per = TEAM / groups;
-#pragma unroll
-  for (int o = 1; o < per; o <<= 1) {
-    const uint64_t other = __shfl_xor_sync(~0u, key, o);
+__device__ __forceinline__ void find_bound(TopShared<TEAM>& sh, uint64_t key, uint64_t other, int k, int t) {
+  constexpr int groups = TopShared<TEAM>::kGroups;
+  if constexpr (TEAM == 32) {
+    sh.keys[t] = key, sh.keys[t + 32] = other;
+  } else {
+    constexpr int per = TEAM / groups;
     key = other > key ? other : key;
+#pragma unroll
+    for (int o = 1; o < per; o <<= 1) {
+      const uint64_t near = __shfl_xor_sync(~0u, key, o);
+      key = near > key ? near : key;
+    }
+    if (t % per == 0) sh.keys[t / per] = key;
   }
-  if (t % per == 0) sh.keys[t / per] = key;
   if (t == 0) sh.count = sh.threads = 0;
   team_sync<TEAM>();
-  if (t < groups) {
-    const uint64_t mine = sh.keys[t];
+  for (int g = t; g < groups; g += TEAM) {
+    const uint64_t mine = sh.keys[g];
     int rank = 0;
-    for (int i = 0; i < groups; ++i) rank += sh.keys[i] > mine || (sh.keys[i] == mine && i < t);
+#pragma unroll 4
+    for (int i = 0; i < groups; i += 2) {
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sh.keys + i);
+      rank += (v.x > mine || (v.x == mine && i < g)) + (v.y > mine || (v.y == mine && i + 1 < g));
+    }
     if (rank == k - 1) sh.bound = mine;
   }
   team_sync<TEAM>();
@@ -399,14 +411,15 @@ __device__ __forceinline__ void find_top(TopShared<TEAM>& sh, const RowPart<DT>&
                                          Put put) {
   constexpr uint32_t cands = TopShared<TEAM>::kCands;
   if (sh.count > cands || sh.count < k) {
-    uint64_t key = 0;
+    uint64_t key = 0, other = 0;
     row.each_of(t, TEAM, [&](uint32_t col, float x) {
       const uint64_t pair = pair_key(x, row.begin + col);
-      key = pair > key ? pair : key;
+      uint64_t& most = (col - row.head) / (TEAM * RowPart<DT>::kVec) % 2 ? other : key;
+      if (pair > most) most = pair;
     });
     team_sync<TEAM>();  // sh.count has been read
-    find_bound<TEAM>(sh, key, k, t);
-    collect<DT, TEAM>(sh, row, sh.bound, key, t);
+    find_bound<TEAM>(sh, key, other, k, t);
+    collect<DT, TEAM>(sh, row, sh.bound, other > key ? other : key, t);
   }
   const uint32_t n = sh.count;
   if (n <= cands) {
@@ -455,6 +468,10 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
     const float bound = warp_bound(run.m, share);
     if (t % 32 == 0) *const_cast<volatile float*>(&sh->notes[t / 32]) = bound;
   };
+  // A warp's own lanes bound a few wanted ones only: of 32 the smallest lane's largest logit would be
+  // the bound.  Without a list find_top looks again, at 64 groups (8192 x 2000 bf16, top 20: 25 us with the
+  // list, 51 without; top 28 35 and 55; top 32 89 and 58).
+  const bool lists = TEAM > 32 || k <= 28;
   // notes after 1, 2, 4, ... steps: all warps take as many
   const uint32_t steps = (uint32_t)max((uint64_t)1, (row.vectors + step - 1) / step);
   for (uint32_t b = 0; b < steps; ++b) {
@@ -466,16 +483,16 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
     const float most = run.take<DT>(v, c);
     if constexpr (TOP) {
       if ((b & (b + 1)) == 0) {
-        note();
+        if (lists) note();
         if (b == 0) {
           if (t == 0) sh->count = sh->threads = sh->listed = 0;
           team_sync<TEAM>();
         } else {
           __syncwarp();
         }
-        least = least_wanted(*sh, need);
+        if (lists) least = least_wanted(*sh, need);
       }
-      if (most >= least) {
+      if (lists && most >= least) {
         uint32_t some = 0;  // bit i: vector i has one that may be wanted
 #pragma unroll
         for (int i = 0; i < unroll; ++i) {
@@ -497,7 +514,7 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
   }
   Stat all = lanes_merge<32>(run.stat(), c);
   if constexpr (TOP) {
-    if (steps & (steps - 1)) note();  // else the last step did
+    if (lists && steps & (steps - 1)) note();  // else the last step did
   }
   if constexpr (TEAM > 32) {
     if (t % 32 == 0) stats[t / 32] = all;
@@ -506,7 +523,7 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
   } else if constexpr (TOP) {
     __syncwarp();
   }
-  if constexpr (TOP) {
+  if (TOP && lists) {
     least = least_wanted(*sh, need);
     if (single && x >= least) sh->push(pair_key(x, row.begin + t));
     if (behind && y >= least) sh->push(pair_key(y, row.begin + col));
