@@ -269,7 +269,7 @@ struct Running {
 template <int TEAM>
 struct TopShared {
   static constexpr int kGroups = 64;
-  static constexpr int kCands = TEAM == 32 ? 512 : 1024;
+  static constexpr int kCands = TEAM == 32 ? 384 : 1024;  // eight warps' stay below 48 KB
   alignas(16) uint64_t keys[kGroups];
   alignas(16) uint64_t cand[kCands];
   uint64_t best[CR_MAX_TOP];
@@ -469,8 +469,8 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
     if (t % 32 == 0) *const_cast<volatile float*>(&sh->notes[t / 32]) = bound;
   };
   // A warp's own lanes bound a few wanted ones only: of 32 the smallest lane's largest logit would be
-  // the bound.  Without a list find_top looks again, at 64 groups (8192 x 2000 bf16, top 20: 25 us with the
-  // list, 51 without; top 28 35 and 55; top 32 89 and 58).
+  // the bound.  Without a list find_top looks again, at 64 groups (8192 x 2000 bf16, top 20: 21 us with the
+  // list, 51 without; top 32 89 and 58; top 28 31 with it).
   const bool lists = TEAM > 32 || k <= 28;
   // notes after 1, 2, 4, ... steps: all warps take as many
   const uint32_t steps = (uint32_t)max((uint64_t)1, (row.vectors + step - 1) / step);
@@ -512,14 +512,14 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
     const float r = run.reference();
     run.add<true>(two(x, y), two(-r, -r), two(c, c));
   }
-  Stat all = lanes_merge<32>(run.stat(), c);
+  Stat sums = lanes_merge<32>(run.stat(), c);
   if constexpr (TOP) {
     if (lists && steps & (steps - 1)) note();  // else the last step did
   }
   if constexpr (TEAM > 32) {
-    if (t % 32 == 0) stats[t / 32] = all;
+    if (t % 32 == 0) stats[t / 32] = sums;
     __syncthreads();
-    all = lanes_merge<warps>(stats[t % warps], c);
+    sums = lanes_merge<warps>(stats[t % warps], c);
   } else if constexpr (TOP) {
     __syncwarp();
   }
@@ -527,8 +527,9 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
     least = least_wanted(*sh, need);
     if (single && x >= least) sh->push(pair_key(x, row.begin + t));
     if (behind && y >= least) sh->push(pair_key(y, row.begin + col));
-    const uint32_t n = min(sh->listed, (uint32_t)TopShared<TEAM>::kCands);
-    if (t == 0 && sh->listed > n) sh->count = TopShared<TEAM>::kCands + 1;
+    const bool all = sh->listed <= TopShared<TEAM>::kCands;
+    const uint32_t n = all ? sh->listed : 0;
+    if (t == 0 && !all) sh->count = TopShared<TEAM>::kCands + 1;
     for (uint32_t i = t; i < n; i += TEAM) {
       const uint32_t vec = sh->vector[i];
       if (vec >= row.vectors) continue;  // past the end: -infinity, where all may be wanted
@@ -542,7 +543,7 @@ __device__ __forceinline__ Stat read_part(const RowPart<DT>& row, float c, int k
     }
     team_sync<TEAM>();
   }
-  return all;
+  return sums;
 }
 
 template <int DT>
