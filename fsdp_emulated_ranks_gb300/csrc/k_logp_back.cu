@@ -55,7 +55,8 @@ __device__ __forceinline__ RowTerms row_terms(const LogProbBackArgs& a, uint64_t
   }
   r.by *= a.scale, r.ent *= a.scale, r.hit = a.scale * dlogp;
   if (r.lse <= kNoToken) {
-    r.lse = __builtin_huge_valf();  // p = 0
+    r.lse = __builtin_huge_valf();  // p = 0, of factors that may not be finite (a z-loss's dlse is -infinity there)
+    r.by = r.ent = r.hit = 0.0f;
     r.target = -1;
   }
   return r;

@@ -132,7 +132,7 @@ cr_status cr_log_probs(const void* logits, size_t ldl, const void* targets,
  *                          + p_v (dlse - dlogp - dentropy (log(p_v) + entropy)))
  * with p_v = exp(z_v - lse).  dlogp counts as 0 where the target is no token, and p_v = 0
  * (also: below 2^-126) gives 0.  A row whose lse is -2^100 or less (every token ruled out, by -infinity or by the
- * type's lowest value) gets zeros.  A row whose lse is otherwise 256 or more in magnitude (filled with a finite mask
+ * type's lowest value) gets zeros, be dlogp, dentropy and dlse finite there or not.  A row whose lse is otherwise 256 or more in magnitude (filled with a finite mask
  * value, say) goes by its own maximum and sum: rounded to fp32, such an lse leaves too little of z_v - lse.
  *   lse, entropy   as cr_log_probs wrote them of these logits (entropy may be NULL without
  *                  dentropy)

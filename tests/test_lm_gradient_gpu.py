@@ -101,3 +101,33 @@ def test_rows_of_a_large_lse_in_a_graph():
         torch.cuda.synchronize()
         want, bound = G.gradient(x, targets, 1.0, d, d, None)
         R.assert_close(dx, want, bound, "f32", f"shift {shift}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [40, 1001, 5003])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_rows_without_tokens_get_zeros(bad, vocab, dt):
+    """Whatever the gradients of their numbers: a z-loss gives such a row dlse = 2 c lse = -infinity, a ratio of
+    its probabilities dlogp = NaN."""
+    g = T.gen(vocab)
+    rows = 6
+    logits = T.normal(g, rows, vocab, dt=dt)
+    logits[1], logits[4] = -math.inf, torch.finfo(TORCH[dt]).min
+    targets = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    _, ent, lse, _, _ = T.forward(logits, targets, dt, 1.0)
+    d, e, q = (T.normal(g, rows) for _ in range(3))
+    want, bound = G.gradient(logits, targets, 1.0, d, e, q)
+    for which in ((0,), (1,), (2,), (0, 1, 2)):
+        terms = [t.clone() for t in (d, e, q)]
+        for k in which:
+            terms[k][1] = terms[k][4] = bad
+        out = torch.full_like(logits, math.nan)
+        cr.cr_log_probs_backward(logits, targets, rows, vocab, dt, 1.0, lse, ent, *terms, out)
+        assert bool((out[1] == 0).all()) and bool((out[4] == 0).all()), f"{which} {bad}"
+        R.assert_close(out, want, bound, dt, "dlogits")
+    dlse = 2e-4 * lse
+    out = torch.full_like(logits, math.nan)
+    cr.cr_log_probs_backward(logits, targets, rows, vocab, dt, 1.0, lse, None, d, None, dlse, out)
+    dlse = torch.where(torch.isinf(dlse), torch.zeros_like(dlse), dlse)
+    want, bound = G.gradient(logits, targets, 1.0, d, None, dlse)
+    R.assert_close(out, want, bound, dt, "z-loss")
