@@ -62,11 +62,15 @@ __device__ __forceinline__ RowTerms row_terms(const LogProbBackArgs& a, uint64_t
   return r;
 }
 
+// exp of this and of all below is 0 (2^-126 is exp(-87.3)), and so has to be its product with log(p), which
+// stays finite from here up.
+constexpr float kLeastLog = -100.0f;
+
 template <bool ENT>
 __device__ __forceinline__ float gradient(float x, float scale, const RowTerms& r) {
   const float log_p = fmaf(x, scale, -r.lse), p = fast_exp2(log_p * kLog2E);
   if constexpr (!ENT) return p * r.by;
-  return p * fmaf(-r.ent, fmaxf(log_p, -1e30f), r.by);  // 0 times -infinity is 0 here
+  return p * fmaf(-r.ent, fmaxf(log_p, kLeastLog), r.by);
 }
 
 // The column of a lane's value 0; value i's is i further, or 32 i where lanes have single values.

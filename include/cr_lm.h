@@ -130,10 +130,13 @@ cr_status cr_log_probs(const void* logits, size_t ldl, const void* targets,
 /* The gradient of  sum over the rows of dlogp logp + dentropy entropy + dlse lse:
  *     dlogits_v = scale * (dlogp [v = target]
  *                          + p_v (dlse - dlogp - dentropy (log(p_v) + entropy)))
- * with p_v = exp(z_v - lse).  dlogp counts as 0 where the target is no token, and p_v = 0
- * (also: below 2^-126) gives 0.  A row whose lse is -2^100 or less (every token ruled out, by -infinity or by the
- * type's lowest value) gets zeros, be dlogp, dentropy and dlse finite there or not.  A row whose lse is otherwise 256 or more in magnitude (filled with a finite mask
- * value, say) goes by its own maximum and sum: rounded to fp32, such an lse leaves too little of z_v - lse.
+ * with p_v = exp(z_v - lse).  dlogp counts as 0 where the target is no token.
+ *  - p_v = 0 (also: below 2^-126) gives 0 where the row's dlogp, dlse and 100 dentropy are finite in fp32,
+ *    scaled or not.
+ *  - A row whose lse is -2^100 or less (every token ruled out, by -infinity or by the type's
+ *    lowest value) gets zeros, be dlogp, dentropy and dlse finite there or not.
+ *  - A row whose lse is otherwise 256 or more in magnitude (filled with a finite mask value, say) goes by its own
+ *    maximum and sum: rounded to fp32, such an lse leaves too little of z_v - lse.
  *   lse, entropy   as cr_log_probs wrote them of these logits (entropy may be NULL without
  *                  dentropy)
  *   targets        rows ids (may be NULL without dlogp)

@@ -131,3 +131,23 @@ def test_rows_without_tokens_get_zeros(bad, vocab, dt):
     dlse = torch.where(torch.isinf(dlse), torch.zeros_like(dlse), dlse)
     want, bound = G.gradient(logits, targets, 1.0, d, None, dlse)
     R.assert_close(out, want, bound, dt, "z-loss")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [40, 1001, 5003])
+def test_ruled_out_tokens_get_zeros(vocab, dt):
+    """Also where the entropy's gradient is large: 0 log(0) is 0 times any finite number."""
+    g = T.gen(vocab)
+    rows = 6
+    logits = T.normal(g, rows, vocab, dt=dt)
+    logits[:, ::3] = -math.inf
+    logits[2:4] += 1e4  # a large lse
+    targets = 1 + 3 * torch.randint(0, vocab // 3, (rows,), generator=g, device=DEV)
+    _, ent, lse, _, _ = T.forward(logits, targets, dt, 1.0)
+    d, q = T.normal(g, rows), T.normal(g, rows)
+    e = torch.tensor([1.0, 1e9, -1e10, 1e20, -1e30, 1e35], device=DEV)
+    out = torch.full_like(logits, math.nan)
+    cr.cr_log_probs_backward(logits, targets, rows, vocab, dt, 1.0, lse, ent, d, e, q, out)
+    assert bool((out[:, ::3] == 0).all())
+    want, bound = G.gradient(logits, targets, 1.0, d, e, q)
+    R.assert_close(out, want, bound, dt, "dlogits")
