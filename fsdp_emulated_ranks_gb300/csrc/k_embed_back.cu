@@ -392,14 +392,21 @@ __global__ void __launch_bounds__(kBlock, 2) k_sum(const __grid_constant__ Embed
 
 constexpr uint32_t kFree = 16;  // chunks of the table that a warp looks at at a time
 
-// base, or zeros.  chained: launched after k_sum, whose blocks have all started, so that k_group has
-// ended; it is k_sum that one block waits for at its end, so that this launch ends after it (pdl.cuh).
+// base, or zeros.  chained: launched after k_sum, and started when each of its blocks has returned from its
+// wait for k_group (pdl.cuh): k_group, and with it all that came before this call, has ended, and what they
+// wrote is in L2.  Without a wait of this launch's own nothing says that L1 holds no older lines of it (a workspace
+// is used by call after call): rows are read by way of L2, and a fence comes before loads of base (where there
+// is none it would cost 0.9 of the 36.6 us above).  It is k_sum that one block waits for at its end, so that this
+// launch ends after it.
 template <int OT, int MODE>
 __global__ void __launch_bounds__(kBlock) k_free(const __grid_constant__ EmbedBackArgs a,
                                                  const __grid_constant__ Sorted w,
                                                  const __grid_constant__ FastDiv slices, bool chained) {
   constexpr int vals = place_vals(MODE), ahead = 4;  // of a warp in flight
-  if (!chained) pdl_wait_prerequisites();
+  if (!chained)
+    pdl_wait_prerequisites();
+  else if (a.base.p)
+    __threadfence();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const uint64_t all = (uint64_t)a.vocab * w.slices, stride = (uint64_t)gridDim.x * (kBlock / 32) * kFree;
@@ -412,7 +419,7 @@ __global__ void __launch_bounds__(kBlock) k_free(const __grid_constant__ EmbedBa
     if (lane < kFree && mine < all) {
       id = (uint32_t)fastdiv_div(slices, mine);
       slice = (uint32_t)(mine - (uint64_t)id * w.slices);
-      is_free = w.rows[id].y == 0;
+      is_free = __ldcg(&w.rows[id].y) == 0;
     }
     uint32_t left = __ballot_sync(~0u, is_free);
     while (left) {
