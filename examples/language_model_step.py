@@ -59,7 +59,7 @@ class Rank:
         q8 = lambda cols: cr.Q8(torch.empty(tokens, cols, dtype=torch.uint8, device="cuda"),
                                 torch.empty(tokens, -(-cols // cr.Q8_GROUP), device="cuda"))
         self.y8, self.gate8, self.up8 = q8(dim), q8(ffn), q8(ffn)
-        # dropout's seed, and an offset that moves once a step
+        # dropout's seed, and an offset that moves by a step's dropout calls: one
         self.rng = torch.tensor([seed, 0], dtype=torch.int64, device="cuda")
         need = max(cr.cr_glu_workspace_bytes(tokens, dim, ffn), cr.cr_glu_backward_workspace_bytes(tokens, dim, ffn),
                    cr.cr_rms_norm_backward_workspace_bytes(tokens, dim),

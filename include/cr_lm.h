@@ -84,7 +84,9 @@ cr_status cr_embedding_backward(const void* dout, size_t lddo, cr_dtype dtype,
  *              which `call` is added (modulo 2^64).  They are read when the
  *              call runs, so a captured step gets new masks where the step (or
  *              the loop between replays) moves the offset.
- *   call       tells the calls of a step apart: its number in the step
+ *   call       tells the calls of a step apart: its number in the step, from 0.  Since it is
+ *              added to the offset, a step of n calls has to move the offset by n or more: moved by one,
+ *              call 1 of a step would have the mask of call 0 of the next.
  *   first_row  the row counter of the matrix's first row: a slab of rows has
  *              the mask of its part of the whole.  first_row + rows is at
  *              most 2^32 (CR_ERR_INVALID_ARG).
