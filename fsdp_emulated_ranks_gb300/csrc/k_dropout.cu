@@ -8,8 +8,6 @@
 //
 // Measured: 8192 x 2048 bf16 with a residual (101 MB) 16.3 us a call in a loop, 6.2 TB/s; without one
 // 15.2, bound by instructions (the generator's products among them); 1777 x 4099 fp32 10.8, 5.4 TB/s.
-#include <type_traits>
-
 #include "lm_internal.cuh"
 #include "pdl.cuh"
 

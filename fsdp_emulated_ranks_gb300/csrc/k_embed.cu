@@ -8,8 +8,6 @@
 // Measured: 8192 x 2048 bf16 of 32000 rows (47 MB) 9.3 us a call in a loop, 5.1 TB/s, with the start and
 // end of a short launch in it (one chunk a warp 10.3, four 9.2 but idle for narrow rows); 8192 x
 // 2047, in spans, 15.1.
-#include <type_traits>
-
 #include "lm_internal.cuh"
 #include "pdl.cuh"
 

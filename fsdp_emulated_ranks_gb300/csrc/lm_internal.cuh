@@ -146,10 +146,6 @@ __device__ __forceinline__ void st_place(void* row, const Place<MODE>& p, const 
   }
 }
 
-// The mode of a call: single values where both types are not bf16, since spans
-// are bf16's.
-inline int place_mode(int vec, bool bf16) { return vec ? vec : bf16 ? kSpan : 0; }
-
 #endif  // __CUDACC__
 
 }  // namespace cr

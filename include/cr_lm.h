@@ -120,8 +120,9 @@ cr_status cr_dropout(const void* x, size_t ldx, const void* residual,
  *   top_ids, top_logp    rows x top packed, int32 and float: tokens in the order of
  *            falling logits, equal ones by rising id, NaN behind all others;
  *            and their log probabilities (each optional)
- * scale is rounded to fp32: > 0 and finite there, one over the temperature
- * (CR_ERR_INVALID_ARG).  vocab is below 2^31 - 65536 (CR_ERR_UNSUPPORTED). */
+ * scale is rounded to fp32: > 0 and at most 2^126 there, one over the temperature
+ * (CR_ERR_INVALID_ARG).  A product with it past fp32's end is infinite: in lse, and in logp where a token is that
+ * far below the largest.  vocab is below 2^31 - 65536 (CR_ERR_UNSUPPORTED). */
 #define CR_MAX_TOP 32
 cr_status cr_log_probs(const void* logits, size_t ldl, const void* targets,
                        int id_bits, size_t rows, size_t vocab, cr_dtype dtype,
