@@ -7,7 +7,9 @@
 // mask exists in registers only.
 //
 // Measured: 8192 x 2048 bf16 with a residual (101 MB) 16.3 us a call in a loop, 6.2 TB/s; without one
-// 15.2, bound by instructions (the generator's products among them); 1777 x 4099 fp32 10.8, 5.4 TB/s.
+// 15.2, bound by instructions: 160 for a lane's eight elements, of which the generator's ten rounds (two
+// products, two exclusive-ors, two key sums) are about 60 and the rest unpacks, compares, packs and starts a
+// warp for each 512 columns; 1777 x 4099 fp32 10.8, 5.4 TB/s.
 #include "lm_internal.cuh"
 #include "pdl.cuh"
 

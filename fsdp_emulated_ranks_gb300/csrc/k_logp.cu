@@ -20,8 +20,8 @@
 //
 // A row is read by a warp, by a block, or by a cluster of blocks where rows are few.
 //
-// Measured, a call in a loop: 8192 x 32000 bf16 (525 MB) 81 us, 6.5 TB/s, top 8 115, top 32 147;
-// 6124 x 50304 fp32 (1.23 GB) 176, 7.0 TB/s, top 8 215; 1 x 32000 5.2, top 20 8.2.  (With a step of a thread
+// Measured, a call in a loop: 8192 x 32000 bf16 (525 MB) 81 us, 6.5 TB/s, top 8 114, top 32 146;
+// 6124 x 50304 fp32 (1.23 GB) 179, 6.9 TB/s, top 8 215; 1 x 32000 5.7, top 20 8.5.  (With a step of a thread
 // listed in place of a vector: 111, 174, 226, 7.9.)
 #include <cooperative_groups.h>
 
@@ -683,9 +683,10 @@ cudaError_t run(const LogProbArgs& a, cudaStream_t s) {
   while (parts < kMostParts && a.rows * parts < 2 * (uint64_t)sms &&
          a.vocab / (2 * parts) >= kUnroll * kBlock * RowPart<DT>::kVec)
     parts *= 2;
-  // Many short rows: fewer threads each, so that a row's end costs less of it (8192 x 32000 bf16 81.0 us
-  // with 128 threads, 87.8 with 256; 1531 x 50257 fp32, top 8, 67.8 and 62.4: rows of 200 KB, of which more
-  // at a time do not fit in L2 until their second look).
+  // Many short rows: fewer threads each, so that a row's end costs less of it.  With 128 threads and with
+  // 256: 8192 x 32000 bf16 81.5 and 88.1 us, top 8 114 and 148; 4096 x 64000 (125 KB a row) 82.6 and 83.6, top 8
+  // 104 and 119; 4096 x 90000 (176 KB) 113 and 116, top 8 137 and 157; 1531 x 50257 fp32 (196 KB) 55.5
+  // and 52.1, top 8 64.1 and 63.0.  The limit is below where the two meet.
   constexpr uint64_t kShort = 128 << 10;
   if (a.rows >= 4 * (uint64_t)sms && a.vocab * (16 / RowPart<DT>::kVec) <= kShort)
     return run_block<DT, 128, TOP>(a, 1, s);

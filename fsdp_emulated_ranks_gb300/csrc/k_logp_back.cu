@@ -13,7 +13,7 @@
 // A block takes the whole row, so that dlogits may be logits there too.
 //
 // Measured: 8192 x 32000 bf16 (1.05 GB) 150 us a call in a loop, 7.0 TB/s; with the entropy's gradient
-// 158; 8192 x 31999, in spans, 197.  Two chunks a warp, which share the row's numbers, at five blocks an SM:
+// 159; 8192 x 31999, in spans, 198.  Two chunks a warp, which share the row's numbers, at five blocks an SM:
 // one chunk 183, four blocks 158.  One row in 32 of a large lse: 154; every row: 500.
 #include <algorithm>
 
